@@ -9,6 +9,14 @@
  * and, beside them, for prefill: msa_prefill_block_score, the fused
  * score-to-selection of a ragged batch of chunks per query block, and
  * attention_sdpa, dense (not paged) GQA attention with a causal flag.
+ * Around the caches, for one step of a serving loop:
+ *   paged_assign_slots               page-table rows grown from a free list;
+ *                                    every token's row, length and slot
+ *   paged_norm_rope_store            per-head RMS norm and rotary positions of
+ *                                    q and k; K and V written into the caches
+ *   paged_prefill_attention          a ragged batch of chunks of new tokens
+ *   paged_sparse_prefill_attention   over the caches: every key, or the blocks
+ *                                    msa_prefill_block_score selected
  *
  * Contract shared by every entry point ("Kernel ABI" -- Core rules; "Slot
  * contract" -- 1. The validator owns the boundary):
@@ -17,7 +25,9 @@
  *     returns and never synchronises the host with the device.
  *   - Each call writes every logical cell of every output, honouring the
  *     output's shape, dtype and strides (outputs need not be contiguous), and
- *     leaves every input unchanged.
+ *     leaves every input unchanged.  Tensors marked IN/OUT (a page table that
+ *     grows, a cache that is written into) are changed only in the cells that
+ *     the call names.
  *   - Work is enqueued on the supplied stream (NULL = the legacy default
  *     stream) and completes asynchronously; inputs must stay valid until it
  *     has run.  No device data is read on the host, so a call can be captured
@@ -328,6 +338,164 @@ SPD_API size_t spd_decode_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, in
                                   int32_t block_size);
 
 /*
+ * Slots of a serving step: the page table grown from a free list and every
+ * token's place, from the requests' lengths alone.
+ *
+ * Request b has prefix_lens[b] keys in the cache and brings new_lens[b]
+ * tokens (negative counts are 0) at positions prefix_lens[b] ..; its page
+ * table is row slot_ids[b].  With cap = NB * block_size,
+ *   cu_seqlens[b]     = min(sum of new_lens before b, T)     (T = rows of req_idx;
+ *                       tokens past T are left out of everything below)
+ *   n_b               = cu_seqlens[b+1] - cu_seqlens[b]
+ *   cu_seqblocks_q[b] = sum over requests before b of ceil(n / block_size_q)
+ *   seq_lens[b]       = prefix_lens[b] + n_b
+ *   grown_b           = ceil(min(seq_lens[b], cap) / block_size) -
+ *                       ceil(min(prefix_lens[b], cap) / block_size)
+ *                       (0 when slot_ids[b] is outside the table)
+ * The grown blocks of all requests, in request order, take the free pages
+ * from the end of the list: the i-th one becomes
+ * free_pages[free_count - 1 - i], written into block_table behind the
+ * request's cached blocks; blocks that find the list empty get -1 (which
+ * every call of this library excludes).  free_left = max(0, free_count -
+ * sum of grown_b) pages stay free: the caller passes it as the next step's
+ * free_count, and returns pages by appending them behind it.  For token i of
+ * request b, row t = cu_seqlens[b] + i:
+ *   req_idx[t] = slot_ids[b], token_lens[t] = prefix_lens[b] + i + 1 (the
+ *   seq_lens argument of the decode calls), slots[t] = page * block_size +
+ *   offset of position token_lens[t] - 1, or -1 where it has no page in
+ *   [0, n_pages).
+ * Rows behind the last token: req_idx -1, token_lens 0, slots -1.
+ *
+ * new_lens, prefix_lens, slot_ids [B] i32; rows named in slot_ids must be
+ *   distinct (a row named twice is written by both requests)
+ * free_pages [F] i32, free_count [1] i32 (clipped to [0, F])
+ * n_pages    pages of the pool, in [0, 2^31 / block_size)
+ * block_size must be 128; block_size_q >= 1
+ * block_table IN/OUT [R, NB] i32: only the grown blocks' cells are written
+ * cu_seqlens, cu_seqblocks_q OUT [B+1] i32, seq_lens OUT [B] i32
+ * req_idx, token_lens, slots OUT [T] i32, free_left OUT [1] i32
+ * Nothing but block_table is read and written, so a second call on the same
+ * inputs gives the same outputs.  Domain: B in [0, 8192], NB in [1, 1024],
+ * T < 2^30.
+ */
+SPD_API void paged_assign_slots(const spd_tensor *new_lens, const spd_tensor *prefix_lens,
+                                const spd_tensor *slot_ids, const spd_tensor *free_pages,
+                                const spd_tensor *free_count, int32_t n_pages, int32_t block_size,
+                                int32_t block_size_q, const spd_tensor *block_table, const spd_tensor *cu_seqlens,
+                                const spd_tensor *cu_seqblocks_q, const spd_tensor *seq_lens,
+                                const spd_tensor *req_idx, const spd_tensor *token_lens, const spd_tensor *slots,
+                                const spd_tensor *free_left, spd_stream_t stream);
+
+/*
+ * Per-head RMS norm and rotary positions of queries and keys, with K and V
+ * written into the paged caches, in one pass.  For every head row x of q
+ * (weight w = q_weight) and of k (w = k_weight) of token t, at position
+ * p = token_lens[t] - 1:
+ *   y   = x * w / sqrt(mean(x^2) + eps)       (no norm where the weight is NULL)
+ *   y'  = y with its first Rd dims rotated by the angles of row p of cos_sin:
+ *         pairs (i, i + Rd/2), or with interleaved nonzero (2i, 2i + 1), i < Rd/2:
+ *         y'_a = y_a cos - y_b sin,  y'_b = y_b cos + y_a sin
+ *   q_out[t]          = y' of q
+ *   k_cache[slots[t]] = y' of k / k_scale;  v_cache[slots[t]] = v[t] / v_scale
+ * in fp32 and rounded once (to nearest even; E4M3 saturates at +-448 and
+ * keeps NaN).  A token with token_lens outside [1, M] (padding) gets a zero
+ * q_out row and stores nothing; a slot outside the pool stores nothing.  The
+ * index queries and keys of the score calls go through the same call, with v
+ * and v_cache NULL.
+ *
+ * q          [T, Hq, D] f32 | bf16 | f16, k [T, Hkv, D] and v [T, Hkv, D] (or
+ *            NULL) of the same dtype, any strides
+ * q_weight, k_weight [D] f32 | bf16 | f16, or NULL
+ * cos_sin    [M, Rd] f32: the cosines of a position's Rd/2 angles, then the sines
+ * token_lens, slots [T] i32 (paged_assign_slots); slots that are stored to
+ *            must be distinct (of two tokens with one slot, each cell holds
+ *            either one's value)
+ * q_out      OUT [T, Hq, D] f32 | bf16 | f16
+ * k_cache, v_cache IN/OUT [P*block_size, Hkv, D] f32 | bf16 | f16 | e4m3, one
+ *            dtype for both; only the named slots are written; v_cache NULL
+ *            exactly when v is
+ * eps        finite and >= 0; k_scale, v_scale finite and > 0 with a finite
+ *            reciprocal (1.0 for a cache stored unscaled)
+ * block_size must be 128
+ * Domain: D in [1, 256], Rd even in [2, D], Hq, Hkv in [1, 65535], T < 2^30.
+ */
+SPD_API void paged_norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v,
+                                   const spd_tensor *q_weight, const spd_tensor *k_weight,
+                                   const spd_tensor *cos_sin, const spd_tensor *token_lens, const spd_tensor *slots,
+                                   const spd_tensor *q_out, const spd_tensor *k_cache, const spd_tensor *v_cache,
+                                   float eps, int32_t interleaved, int32_t block_size, float k_scale,
+                                   float v_scale, spd_stream_t stream);
+
+/*
+ * Paged prefill attention: GQA attention of a ragged batch of chunks of new
+ * tokens over the paged caches that already hold them.
+ *
+ * Sequence b owns query tokens cu_seqlens[b] .. cu_seqlens[b+1]-1, the first
+ * at key position prefix_lens[b]; its keys lie in row slot_ids[b] of
+ * block_table.  Token i of the chunk reads the keys
+ *   tau < L,  L = min(prefix_lens[b] + i + 1, seq_lens[b], NB * block_size)
+ * (none where slot_ids[b] is outside the table), blocks whose page lies
+ * outside the pool left out, and writes
+ *   out[t][g] = sum_tau softmax(z)_tau * v_scale * v_cache[slot(tau)][h]
+ *   z_tau = sm_scale * k_scale * (q[t][g] . k_cache[slot(tau)][h]),  h = g / (Hq / Hkv)
+ * A token that reads no key, and one that no sequence owns, writes zeros.
+ * Slots that a token does not read never reach its output, whatever they
+ * hold (NaN and infinities included).  Logits, softmax and accumulation are
+ * fp32; the output is rounded to bf16 (nearest even).
+ *
+ * q          [total_q, Hq, D] f32 | bf16 | f16
+ * k_cache, v_cache [P*128, Hkv, D] e4m3 | bf16, innermost stride 1
+ * block_table [R, NB] i32; slot_ids, seq_lens, prefix_lens [B] i32;
+ * cu_seqlens [B+1] i32, nondecreasing
+ * out        OUT [total_q, Hq, D] bf16
+ * workspace  device scratch of at least
+ *            spd_prefill_attention_workspace_bytes(total_q, Hq, Hkv, D, B,
+ *            NB, 0) bytes, 256-byte aligned, no initialisation needed, not
+ *            shared by calls that may run concurrently
+ * sm_scale, k_scale, v_scale finite; block_size must be 128
+ * Domain: D in [1, 256], Hq / Hkv <= 16, NB in [1, 1024], B <= 8192,
+ * total_q * Hq < 2^30.
+ */
+SPD_API void paged_prefill_attention(const spd_tensor *q, const spd_tensor *k_cache, const spd_tensor *v_cache,
+                                     const spd_tensor *block_table, const spd_tensor *slot_ids,
+                                     const spd_tensor *cu_seqlens, const spd_tensor *seq_lens,
+                                     const spd_tensor *prefix_lens, const spd_tensor *out, float sm_scale,
+                                     int32_t block_size, float k_scale, float v_scale, void *workspace,
+                                     size_t workspace_bytes, spd_stream_t stream);
+
+/*
+ * The same over selected key blocks: token i of sequence b reads, of the keys
+ * above, those of the blocks in topk_idx[h][cu_seqblocks_q[b] + i /
+ * block_size_q][:] (the rows msa_prefill_block_score writes).  A selection is
+ * a set: repeated ids count once; negative ids and ids >= NB select nothing.
+ * A token whose row is not below cu_seqblocks_q[b+1], or not a row of
+ * topk_idx, has no selection.
+ *
+ * topk_idx   [Hkv, n_rows, K] i32; a stride of 0 on dim 0 shares one
+ *            selection across kv heads
+ * block_size_q >= 1; cu_seqblocks_q [B+1] i32, nondecreasing
+ * workspace  spd_prefill_attention_workspace_bytes(total_q, Hq, Hkv, D, B,
+ *            NB, n_rows) bytes
+ */
+SPD_API void paged_sparse_prefill_attention(const spd_tensor *q, const spd_tensor *k_cache,
+                                            const spd_tensor *v_cache, const spd_tensor *block_table,
+                                            const spd_tensor *slot_ids, const spd_tensor *cu_seqlens,
+                                            const spd_tensor *seq_lens, const spd_tensor *prefix_lens,
+                                            const spd_tensor *topk_idx, int32_t block_size_q,
+                                            const spd_tensor *cu_seqblocks_q, const spd_tensor *out,
+                                            float sm_scale, int32_t block_size, float k_scale, float v_scale,
+                                            void *workspace, size_t workspace_bytes, spd_stream_t stream);
+
+/*
+ * Workspace bytes the two prefill attention calls need for these capacities;
+ * n_rows is 0 for paged_prefill_attention and the rows of topk_idx for the
+ * sparse call.  Never depends on device data, so one allocation serves every
+ * replay of a captured graph.  Returns 0 for shapes outside the domain.
+ */
+SPD_API size_t spd_prefill_attention_workspace_bytes(int64_t total_q, int64_t Hq, int64_t Hkv, int64_t D,
+                                                     int64_t B, int64_t NB, int64_t n_rows);
+
+/*
  * Status of the last call made on this thread: SPD_OK or an spd_status code.
  * When msg is not NULL, up to cap-1 bytes of a NUL-terminated description
  * are copied into it.
@@ -354,7 +522,8 @@ SPD_API int spd_set_attention_kernel(int policy);
 /*
  * Diagnostics: kernel selection per stage on this thread's subsequent calls.
  * stage 1 = msa_block_score, 2 = msa_select_topk, 3 = the attention calls
- * (the same setting as spd_set_attention_kernel), 4 = attention_sdpa.  policy
+ * (the same setting as spd_set_attention_kernel), 4 = attention_sdpa, 5 = the
+ * prefill attention calls, 6 = paged_norm_rope_store.  policy
  * 0 (default) picks the specialised kernel whenever the shapes and layouts
  * allow it, 1 always the general-layout kernel; for stage 2, policy 2 picks
  * the shared-memory rank kernel (the default sorts rows of up to 256 blocks

@@ -9,6 +9,10 @@ CUDA kernel:
   paged_decode_attention          the same over every block (dense decode)
   msa_prefill_block_score         fused prefill score-to-selection per query block
   attention_sdpa                  dense (not paged) GQA attention, causal flag
+  paged_assign_slots              page tables grown from a free list, token slots
+  paged_norm_rope_store           per-head norm and rotary positions into the caches
+  paged_prefill_attention         chunks of new tokens over the caches, every key
+  paged_sparse_prefill_attention  the same over the selected blocks
 
 The Python functions of the same names (in :mod:`.binding`) only marshal
 torch tensors into the C ABI; every step runs in the CUDA library.  They
@@ -26,6 +30,11 @@ __all__ = [
     "attention_sdpa",
     "msa_prefill_block_score",
     "prefill_workspace_bytes",
+    "paged_assign_slots",
+    "paged_norm_rope_store",
+    "paged_prefill_attention",
+    "paged_sparse_prefill_attention",
+    "prefill_attention_workspace_bytes",
     "decode_workspace_bytes",
     "launch_count",
     "set_attention_kernel",

@@ -27,6 +27,11 @@ __all__ = [
     "attention_sdpa",
     "msa_prefill_block_score",
     "prefill_workspace_bytes",
+    "paged_assign_slots",
+    "paged_norm_rope_store",
+    "paged_prefill_attention",
+    "paged_sparse_prefill_attention",
+    "prefill_attention_workspace_bytes",
     "decode_workspace_bytes",
     "launch_count",
     "set_attention_kernel",
@@ -90,6 +95,16 @@ def _load():
     L.msa_prefill_block_score.restype = None
     L.spd_prefill_workspace_bytes.argtypes = [ctypes.c_int64] * 3
     L.spd_prefill_workspace_bytes.restype = sz
+    L.paged_assign_slots.argtypes = [P] * 5 + [i32] * 3 + [P] * 8 + [vp]
+    L.paged_assign_slots.restype = None
+    L.paged_norm_rope_store.argtypes = [P] * 11 + [f32, i32, i32, f32, f32, vp]
+    L.paged_norm_rope_store.restype = None
+    L.paged_prefill_attention.argtypes = [P] * 9 + [f32, i32, f32, f32, vp, sz, vp]
+    L.paged_prefill_attention.restype = None
+    L.paged_sparse_prefill_attention.argtypes = [P] * 9 + [i32, P, P, f32, i32, f32, f32, vp, sz, vp]
+    L.paged_sparse_prefill_attention.restype = None
+    L.spd_prefill_attention_workspace_bytes.argtypes = [ctypes.c_int64] * 7
+    L.spd_prefill_attention_workspace_bytes.restype = sz
     L.attention_sdpa.argtypes = [P, P, P, P, f32, i32, vp]
     L.attention_sdpa.restype = None
     L.spd_decode_workspace_bytes.argtypes = [ctypes.c_int64] * 5 + [i32]
@@ -223,6 +238,73 @@ def prefill_workspace_bytes(total_q: int, Hi: int, NB: int) -> int:
     return int(lib.spd_prefill_workspace_bytes(total_q, Hi, NB))
 
 
+def paged_assign_slots(new_lens, prefix_lens, slot_ids, free_pages, free_count, n_pages, block_size, block_size_q,
+                       block_table, cu_seqlens, cu_seqblocks_q, seq_lens, req_idx, token_lens, slots, free_left,
+                       stream=None) -> None:
+    """Slots of a serving step: grow ``block_table`` [R, NB] in place from the
+    end of ``free_pages`` and fill the offsets, lengths and every token's row,
+    length and slot from the requests' ``new_lens`` and ``prefix_lens``."""
+    lib.paged_assign_slots(
+        _desc(new_lens, "new_lens"), _desc(prefix_lens, "prefix_lens"), _desc(slot_ids, "slot_ids"),
+        _desc(free_pages, "free_pages"), _desc(free_count, "free_count"), int(n_pages), int(block_size),
+        int(block_size_q), _desc(block_table, "block_table"), _desc(cu_seqlens, "cu_seqlens"),
+        _desc(cu_seqblocks_q, "cu_seqblocks_q"), _desc(seq_lens, "seq_lens"), _desc(req_idx, "req_idx"),
+        _desc(token_lens, "token_lens"), _desc(slots, "slots"), _desc(free_left, "free_left"), _stream(stream))
+    _check()
+
+
+def paged_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, token_lens, slots, q_out, k_cache, v_cache, eps,
+                          interleaved, block_size, k_scale, v_scale, stream=None) -> None:
+    """Per-head RMS norm (``q_weight``, ``k_weight`` [D], or None) and rotary
+    positions (``cos_sin`` [M, Rd]) of q and k: fill ``q_out`` [T, Hq, D] and
+    write k and v into ``slots`` of the caches.  ``v`` and ``v_cache`` may be
+    None together (index queries and keys)."""
+    lib.paged_norm_rope_store(
+        _desc(q, "q"), _desc(k, "k"), _desc(v, "v"), _desc(q_weight, "q_weight"), _desc(k_weight, "k_weight"),
+        _desc(cos_sin, "cos_sin"), _desc(token_lens, "token_lens"), _desc(slots, "slots"), _desc(q_out, "q_out"),
+        _desc(k_cache, "k_cache"), _desc(v_cache, "v_cache"), float(eps), 1 if interleaved else 0, int(block_size),
+        float(k_scale), float(v_scale), _stream(stream))
+    _check()
+
+
+def paged_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqlens, seq_lens, prefix_lens, out,
+                            sm_scale, block_size, k_scale, v_scale, workspace, stream=None) -> None:
+    """Prefill attention: fill ``out`` [total_q, Hq, D] (bf16) with attention
+    of a ragged batch of chunks over every key of the paged caches.
+
+    ``workspace`` is a CUDA uint8 tensor of at least
+    ``prefill_attention_workspace_bytes`` bytes."""
+    ws_ptr, ws_bytes = _workspace(workspace)
+    lib.paged_prefill_attention(
+        _desc(q, "q"), _desc(k_cache, "k_cache"), _desc(v_cache, "v_cache"), _desc(block_table, "block_table"),
+        _desc(slot_ids, "slot_ids"), _desc(cu_seqlens, "cu_seqlens"), _desc(seq_lens, "seq_lens"),
+        _desc(prefix_lens, "prefix_lens"), _desc(out, "out"), float(sm_scale), int(block_size), float(k_scale),
+        float(v_scale), ws_ptr, ws_bytes, _stream(stream))
+    _check()
+
+
+def paged_sparse_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqlens, seq_lens, prefix_lens,
+                                   topk_idx, block_size_q, cu_seqblocks_q, out, sm_scale, block_size, k_scale,
+                                   v_scale, workspace, stream=None) -> None:
+    """The same over the key blocks that ``topk_idx`` [Hkv, rows, K] lists for
+    each query block of ``block_size_q`` tokens (the rows that
+    msa_prefill_block_score writes)."""
+    ws_ptr, ws_bytes = _workspace(workspace)
+    lib.paged_sparse_prefill_attention(
+        _desc(q, "q"), _desc(k_cache, "k_cache"), _desc(v_cache, "v_cache"), _desc(block_table, "block_table"),
+        _desc(slot_ids, "slot_ids"), _desc(cu_seqlens, "cu_seqlens"), _desc(seq_lens, "seq_lens"),
+        _desc(prefix_lens, "prefix_lens"), _desc(topk_idx, "topk_idx"), int(block_size_q),
+        _desc(cu_seqblocks_q, "cu_seqblocks_q"), _desc(out, "out"), float(sm_scale), int(block_size), float(k_scale),
+        float(v_scale), ws_ptr, ws_bytes, _stream(stream))
+    _check()
+
+
+def prefill_attention_workspace_bytes(total_q: int, Hq: int, Hkv: int, D: int, B: int, NB: int, n_rows: int = 0) -> int:
+    """Workspace bytes the prefill attention calls need for these capacities
+    (``n_rows``: the rows of topk_idx, 0 for paged_prefill_attention)."""
+    return int(lib.spd_prefill_attention_workspace_bytes(total_q, Hq, Hkv, D, B, NB, n_rows))
+
+
 def attention_sdpa(q, k, v, out, sm_scale, causal, stream=None) -> None:
     """Dense GQA attention: fill ``out`` [T, Hq, D] from q [T, Hq, D] and
     k, v [S, Hkv, D]; with ``causal`` query t reads keys j <= t + S - T."""
@@ -245,12 +327,12 @@ def set_attention_kernel(policy: int) -> int:
     return int(lib.spd_set_attention_kernel(int(policy)))
 
 
-STAGE_SCORE, STAGE_SELECT, STAGE_ATTENTION, STAGE_SDPA = 1, 2, 3, 4
+STAGE_SCORE, STAGE_SELECT, STAGE_ATTENTION, STAGE_SDPA, STAGE_PREFILL_ATTENTION, STAGE_STORE = 1, 2, 3, 4, 5, 6
 
 
 def set_kernel_policy(stage: int, policy: int) -> int:
     """Kernel choice of one stage (1 score, 2 select, 3 attention, 4 dense
-    attention) on this thread: 0 = specialised kernel where it applies
+    attention, 5 prefill attention, 6 norm and store) on this thread: 0 = specialised kernel where it applies
     (default), 1 = general-layout kernel always.  Returns the previous
     policy."""
     old = int(lib.spd_set_kernel_policy(int(stage), int(policy)))
