@@ -1,0 +1,1011 @@
+// chunk_tc.cu -- the prefill attention calls on the sm_103a tensor cores, for
+// 16-bit queries of head dim 64 or 128 over a BF16 or FP8-E4M3 paged cache.
+//
+// A CTA works through units of the plan (chunk_plan.cuh): two tiles of 128
+// query rows (128 / G tokens with their G heads each) of one kv head, over a
+// piece of their key blocks, one page of 128 keys at a time:
+//
+//   S_i  = Q_i K^T      tcgen05.mma kind::f16, M = 128 rows, N = 128 keys
+//   P_i  = 2^(S_i c - m) one thread per row; its 128 logits sit in registers,
+//                        so the block maximum and the row sum need no exchange
+//   O_i += P_i V        P from tensor memory (written over its own S), V as it
+//                        lies in the page (MN-major)
+//
+// The two tiles share every K and V page in shared memory and alternate on the
+// tensor pipe: the products are issued PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1), so
+// one tile's softmax runs while the other tile's products do.  Products of one
+// issuing thread execute in order: S_i(j+1) is written after PV_i(j) has read
+// P_i(j) from the same columns, and whoever sees S_i(j+1) knows that PV_i(j)
+// is done.
+//
+// A BF16 cache is multiplied as bf16, straight from the pages.  E4M3 pages are
+// widened to f16 (exact) by a warpgroup of their own, and the queries are made
+// f16 by a power of two per row (exact for elements within 2^38 of their row's
+// largest), which the row's logit factor takes back.
+//
+// Softmax: c = sm_scale * k_scale * log2(e) > 0.  The exponent offset m of a
+// row is raised only when a block's maximum exceeds it by more than 2^kRaise
+// (then the row's O is rescaled in tensor memory), so p <= 2^kRaise; p is
+// rounded to the 16-bit type of the products, the row sum is kept in fp32.
+//
+// Keys that a row does not read take p = 0 by its limit, a count of keys.  A
+// product with V would still turn 0 * NaN into NaN, so the V tile of a block
+// that some row of the unit does not read in full is scrubbed in shared memory
+// first: keys that no row reads become zeros, and elements that are not finite
+// become zeros and leave a mark; rows that do read such a key look its
+// elements up in the page at the end and take the NaN or infinity from there.
+//
+// Roles (16 warps): warps 0-3 and 4-7 the softmax and epilogue of tile 0 and 1
+// (warp w reads TMEM lanes 32 (w % 4) .. +31), warps 8-11 widen (E4M3) and
+// scrub, warp 12 issues the TMA loads, warp 13 owns tensor memory and issues
+// every MMA, warp 14 claims units and builds their page lists one unit ahead.
+// Every wait is bounded: one that gives up sets bit 0 of the workspace status
+// word and the CTA winds down.
+#include <math.h>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "chunk_plan.cuh"
+#include "spd_dispatch.h"
+#include "spd_internal.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.cuh"
+
+namespace spd {
+
+namespace {
+
+constexpr int kRows = 128;           // query rows of a tile (M)
+constexpr int kKeys = kBlock;        // keys of a block (N of S, K of P V)
+constexpr int kThreads = 512;
+constexpr int kWarpSide = 8, kWarpTma = 12, kWarpMma = 13, kWarpSched = 14;
+constexpr int kBox = 128 * 128;      // 64 dims of 128 rows of a 16-bit type, bytes
+constexpr float kRaise = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+// registers: 128 a thread at launch; the softmax warpgroups rise to 184, the
+// two others drop to 72
+constexpr uint32_t kRegsSoft = 184, kRegsOther = 72;
+static_assert(256 * kRegsSoft + 256 * kRegsOther <= kThreads * 128, "register split");
+constexpr uint32_t kUnitReleases = 8 + 4 + 1 + 1;  // warps that read a unit record
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;         // S_i at 128 i, O_i at 256 + 128 i
+
+template <int D, bool F8>
+struct Shape {
+    static constexpr int kBoxes = D / 64;
+    static constexpr int kTileQ = kBoxes * kBox;  // one tile of queries
+    static constexpr int kTile = kBoxes * kBox;   // one 16-bit K or V page
+    static constexpr int kRaw = kKeys * D;        // one E4M3 page
+    static constexpr int kTiles = F8 ? 3 : 4;
+    static constexpr int kRaws = F8 ? 3 : 0;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffTile = kOffQ + 2 * kTileQ;
+    static constexpr int kOffRaw = kOffTile + kTiles * kTile;
+    static constexpr int kEnd = kOffRaw + kRaws * kRaw;
+};
+
+struct UnitRec {
+    int32_t nblk;        // key blocks; -1: no more units
+    int32_t tok0, i0, nt;  // first query token, its index in the chunk, tokens
+    int32_t h, two;      // kv head; the second tile has rows
+    int32_t pre, cap;    // a row's limit is min(pre + i + 1, cap), at least 0
+    int32_t lim_lo;      // limits of the first and the last token
+    int32_t lim_hi;
+    int32_t mixed;       // rows of several query blocks: each tests its own bitmap
+    int32_t qrow0, qrow_end;  // selection row of the sequence's first token, and the end of its rows
+    int32_t pieces, part;     // pieces of the pair; partial slot of this one
+    int32_t part0;       // partial slot of piece 0
+    int32_t ticket;      // of tile 0
+    int32_t bt_row;      // page-table row
+    int32_t marked;      // some V element of a scrubbed block is not finite
+    int32_t page[kMaxNB];
+    uint16_t kb[kMaxNB];
+    uint32_t marks[kMaxNB / 32];  // key blocks that hold such elements
+};
+
+struct Shared {
+    uint64_t u_full[2], u_empty[2];
+    uint64_t q_full, q_empty, q_ready[2];
+    uint64_t t_full[4], t_empty[4], t_ready[4];
+    uint64_t r_full[3], r_empty[3];
+    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    float row_factor[2][2 * kRows];  // by parity of the units with products: what the queries' scaling takes from the logits
+    UnitRec unit[2];
+};
+
+struct TcArgs {
+    ChunkArgs a;
+    ChunkLayout lay;
+    char *ws;
+    int32_t G, heads_built, q_f16;
+    float c;  // sm_scale * k_scale * log2(e)
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ bool aborted(Shared &sh) { return *reinterpret_cast<volatile int *>(&sh.abort) != 0; }
+
+__device__ __forceinline__ bool wait_or_abort(Shared &sh, uint64_t *bar, uint32_t parity) {
+    if (tc::mbar_wait(bar, parity)) return true;
+    *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+    return false;
+}
+
+// Warp-uniform wait, for the warp-collective accesses that follow it.
+__device__ __forceinline__ bool warp_wait(Shared &sh, uint64_t *bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity));
+    if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+    return ok;
+}
+
+// Arrival of a whole warp, after what its lanes wrote.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, bool bf16) {
+    if (bf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return tc::f32x2_to_f16x2(lo, hi);
+}
+
+__device__ __forceinline__ int32_t row_limit(const UnitRec &u, int32_t i) {
+    return max(min(u.pre + i + 1, u.cap), 0);
+}
+
+__device__ __forceinline__ bool finite_bits(uint32_t x, bool bf16) {
+    const uint32_t e = bf16 ? 0x7f80u : 0x7c00u;
+    return (x & e) != e;
+}
+
+// Elements of the marked blocks' V rows that this row reads and that are not
+// finite: bits of masks[0] NaN, [1] +inf, [2] -inf, a word per 32 dims.
+template <int D, bool F8>
+__device__ __noinline__ void marked_values(const TcArgs &t, const UnitRec &u, int32_t lim, const uint32_t *row_bits,
+                                           uint32_t (*masks)[D / 32]) {
+    const ChunkArgs &a = t.a;
+    for (int kb = 0; kb * kKeys < lim; ++kb) {
+        if (!((u.marks[kb >> 5] >> (kb & 31)) & 1u)) continue;
+        if (row_bits != nullptr && !((row_bits[kb >> 5] >> (kb & 31)) & 1u)) continue;
+        const int64_t page = a.bt[u.bt_row * a.bt_s0 + kb * a.bt_s1];
+        const int n = min(kKeys, lim - kb * kKeys);
+        for (int i = 0; i < n; ++i) {
+            const uint8_t *v = a.v + ((page * kKeys + i) * a.v_s0 + u.h * a.v_s1) * (F8 ? 1 : 2);
+            for (int d0 = 0; d0 < D; d0 += F8 ? 16 : 8) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(v + d0 * (F8 ? 1 : 2));
+                const uint32_t wp[4] = {w.x, w.y, w.z, w.w};
+                for (int k = 0; k < 4; ++k) {
+                    if (F8 ? __vcmpeq4(wp[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) == 0
+                           : finite_bits(wp[k], true) && finite_bits(wp[k] >> 16, true))
+                        continue;
+                    for (int e = 0; e < (F8 ? 4 : 2); ++e) {
+                        const int d = d0 + k * (F8 ? 4 : 2) + e;
+                        const uint32_t bits = F8 ? (wp[k] >> (8 * e)) & 0xffu : (wp[k] >> (16 * e)) & 0xffffu;
+                        if (F8 ? (bits & 0x7fu) == 0x7fu : (bits & 0x7fffu) > 0x7f80u) masks[0][d >> 5] |= 1u << (d & 31);
+                        else if (!F8 && (bits & 0x7fffu) == 0x7f80u) masks[bits >> 15 ? 2 : 1][d >> 5] |= 1u << (d & 31);
+                    }
+                }
+            }
+            uint32_t all = 0xffffffffu;
+            for (int k = 0; k < D / 32; ++k) all &= masks[0][k];
+            if (all == 0xffffffffu) return;
+        }
+    }
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreads, 1)
+chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TcArgs t) {
+    using S = Shape<D, F8>;
+    constexpr bool kBf16 = !F8;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Shared &sh = *reinterpret_cast<Shared *>(smem + S::kEnd);
+    const ChunkArgs &a = t.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ChunkHeader *hd = reinterpret_cast<ChunkHeader *>(t.ws + t.lay.header);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sh.u_full[i], 1);
+            tc::mbar_init(&sh.u_empty[i], kUnitReleases);
+            tc::mbar_init(&sh.q_ready[i], 4);
+            tc::mbar_init(&sh.s_full[i], 1);
+            tc::mbar_init(&sh.p_full[i], 4);
+            tc::mbar_init(&sh.o_full[i], 1);
+            tc::mbar_init(&sh.o_free[i], 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(&sh.t_full[i], 1);
+            tc::mbar_init(&sh.t_empty[i], 1);
+            tc::mbar_init(&sh.t_ready[i], 4);
+        }
+        for (int i = 0; i < 3; ++i) {
+            tc::mbar_init(&sh.r_full[i], 1);
+            tc::mbar_init(&sh.r_empty[i], 4);
+        }
+        tc::mbar_init(&sh.q_full, 1);
+        tc::mbar_init(&sh.q_empty, 1);
+        tc::mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == kWarpMma) tc::tmem_alloc(&sh.tmem_base, kTmemCols);
+    if (threadIdx.x == kWarpTma * 32) {
+        tc::prefetch_tmap(&tmap_q);
+        tc::prefetch_tmap(&tmap_k);
+        tc::prefetch_tmap(&tmap_v);
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    tc::pdl_wait();  // the plan
+
+    if (warp < kWarpSide) {
+        tc::regs_inc<kRegsSoft>();
+        // ----------------------------------------------- softmax, epilogue
+        const int tile = warp >> 2, quad = warp & 3;
+        const int r = quad * 32 + lane;  // row of the tile = TMEM lane
+        const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t col_s = tmem + lane_base + kColS + tile * 128;
+        const uint32_t col_o = tmem + lane_base + kColO + tile * 128;
+        const int j_tok = tile * t.lay.tt + r / t.G, g = r % t.G;  // token within the pair, head within the group
+        const bool in_tile = r < t.lay.tt * t.G;
+        uint32_t n_s = 0, n_o = 0;  // S buffers seen, O tiles seen
+        uint32_t nq = 0;            // units with products
+        for (uint32_t n = 0;; ++n) {
+            UnitRec &u = sh.unit[n & 1];
+            if (!warp_wait(sh, &sh.u_full[n & 1], (n >> 1) & 1) || u.nblk < 0) break;
+            const int nblk = u.nblk;
+            const bool have = in_tile && j_tok < u.nt;
+            const int32_t lim = have ? row_limit(u, u.i0 + j_tok) : 0;
+            const uint32_t iq = nq;
+            if (nblk > 0) ++nq;
+            if (tile == 1 && !u.two) {
+                warp_arrive(&sh.u_empty[n & 1], lane);
+                continue;
+            }
+            const uint32_t *bits = nullptr;  // the row's own selection, when the unit's rows differ
+            bool chosen = true;
+            if (u.mixed && have) {
+                const int64_t row = static_cast<int64_t>(u.qrow0) + (u.i0 + j_tok) / a.bsq;
+                chosen = row >= 0 && row < u.qrow_end;
+                if (chosen)
+                    bits = reinterpret_cast<const uint32_t *>(t.ws + t.lay.bitmaps) +
+                           ((t.heads_built > 1 ? static_cast<int64_t>(u.h) : 0) * a.n_rows + row) * t.lay.words;
+            }
+            float c = t.c;
+            if (F8 && nblk > 0) {
+                if (!warp_wait(sh, &sh.q_ready[iq & 1], (iq >> 1) & 1)) break;
+                c *= sh.row_factor[iq & 1][tile * kRows + r];
+            }
+            float m_run = -INFINITY, l = 0.f;
+            bool seen = false, ok = true;
+            int word_at = -1;
+            uint32_t word = 0;
+            for (int j = 0; j < nblk; ++j) {
+                ok = warp_wait(sh, &sh.s_full[tile], n_s & 1);
+                if (!ok) break;
+                ++n_s;
+                tc::tc_fence_after();
+                float s[kKeys];
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) tmem_ld32(col_s + ch * 32, s + ch * 32);
+                const int kb = u.kb[j];
+                int left = lim - kb * kKeys;  // keys of the block that the row reads
+                if (u.mixed) {
+                    if (bits != nullptr && (kb >> 5) != word_at) {
+                        word_at = kb >> 5;
+                        word = bits[word_at];
+                    }
+                    if (!chosen || !((word >> (kb & 31)) & 1u)) left = 0;
+                }
+                seen |= left > 0;
+                tc::tmem_wait_ld();
+                if (left < kKeys) {
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i)
+                        if (i >= left) s[i] = -INFINITY;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[i + k]), s[i + 4 + k]);
+                const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                // raise the offset if the block's maximum runs more than
+                // 2^kRaise above it (or the row had none yet)
+                float alpha = 1.f;
+                if (bm != -INFINITY && bm > m_run + kRaise) {
+                    alpha = (m_run == -INFINITY) ? 0.f : tc::ex2(m_run - bm);
+                    m_run = bm;
+                    l *= alpha;
+                }
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // S(j) is there, so the products of block j - 1 are done
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 16; ++ch) {
+                        float o[16];
+                        tc::tmem_ld16(col_o + ch * 16, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                        tc::tmem_st16(col_o + ch * 16, o);
+                    }
+                }
+                const float m_eff = (m_run == -INFINITY) ? 0.f : m_run;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float p0 = tc::ex2(fmaf(s[half * 64 + 2 * i], c, -m_eff));
+                        const float p1 = tc::ex2(fmaf(s[half * 64 + 2 * i + 1], c, -m_eff));
+                        sum[i & 1] += p0;
+                        sum[2 + (i & 1)] += p1;
+                        pk[i] = pack2(p0, p1, kBf16);
+                    }
+                    tc::tmem_st32u(col_s + half * 32, pk);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                warp_arrive(&sh.p_full[tile], lane);
+            }
+            if (!ok) break;
+            // a row that reads keys whose logits are all -inf (or NaN) has no
+            // finite softmax: NaN, as the formula gives
+            if (seen && m_run == -INFINITY) {
+                m_run = 0.f;
+                l = NAN;
+            }
+
+            // ------------------------------------------------- epilogue
+            if (nblk > 0) {
+                ok = warp_wait(sh, &sh.o_full[tile], n_o & 1);
+                if (!ok) break;
+                ++n_o;
+                tc::tc_fence_after();
+            }
+            uint32_t odd[3][D / 32];  // NaN, +inf, -inf dims from scrubbed V rows
+            const bool any_odd = nblk > 0 && u.marked != 0 && have && chosen;
+            if (any_odd) {
+                for (int k = 0; k < 3; ++k)
+                    for (int i = 0; i < D / 32; ++i) odd[k][i] = 0;
+                marked_values<D, F8>(t, u, lim, bits, odd);
+            }
+            const bool split = u.pieces > 1;
+            const int64_t tok = u.tok0 + j_tok;
+            const int64_t obase = tok * a.o_s0 + static_cast<int64_t>(u.h * t.G + g) * a.o_s1;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
+            const bool vec = a.o_s2 == 1 && (reinterpret_cast<uintptr_t>(out + obase) & 15) == 0;
+            float *part = reinterpret_cast<float *>(t.ws + t.lay.partials) +
+                          (static_cast<int64_t>(u.part) * 256 + tile * kRows + r) * (D + 2);
+            const float f = (l == 0.f && m_run == -INFINITY) ? 0.f : a.v_scale / l;
+#pragma unroll 1
+            for (int ch = 0; ch < D / 16; ++ch) {
+                float o[16];
+                if (nblk > 0) {
+                    tc::tmem_ld16(col_o + ch * 16, o);
+                    tc::tmem_wait_ld();
+                }
+                if (nblk == 0 || (!split && m_run == -INFINITY)) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+                }
+                if (any_odd) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int d = ch * 16 + i;
+                        const bool nan = (odd[0][d >> 5] >> (d & 31)) & 1u, pos = (odd[1][d >> 5] >> (d & 31)) & 1u,
+                                   neg = (odd[2][d >> 5] >> (d & 31)) & 1u;
+                        if (nan || (pos && neg)) o[i] = NAN;
+                        else if (pos) o[i] += INFINITY;
+                        else if (neg) o[i] -= INFINITY;
+                    }
+                }
+                if (!have) continue;
+                if (split) {
+                    float2 *dst = reinterpret_cast<float2 *>(part + ch * 16);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dst[i] = make_float2(o[2 * i], o[2 * i + 1]);
+                } else if (vec) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = pack2(o[2 * i] * f, o[2 * i + 1] * f, true);
+                    uint4 *dst = reinterpret_cast<uint4 *>(out + obase + ch * 16);
+                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) out[obase + (ch * 16 + i) * a.o_s2] = __float2bfloat16_rn(o[i] * f);
+                }
+            }
+            if (nblk > 0) {
+                tc::tc_fence_before();
+                warp_arrive(&sh.o_free[tile], lane);
+            }
+            if (split) {
+                if (have) *reinterpret_cast<float2 *>(part + D) = make_float2(m_run, l);
+                // the last piece to finish joins them all, in order; each of
+                // the tile's four warps counts, and joins, for its own rows
+                __threadfence();
+                __syncwarp();
+                int32_t *ticket = reinterpret_cast<int32_t *>(t.ws + t.lay.tickets) + u.ticket + tile;
+                int last = 0;
+                if (lane == 0) {
+                    last = atomicAdd(ticket, 1 << (8 * quad));
+                    last = ((last >> (8 * quad)) & 0xff) == u.pieces - 1;
+                }
+                last = __shfl_sync(0xffffffffu, last, 0);
+                if (last) {
+                    __threadfence();
+                    const float *p0 = reinterpret_cast<const float *>(t.ws + t.lay.partials) +
+                                      (static_cast<int64_t>(u.part0) * 256 + tile * kRows + r) * (D + 2);
+                    const int64_t step = 256 * (D + 2);
+                    float M = -INFINITY;
+                    if (have)
+                        for (int k = 0; k < u.pieces; ++k) M = fmaxf(M, __ldcg(p0 + k * step + D));
+                    float L = 0.f;
+                    if (have)
+                        for (int k = 0; k < u.pieces; ++k) {
+                            const float m = __ldcg(p0 + k * step + D);
+                            if (m != -INFINITY) L = fmaf(__ldcg(p0 + k * step + D + 1), tc::ex2(m - M), L);
+                        }
+                    const float fj = M == -INFINITY ? 0.f : a.v_scale / L;
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 16; ++ch) {
+                        if (!have) break;
+                        float o[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = 0.f;
+                        for (int k = 0; k < u.pieces; ++k) {
+                            const float m = __ldcg(p0 + k * step + D);
+                            if (m == -INFINITY) continue;
+                            const float w = tc::ex2(m - M);
+                            const float2 *src = reinterpret_cast<const float2 *>(p0 + k * step + ch * 16);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 x = __ldcg(src + i);
+                                o[2 * i] = fmaf(x.x, w, o[2 * i]);
+                                o[2 * i + 1] = fmaf(x.y, w, o[2 * i + 1]);
+                            }
+                        }
+                        if (vec) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) w[i] = pack2(o[2 * i] * fj, o[2 * i + 1] * fj, true);
+                            uint4 *dst = reinterpret_cast<uint4 *>(out + obase + ch * 16);
+                            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                out[obase + (ch * 16 + i) * a.o_s2] = __float2bfloat16_rn(o[i] * fj);
+                        }
+                    }
+                }
+            }
+            warp_arrive(&sh.u_empty[n & 1], lane);
+        }
+    } else {
+        tc::regs_dec<kRegsOther>();
+        if (warp < kWarpTma) {
+            // ------------------------------------------- widen and scrub
+            const int row = (warp - kWarpSide) * 32 + lane;  // key of the page; query row of each tile
+            uint32_t x = 0;                                  // 16-bit tiles so far (K, V, K, V, ...)
+            uint32_t nq = 0;                                 // units with products
+            for (uint32_t n = 0;; ++n) {
+                UnitRec &u = sh.unit[n & 1];
+                if (!warp_wait(sh, &sh.u_full[n & 1], (n >> 1) & 1) || u.nblk < 0) break;
+                const int nblk = u.nblk;
+                bool ok = true;
+                if (F8 && nblk > 0) {
+                    // queries to f16, in place, scaled by a power of two per row
+                    ok = warp_wait(sh, &sh.q_full, nq & 1);
+                    if (!ok) break;
+                    for (int tile = 0; tile < 1 + u.two; ++tile) {
+                        float factor = 1.f;
+                        if (!t.q_f16) {
+                            uint8_t *q = smem + S::kOffQ + tile * S::kTileQ + row * 128;
+                            uint32_t top = 0;
+#pragma unroll
+                            for (int b = 0; b < S::kBoxes; ++b)
+#pragma unroll
+                                for (int ch = 0; ch < 8; ++ch) {
+                                    const uint4 w = *reinterpret_cast<const uint4 *>(q + b * kBox + ((ch ^ (row & 7)) << 4));
+                                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                                                 __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+                                }
+                            const int e = static_cast<int>(max(top & 0xffffu, top >> 16) >> 7);  // biased exponent
+                            const int shift = e == 0 ? 0 : min(14 - (e - 127), 100);
+                            const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+                            factor = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+#pragma unroll
+                            for (int b = 0; b < S::kBoxes; ++b)
+#pragma unroll 2
+                                for (int ch = 0; ch < 8; ++ch) {
+                                    uint4 *at = reinterpret_cast<uint4 *>(q + b * kBox + ((ch ^ (row & 7)) << 4));
+                                    uint4 w = *at;
+                                    uint32_t *wp = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        wp[i] = tc::f32x2_to_f16x2(__uint_as_float(wp[i] << 16) * up,
+                                                                   __uint_as_float(wp[i] & 0xffff0000u) * up);
+                                    *at = w;
+                                }
+                        }
+                        sh.row_factor[nq & 1][tile * kRows + row] = factor;
+                    }
+                    tc::fence_proxy_async();
+                    warp_arrive(&sh.q_ready[nq & 1], lane);
+                    ++nq;
+                }
+                for (int j = 0; j < nblk && ok; ++j) {
+                    const int kb = u.kb[j];
+                    // V of a block that some row does not read in full
+                    const bool scrub = u.mixed || (kb + 1) * kKeys > u.lim_lo;
+                    const bool unread = kb * kKeys + row >= u.lim_hi;  // by every row
+                    bool mark = false;
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv, ++x) {
+                        const int slot = x % S::kTiles;
+                        uint8_t *dst = smem + S::kOffTile + slot * S::kTile + row * 128;
+                        if (F8) {
+                            const int rs = x % 3;
+                            ok = warp_wait(sh, &sh.r_full[rs], (x / 3) & 1);
+                            if (ok && x >= static_cast<uint32_t>(S::kTiles))
+                                ok = warp_wait(sh, &sh.t_empty[slot], ((x / S::kTiles) - 1) & 1);
+                            if (!ok) break;
+                            const uint8_t *src = smem + S::kOffRaw + rs * S::kRaw + row * D;
+                            uint4 w[D / 16];
+#pragma unroll
+                            for (int ch = 0; ch < D / 16; ++ch)
+                                w[ch] = *reinterpret_cast<const uint4 *>(
+                                    src + ((ch ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4));
+                            if (kv == 1 && scrub) {
+#pragma unroll
+                                for (int ch = 0; ch < D / 16; ++ch) {
+                                    uint32_t *wp = reinterpret_cast<uint32_t *>(&w[ch]);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const uint32_t bad = __vcmpeq4(wp[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);  // NaN bytes
+                                        mark |= bad != 0 && !unread;
+                                        wp[i] = unread ? 0u : wp[i] & ~bad;
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int ch = 0; ch < D / 16; ++ch) {
+                                uint32_t h[8];
+                                const uint32_t *wp = reinterpret_cast<const uint32_t *>(&w[ch]);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) tc::e4m3x4_to_f16x4(wp[i], h[2 * i], h[2 * i + 1]);
+                                uint8_t *box = dst + (ch >> 2) * kBox;
+                                const int c0 = (2 * ch) & 7;
+                                *reinterpret_cast<uint4 *>(box + ((c0 ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                                *reinterpret_cast<uint4 *>(box + (((c0 + 1) ^ (row & 7)) << 4)) =
+                                    make_uint4(h[4], h[5], h[6], h[7]);
+                            }
+                            if (mark) {
+                                atomicOr(&u.marks[kb >> 5], 1u << (kb & 31));
+                                *reinterpret_cast<volatile int32_t *>(&u.marked) = 1;
+                            }
+                            tc::fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tc::mbar_arrive(&sh.r_empty[rs]);
+                                tc::mbar_arrive(&sh.t_ready[slot]);
+                            }
+                        } else if (kv == 1) {
+                            ok = warp_wait(sh, &sh.t_full[slot], (x / S::kTiles) & 1);
+                            if (!ok) break;
+                            if (scrub) {
+#pragma unroll
+                                for (int b = 0; b < S::kBoxes; ++b)
+#pragma unroll 2
+                                    for (int ch = 0; ch < 8; ++ch) {
+                                        uint4 *at = reinterpret_cast<uint4 *>(dst + b * kBox + ((ch ^ (row & 7)) << 4));
+                                        uint4 w = *at;
+                                        uint32_t *wp = reinterpret_cast<uint32_t *>(&w);
+                                        bool change = unread;
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            if (unread) { wp[i] = 0; continue; }
+                                            if (!finite_bits(wp[i], true)) { wp[i] &= 0xffff0000u; change = mark = true; }
+                                            if (!finite_bits(wp[i] >> 16, true)) { wp[i] &= 0xffffu; change = mark = true; }
+                                        }
+                                        if (change) *at = w;
+                                    }
+                                if (mark) {
+                                    atomicOr(&u.marks[kb >> 5], 1u << (kb & 31));
+                                    *reinterpret_cast<volatile int32_t *>(&u.marked) = 1;
+                                }
+                                tc::fence_proxy_async();
+                            }
+                            warp_arrive(&sh.t_ready[slot], lane);
+                        }
+                    }
+                }
+                if (!ok) break;
+                warp_arrive(&sh.u_empty[n & 1], lane);
+            }
+        } else if (warp == kWarpTma) {
+            // ------------------------------------------------- TMA loads
+            if (lane == 0) {
+                uint32_t x = 0;  // K and V pages so far
+                uint32_t nq = 0;
+                bool ok = true;
+                for (uint32_t n = 0; ok; ++n) {
+                    UnitRec &u = sh.unit[n & 1];
+                    ok = wait_or_abort(sh, &sh.u_full[n & 1], (n >> 1) & 1);
+                    if (!ok || u.nblk < 0) break;
+                    const int nblk = u.nblk;
+                    for (int j = 0; j < nblk && ok; ++j) {
+                        const int slot0 = u.page[j] * kKeys;
+                        for (int kv = 0; kv < 2; ++kv, ++x) {
+                            const CUtensorMap *map = kv == 0 ? &tmap_k : &tmap_v;
+                            if (F8) {
+                                const int rs = x % 3;
+                                ok = !aborted(sh) && (x < 3 || wait_or_abort(sh, &sh.r_empty[rs], ((x / 3) - 1) & 1));
+                                if (!ok) break;
+                                tc::mbar_arrive_expect_tx(&sh.r_full[rs], S::kRaw);
+                                tc::tma_load_3d(smem + S::kOffRaw + rs * S::kRaw, map, &sh.r_full[rs], 0, u.h, slot0);
+                            } else {
+                                const int slot = x % S::kTiles;
+                                ok = !aborted(sh) && (x < static_cast<uint32_t>(S::kTiles) ||
+                                                      wait_or_abort(sh, &sh.t_empty[slot], ((x / S::kTiles) - 1) & 1));
+                                if (!ok) break;
+                                tc::mbar_arrive_expect_tx(&sh.t_full[slot], S::kTile);
+                                for (int b = 0; b < S::kBoxes; ++b)
+                                    tc::tma_load_3d(smem + S::kOffTile + slot * S::kTile + b * kBox, map, &sh.t_full[slot],
+                                                    64 * b, u.h, slot0);
+                            }
+                        }
+                        if (j == 0 && ok) {
+                            // the queries, once the last unit's products have read theirs
+                            ok = nq == 0 || wait_or_abort(sh, &sh.q_empty, (nq - 1) & 1);
+                            if (!ok) break;
+                            const int tiles = 1 + u.two;
+                            tc::mbar_arrive_expect_tx(&sh.q_full, tiles * S::kBoxes * 128 * t.G * t.lay.tt);
+                            for (int i = 0; i < tiles; ++i)
+                                for (int b = 0; b < S::kBoxes; ++b)
+                                    tc::tma_load_3d(smem + S::kOffQ + i * S::kTileQ + b * kBox, &tmap_q, &sh.q_full, 64 * b,
+                                                    u.h * t.G, u.tok0 + i * t.lay.tt);
+                            ++nq;
+                        }
+                    }
+                    if (ok) tc::mbar_arrive(&sh.u_empty[n & 1]);
+                }
+                // every issued copy lands before the CTA may exit; only after
+                // an abort can one still be in flight
+                if (!ok) {
+                    if (nq > 0) tc::mbar_wait(&sh.q_full, (nq - 1) & 1);
+                    const uint32_t ring = F8 ? 3 : S::kTiles;
+                    for (uint32_t y = x > ring ? x - ring : 0; y < x; ++y)
+                        tc::mbar_wait(F8 ? &sh.r_full[y % ring] : &sh.t_full[y % ring], (y / ring) & 1);
+                }
+            }
+        } else if (warp == kWarpMma) {
+            // ------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                const uint32_t idesc_s = tc::idesc_f16_m128(kKeys, kBf16);
+                const uint32_t idesc_o = tc::idesc_f16_m128(D, kBf16) | (1u << 16);  // B (V) MN-major
+                const uint32_t aQ = tc::smem_u32(smem + S::kOffQ), aT = tc::smem_u32(smem + S::kOffTile);
+                uint32_t x = 0, nq = 0;          // tiles consumed, units with products
+                uint32_t n_p[2] = {0, 0}, n_o[2] = {0, 0};
+                bool ok = true;
+                auto tile_wait = [&](uint32_t y, bool v) {
+                    uint64_t *bar = (F8 || v) ? &sh.t_ready[y % S::kTiles] : &sh.t_full[y % S::kTiles];
+                    return wait_or_abort(sh, bar, (y / S::kTiles) & 1);
+                };
+                auto qk = [&](int i, uint32_t y) {
+                    const uint32_t q = aQ + i * S::kTileQ, k = aT + (y % S::kTiles) * S::kTile;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        // 16 dims a step: 32 bytes into a 128-byte row, the next 64 dims one box on
+                        const uint32_t off = (ks >> 2) * kBox + (ks & 3) * 32;
+                        tc::mma_f16(tmem + kColS + i * 128, tc::smem_desc(q + off, 16, 1024, tc::kSw128),
+                                    tc::smem_desc(k + off, 16, 1024, tc::kSw128), idesc_s, ks > 0);
+                    }
+                    tc::mma_commit(&sh.s_full[i]);
+                };
+                auto pv = [&](int i, uint32_t y, bool add) {
+                    const uint32_t v = aT + (y % S::kTiles) * S::kTile;
+#pragma unroll
+                    for (int ks = 0; ks < kKeys / 16; ++ks)
+                        // P: 16 keys = 8 columns of 16-bit pairs; V: two 8-key groups, the next 64 dims one box on
+                        tc::mma_f16_tmem_a(tmem + kColO + i * 128, tmem + kColS + i * 128 + ks * 8,
+                                           tc::smem_desc(v + ks * 2048, kBox, 1024, tc::kSw128), idesc_o, add || ks > 0);
+                };
+                for (uint32_t n = 0; ok; ++n) {
+                    UnitRec &u = sh.unit[n & 1];
+                    ok = wait_or_abort(sh, &sh.u_full[n & 1], (n >> 1) & 1);
+                    if (!ok || u.nblk < 0) break;
+                    const int nblk = u.nblk, tiles = 1 + u.two;
+                    if (nblk > 0) {
+                        ok = (F8 ? wait_or_abort(sh, &sh.q_ready[nq & 1], (nq >> 1) & 1) : wait_or_abort(sh, &sh.q_full, nq & 1)) &&
+                             tile_wait(x, false);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        for (int i = 0; i < tiles; ++i) qk(i, x);
+                        tc::mma_commit(&sh.t_empty[x % S::kTiles]);
+                        if (nblk == 1) tc::mma_commit(&sh.q_empty);
+                        for (int j = 0; j < nblk && ok; ++j) {
+                            const uint32_t yk = x + 2, yv = x + 1;  // K of block j + 1, V of block j
+                            for (int i = 0; i < tiles; ++i) {
+                                if (j == 0 && n_o[i] > 0) ok = wait_or_abort(sh, &sh.o_free[i], (n_o[i] - 1) & 1);
+                                ok = ok && wait_or_abort(sh, &sh.p_full[i], n_p[i] & 1) && (i > 0 || tile_wait(yv, true));
+                                if (!ok) break;
+                                ++n_p[i];
+                                tc::tc_fence_after();
+                                pv(i, yv, j > 0);
+                                if (i == tiles - 1) tc::mma_commit(&sh.t_empty[yv % S::kTiles]);
+                                if (j == nblk - 1) {
+                                    tc::mma_commit(&sh.o_full[i]);
+                                    ++n_o[i];
+                                    continue;
+                                }
+                                if (i == 0) {
+                                    ok = tile_wait(yk, false);
+                                    if (!ok) break;
+                                    tc::tc_fence_after();
+                                }
+                                qk(i, yk);
+                                if (i == tiles - 1) {
+                                    tc::mma_commit(&sh.t_empty[yk % S::kTiles]);
+                                    if (j == nblk - 2) tc::mma_commit(&sh.q_empty);
+                                }
+                            }
+                            x += 2;
+                        }
+                        ++nq;
+                    }
+                    if (ok) tc::mbar_arrive(&sh.u_empty[n & 1]);
+                }
+                // every issued product completes before tensor memory is released
+                tc::mma_commit(&sh.drain);
+                tc::mbar_wait(&sh.drain, 0);
+            }
+        } else if (warp == kWarpSched) {
+            // ---------------------------------------------- units, page lists
+            const ChunkPair *pairs = reinterpret_cast<const ChunkPair *>(t.ws + t.lay.pairs);
+            const int32_t n_units = hd->n_units, head_units = hd->head_units, n_pairs = hd->n_pairs;
+            int32_t id = blockIdx.x;
+            for (uint32_t n = 0;; ++n) {
+                UnitRec &u = sh.unit[n & 1];
+                if (n >= 2 && !warp_wait(sh, &sh.u_empty[n & 1], ((n >> 1) - 1) & 1)) break;
+                if (aborted(sh)) break;
+                if (id >= n_units) {
+                    if (lane == 0) {
+                        u.nblk = -1;
+                        tc::mbar_arrive(&sh.u_full[n & 1]);
+                    }
+                    break;
+                }
+                const int h = id / head_units, v = id % head_units;
+                int lo = 0, hi = n_pairs;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (pairs[mid].unit0 <= v) lo = mid; else hi = mid;
+                }
+                const ChunkPair pr = pairs[lo];
+                const int piece = v - pr.unit0;
+                const int32_t table_row = a.sid[pr.b * a.sid_s0];
+                const bool in_table = table_row >= 0 && table_row < a.R;
+                const int32_t pre = min(max(a.pre[pr.b * a.pre_s0], -(1 << 30)), 1 << 30);
+                const int32_t cap = in_table ? min(a.sl[pr.b * a.sl_s0], a.NB * kKeys) : 0;
+                const int32_t lim_lo = max(min(pre + pr.i0 + 1, cap), 0);
+                const int32_t lim_hi = max(min(pre + pr.i0 + pr.nt, cap), 0);
+                const int vis = (lim_hi + kKeys - 1) / kKeys;  // blocks that the last token sees
+                // blocks of the pair: all that it sees, or the union of its query blocks' selections
+                uint32_t word = 0;  // lane l: blocks 32 l ..
+                int32_t qrow0 = 0, qrow_end = 0, q0 = 0, q1 = 0;
+                if (lane * 32 < vis) word = vis - lane * 32 >= 32 ? 0xffffffffu : (1u << (vis - lane * 32)) - 1u;
+                if (a.tk != nullptr) {
+                    q0 = pr.i0 / a.bsq;
+                    q1 = (pr.i0 + pr.nt - 1) / a.bsq;
+                    qrow0 = a.cub[pr.b * a.cub_s0];
+                    qrow_end = min(a.cub[(pr.b + 1) * a.cub_s0], a.n_rows);
+                    uint32_t any = 0;
+                    if (lane < t.lay.words) {
+                        const uint32_t *bm = reinterpret_cast<const uint32_t *>(t.ws + t.lay.bitmaps) +
+                                             (t.heads_built > 1 ? static_cast<int64_t>(h) : 0) * a.n_rows * t.lay.words + lane;
+#pragma unroll 4
+                        for (int q = q0; q <= q1; ++q) {
+                            const int64_t row = static_cast<int64_t>(qrow0) + q;
+                            if (row >= 0 && row < qrow_end) any |= bm[row * t.lay.words];
+                        }
+                    }
+                    word &= any;
+                }
+                // this piece's share of the list, by rank
+                int before = __popc(word);
+                const int mine = before;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, before, d);
+                    if (lane >= d) before += y;
+                }
+                const int listed = __shfl_sync(0xffffffffu, before, 31);
+                before -= mine;
+                const int r0 = static_cast<int>(static_cast<int64_t>(listed) * piece / pr.pieces);
+                const int r1 = static_cast<int>(static_cast<int64_t>(listed) * (piece + 1) / pr.pieces);
+                int count = 0;
+                for (int w = 0; w * 32 < vis; ++w) {
+                    const uint32_t ww = __shfl_sync(0xffffffffu, word, w);
+                    const int wb = __shfl_sync(0xffffffffu, before, w);
+                    if (wb >= r1 || wb + __popc(ww) <= r0) continue;
+                    const int rank = wb + __popc(ww & ((1u << lane) - 1u));
+                    bool take = ((ww >> lane) & 1u) && rank >= r0 && rank < r1;
+                    int32_t page = -1;
+                    if (take) page = a.bt[table_row * a.bt_s0 + (w * 32 + lane) * a.bt_s1];
+                    take = take && page >= 0 && page < a.P;
+                    const uint32_t taken = __ballot_sync(0xffffffffu, take);
+                    if (take) {
+                        const int at = count + __popc(taken & ((1u << lane) - 1u));
+                        u.page[at] = page;
+                        u.kb[at] = static_cast<uint16_t>(w * 32 + lane);
+                    }
+                    count += __popc(taken);
+                }
+                u.marks[lane] = 0;
+                if (lane == 0) {
+                    u.nblk = count;
+                    u.tok0 = pr.tok0;
+                    u.i0 = pr.i0;
+                    u.nt = pr.nt;
+                    u.h = h;
+                    u.two = pr.nt > t.lay.tt;
+                    u.pre = pre;
+                    u.cap = cap;
+                    u.lim_lo = lim_lo;
+                    u.lim_hi = lim_hi;
+                    // query blocks without a selection of their own also make the rows differ
+                    u.mixed = a.tk != nullptr && (q1 > q0 || static_cast<int64_t>(qrow0) + q1 >= qrow_end || qrow0 < 0);
+                    u.qrow0 = qrow0;
+                    u.qrow_end = qrow_end;
+                    u.pieces = pr.pieces;
+                    u.part0 = h * hd->head_parts + pr.part0;
+                    u.part = u.part0 + piece;
+                    u.ticket = 2 * (h * n_pairs + lo);
+                    u.bt_row = table_row;
+                    u.marked = 0;
+                    id = static_cast<int32_t>(gridDim.x) + atomicAdd(&hd->next_unit, 1);
+                }
+                warp_arrive(&sh.u_full[n & 1], lane);
+                id = __shfl_sync(0xffffffffu, id, 0);
+            }
+        }
+    }
+
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (threadIdx.x == 0 && aborted(sh)) atomicOr(&hd->status, 1);
+    if (warp == kWarpMma) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// [rows, heads, D] tensor as a 3-D map: boxes of `dims` dims x `heads_box`
+// heads x `rows_box` rows, swizzled over the box's row width.
+bool make_map(CUtensorMap *m, CUtensorMapDataType type, int es, const void *base, int64_t D, int64_t heads, int64_t rows,
+              int64_t s1, int64_t s0, int dims, int heads_box, int rows_box) {
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t shape[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * es, static_cast<cuuint64_t>(s0) * es};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(dims), static_cast<cuuint32_t>(heads_box),
+                               static_cast<cuuint32_t>(rows_box)};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return fn(m, type, 3, const_cast<void *>(base), shape, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              dims * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Strides of extents above one must be positive multiples of 16 bytes below
+// the map's limit of 2^40 bytes.
+bool map_ok(const void *base, int es, int64_t s0, int64_t s1, int64_t n0, int64_t n1) {
+    auto legal = [es](int64_t s) { return s > 0 && (s * es) % 16 == 0 && s < (int64_t(1) << 40) / es; };
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (n1 <= 1 || legal(s1)) && (n0 <= 1 || legal(s0));
+}
+
+template <int D, bool F8>
+cudaError_t launch(const ChunkArgs &a, void *ws, cudaStream_t stream, bool *used) {
+    using S = Shape<D, F8>;
+    constexpr int kSmem = S::kEnd + 1024 + static_cast<int>(sizeof(Shared));
+    static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+    const int G = a.Hq / a.Hkv;
+    const ChunkLayout lay(a.total_q, a.Hq, a.Hkv, a.D, a.B, a.NB, a.n_rows);
+    constexpr int es = F8 ? 1 : 2;
+    constexpr CUtensorMapDataType kv_type = F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    const int64_t slots = a.P * kKeys;
+    // strides of extents of one are never stepped over: any legal value does
+    const int64_t qs1 = a.Hq > 1 ? a.q_s1 : D, qs0 = a.total_q > 1 ? a.q_s0 : D;
+    const int64_t ks1 = a.Hkv > 1 ? a.k_s1 : D, vs1 = a.Hkv > 1 ? a.v_s1 : D;
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.q, D, a.Hq, a.total_q, qs1, qs0, 64, G, lay.tt) ||
+        !make_map(&mk, kv_type, es, a.k, D, a.Hkv, slots, ks1, a.k_s0, F8 ? D : 64, 1, kKeys) ||
+        !make_map(&mv, kv_type, es, a.v, D, a.Hkv, slots, vs1, a.v_s0, F8 ? D : 64, 1, kKeys))
+        return cudaSuccess;
+    const void *func = reinterpret_cast<const void *>(chunk_tc_kernel<D, F8>);
+    cudaError_t e = opt_in_smem(func, kSmem);
+    if (e != cudaSuccess) return e;
+
+    ChunkPlanArgs p{};
+    p.a = a;
+    p.lay = lay;
+    p.ws = static_cast<char *>(ws);
+    p.heads_built = (a.tk_s0 == 0 || a.Hkv == 1) ? 1 : a.Hkv;
+    p.ctas = device_sm_count();
+    e = launch_chunk_plan(p, stream);
+    if (e != cudaSuccess) return e;
+
+    TcArgs t{};
+    t.a = a;
+    t.lay = lay;
+    t.ws = p.ws;
+    t.G = G;
+    t.heads_built = p.heads_built;
+    t.q_f16 = a.q_dt == SPD_F16;
+    t.c = a.sm_scale * a.k_scale * kLog2e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    // the prologue may run beside the plan kernel's tail; the kernel waits for
+    // its end before it reads global memory
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, F8>, mq, mk, mv, t);
+    if (e != cudaSuccess) return e;
+    count_launches(2);
+    *used = true;
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tc(const ChunkArgs &a, void *ws, cudaStream_t stream, bool *used) {
+    *used = false;
+    const bool f8 = a.kv_dt == SPD_E4M3;
+    if (a.D != 64 && a.D != 128) return cudaSuccess;
+    if (a.q_dt != SPD_BF16 && !(f8 && a.q_dt == SPD_F16)) return cudaSuccess;
+    // the exponents need one sign, and the queries' scaling some headroom
+    const float c = a.sm_scale * a.k_scale * kLog2e;
+    if (!(c > 1e-30f) || !(c < 1e30f)) return cudaSuccess;
+    const int es = f8 ? 1 : 2;
+    if (a.P < 1 || a.q_s2 != 1 || !map_ok(a.q, 2, a.q_s0, a.q_s1, a.total_q, a.Hq) ||
+        !map_ok(a.k, es, a.k_s0, a.k_s1, a.P * kKeys, a.Hkv) || !map_ok(a.v, es, a.v_s0, a.v_s1, a.P * kKeys, a.Hkv))
+        return cudaSuccess;
+    if (f8) return a.D == 128 ? launch<128, true>(a, ws, stream, used) : launch<64, true>(a, ws, stream, used);
+    return a.D == 128 ? launch<128, false>(a, ws, stream, used) : launch<64, false>(a, ws, stream, used);
+}
+
+}  // namespace spd

@@ -1,4 +1,5 @@
 // serve_dispatch.cu -- picks the kernel of the serving-step calls.
+#include "chunk_plan.cuh"
 #include "serve.cuh"
 #include "spd_dispatch.h"
 #include "spd_internal.cuh"
@@ -22,6 +23,11 @@ cudaError_t dispatch_store(const StoreArgs &a, cudaStream_t stream) { return lau
 
 cudaError_t dispatch_chunk(const ChunkArgs &a, void *ws, size_t ws_bytes, cudaStream_t stream) {
     (void)ws_bytes;
+    if (g_serve_policy[0] == 0) {
+        bool used = false;
+        const cudaError_t e = launch_chunk_tc(a, ws, stream, &used);
+        if (e != cudaSuccess || used) return e;
+    }
     const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int32_t), stream);  // the status word
     if (e != cudaSuccess) return e;
     return launch_chunk_generic(a, stream);
@@ -29,8 +35,7 @@ cudaError_t dispatch_chunk(const ChunkArgs &a, void *ws, size_t ws_bytes, cudaSt
 
 size_t chunk_workspace_bytes(int64_t total_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t NB,
                              int64_t n_rows) {
-    (void)total_q; (void)Hq; (void)Hkv; (void)D; (void)B; (void)NB; (void)n_rows;
-    return 256;  // the status word
+    return ChunkLayout(total_q, Hq, Hkv, D, B, NB, n_rows).total;
 }
 
 }  // namespace spd
