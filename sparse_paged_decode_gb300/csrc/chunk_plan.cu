@@ -192,13 +192,16 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
     }
 
     // unit and partial ranges
-    int32_t ucarry = 0, pcarry = 0;
+    int32_t ucarry = 0, pcarry = 0, scarry = 0;
+    int32_t *splits = reinterpret_cast<int32_t *>(p.ws + p.lay.splits);
     for (int base = 0; base < n_pairs; base += kPlanT) {
         const int q = base + tid;
-        int32_t k = 0, utotal, ptotal;
+        int32_t k = 0, utotal, ptotal, stotal;
         if (q < n_pairs) k = max((pairs[q].cost + U - 1) / U, 1);
         const int32_t ku = scan_cta(k, sums, &utotal);
         const int32_t kp = scan_cta(k > 1 ? k : 0, sums, &ptotal);
+        const int32_t ks = scan_cta(k > 1 ? 1 : 0, sums, &stotal);
+        if (k > 1) splits[scarry + ks] = q;
         if (q < n_pairs) {
             pairs[q].unit0 = ucarry + ku;
             pairs[q].pieces = k;
@@ -206,9 +209,8 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
         }
         ucarry += utotal;
         pcarry += ptotal;
+        scarry += stotal;
     }
-    int32_t *tickets = reinterpret_cast<int32_t *>(p.ws + p.lay.tickets);
-    for (int64_t q = tid; q < 2LL * n_pairs * a.Hkv; q += kPlanT) tickets[q] = 0;
     if (tid == 0) {
         hd->status = 0;
         hd->next_unit = 0;
@@ -216,6 +218,7 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
         hd->n_units = ucarry * a.Hkv;
         hd->head_units = ucarry;
         hd->head_parts = pcarry;
+        hd->n_splits = scarry;
     }
 }
 

@@ -8,8 +8,8 @@
 //   unit   (pair, kv head, piece): a contiguous piece of the pair's key
 //          blocks, the work item of one CTA.  A pair in one piece writes its
 //          rows at once; the pieces of a split pair leave fp32 partials
-//          (running max, sum, unnormalised output) that the last piece to
-//          finish joins, in piece order
+//          (running max, sum, unnormalised output) that a kernel behind the
+//          attention kernel joins, in piece order
 //
 // Units are numbered head by head, pairs of the longest sequences first, and
 // within a head the pieces of a sequence's pairs lie next to each other: the
@@ -30,7 +30,8 @@ struct ChunkHeader {
     int32_t n_units;    // of all heads
     int32_t head_units; // of one head
     int32_t head_parts; // partial slots of one head
-    int32_t reserved[58];
+    int32_t n_splits;   // pairs in more than one piece
+    int32_t reserved[57];
 };
 static_assert(sizeof(ChunkHeader) == 256, "header is one 256-byte line");
 
@@ -50,7 +51,7 @@ constexpr int kChunkMaxParts = 608;  // partial slots: four pieces per SM of a 1
 
 // Byte layout of the workspace for capacities.
 struct ChunkLayout {
-    size_t header, pairs, tickets, bitmaps, partials, total;
+    size_t header, pairs, splits, bitmaps, stats, partials, total;
     int64_t pair_cap, part_cap;
     int tt, words;
 
@@ -68,9 +69,10 @@ struct ChunkLayout {
         size_t off = 0;
         header = off;   off += align(sizeof(ChunkHeader));
         pairs = off;    off += align(sizeof(ChunkPair) * (size_t)pair_cap);
-        tickets = off;  off += align(sizeof(int32_t) * 2 * (size_t)pair_cap * (size_t)Hkv);
+        splits = off;   off += align(sizeof(int32_t) * (size_t)pair_cap);
         bitmaps = off;  off += align(sizeof(uint32_t) * (size_t)Hkv * (size_t)n_rows * (size_t)words);
-        partials = off; off += align(sizeof(float) * (size_t)part_cap * 256 * (size_t)(D + 2));
+        stats = off;    off += align(sizeof(float) * 2 * (size_t)part_cap * 256);
+        partials = off; off += align(sizeof(float) * (size_t)part_cap * 256 * (size_t)D);
         total = off;
     }
 };

@@ -12,11 +12,10 @@
 //                        lies in the page (MN-major)
 //
 // The two tiles share every K and V page in shared memory and alternate on the
-// tensor pipe: the products are issued PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1), so
-// one tile's softmax runs while the other tile's products do.  Products of one
-// issuing thread execute in order: S_i(j+1) is written after PV_i(j) has read
-// P_i(j) from the same columns, and whoever sees S_i(j+1) knows that PV_i(j)
-// is done.
+// tensor pipe, each with an issuing warp of its own: one tile's softmax runs
+// while the other tile's products do.  Products of one issuing thread execute
+// in order: S(j+1) of a tile is written after its P V(j) has read P(j) from
+// the same columns, and whoever sees S(j+1) knows that P V(j) is done.
 //
 // A BF16 cache is multiplied as bf16, straight from the pages.  E4M3 pages are
 // widened to f16 (exact) by a warpgroup of their own, and the queries are made
@@ -37,8 +36,9 @@
 //
 // Roles (16 warps): warps 0-3 and 4-7 the softmax and epilogue of tile 0 and 1
 // (warp w reads TMEM lanes 32 (w % 4) .. +31), warps 8-11 widen (E4M3) and
-// scrub, warp 12 issues the TMA loads, warp 13 owns tensor memory and issues
-// every MMA, warp 14 claims units and builds their page lists one unit ahead.
+// scrub, warp 12 issues the TMA loads, warps 13 and 15 the products of tile 0
+// and 1 (warp 13 owns tensor memory), warp 14 claims units and builds their
+// page lists one unit ahead.
 // Every wait is bounded: one that gives up sets bit 0 of the workspace status
 // word and the CTA winds down.
 #include <math.h>
@@ -59,7 +59,7 @@ namespace {
 constexpr int kRows = 128;           // query rows of a tile (M)
 constexpr int kKeys = kBlock;        // keys of a block (N of S, K of P V)
 constexpr int kThreads = 512;
-constexpr int kWarpSide = 8, kWarpTma = 12, kWarpMma = 13, kWarpSched = 14;
+constexpr int kWarpSide = 8, kWarpTma = 12, kWarpMma = 13, kWarpSched = 14, kWarpMma1 = 15;
 constexpr int kBox = 128 * 128;      // 64 dims of 128 rows of a 16-bit type, bytes
 constexpr float kRaise = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -67,7 +67,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // two others drop to 72
 constexpr uint32_t kRegsSoft = 184, kRegsOther = 72;
 static_assert(256 * kRegsSoft + 256 * kRegsOther <= kThreads * 128, "register split");
-constexpr uint32_t kUnitReleases = 8 + 4 + 1 + 1;  // warps that read a unit record
+constexpr uint32_t kUnitReleases = 8 + 4 + 1 + 2;  // warps that read a unit record
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;         // S_i at 128 i, O_i at 256 + 128 i
 
@@ -95,8 +95,6 @@ struct UnitRec {
     int32_t mixed;       // rows of several query blocks: each tests its own bitmap
     int32_t qrow0, qrow_end;  // selection row of the sequence's first token, and the end of its rows
     int32_t pieces, part;     // pieces of the pair; partial slot of this one
-    int32_t part0;       // partial slot of piece 0
-    int32_t ticket;      // of tile 0
     int32_t bt_row;      // page-table row
     int32_t marked;      // some V element of a scrubbed block is not finite
     int32_t page[kMaxNB];
@@ -110,7 +108,7 @@ struct Shared {
     uint64_t t_full[4], t_empty[4], t_ready[4];
     uint64_t r_full[3], r_empty[3];
     uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
-    uint64_t drain;
+    uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
     float row_factor[2][2 * kRows];  // by parity of the units with products: what the queries' scaling takes from the logits
@@ -138,6 +136,56 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Matrix descriptors of the 128-byte-swizzled operands (128 rows or keys of
+// 128 bytes, 8-row groups 1024 bytes apart; `lbo`: the next 64 dims of an
+// MN-major operand).  Only the address field differs between the steps of a
+// product, so a product builds the low word once and each step adds a
+// constant to it.
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (static_cast<uint32_t>(tc::kSw128) << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+
+// D (+)= A B, kind::f16, A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %4};\n\t"
+        "mov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(kDescHigh), "r"(add)
+        : "memory");
+}
+
+// D (+)= A B, kind::f16, A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_low, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_low), "r"(idesc), "r"(kDescHigh), "r"(add)
+        : "memory");
+}
+
+// 32 bytes, a whole memory sector, in one store (32-byte aligned).
+__device__ __forceinline__ void store32(void *dst, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// One lane of the converged warp, the same one every time.  It is asked anew
+// for every product: from its answer the compiler knows that one thread issues
+// the products.  (A loop-invariant answer kept in a variable must not be used
+// instead: it invites the compiler to give the two kinds of lanes loops of
+// their own, which then run interleaved.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(one)::"memory");
+    return one != 0;
 }
 
 __device__ __forceinline__ bool aborted(Shared &sh) { return *reinterpret_cast<volatile int *>(&sh.abort) != 0; }
@@ -178,18 +226,24 @@ __device__ __forceinline__ bool finite_bits(uint32_t x, bool bf16) {
     return (x & e) != e;
 }
 
-// Elements of the marked blocks' V rows that this row reads and that are not
-// finite: bits of masks[0] NaN, [1] +inf, [2] -inf, a word per 32 dims.
+// Elements of the marked blocks' V rows that this row reads (keys below lim, of
+// its own selection where row_bits is given) and that are not finite, added to
+// the row's O in tensor memory, where the products saw zeros in their place.
+// A warp-collective, and a rare, call.
 template <int D, bool F8>
-__device__ __noinline__ void marked_values(const TcArgs &t, const UnitRec &u, int32_t lim, const uint32_t *row_bits,
-                                           uint32_t (*masks)[D / 32]) {
+__device__ __noinline__ void take_marked(const TcArgs &t, const UnitRec &u, int32_t lim, const uint32_t *row_bits,
+                                         uint32_t col_o) {
     const ChunkArgs &a = t.a;
-    for (int kb = 0; kb * kKeys < lim; ++kb) {
+    uint32_t odd[3][D / 32];  // NaN, +inf, -inf dims
+    for (int k = 0; k < 3; ++k)
+        for (int i = 0; i < D / 32; ++i) odd[k][i] = 0;
+    uint32_t all = 0;  // all dims NaN: nothing more to find
+    for (int kb = 0; kb * kKeys < lim && all != 0xffffffffu; ++kb) {
         if (!((u.marks[kb >> 5] >> (kb & 31)) & 1u)) continue;
         if (row_bits != nullptr && !((row_bits[kb >> 5] >> (kb & 31)) & 1u)) continue;
         const int64_t page = a.bt[u.bt_row * a.bt_s0 + kb * a.bt_s1];
         const int n = min(kKeys, lim - kb * kKeys);
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < n && all != 0xffffffffu; ++i) {
             const uint8_t *v = a.v + ((page * kKeys + i) * a.v_s0 + u.h * a.v_s1) * (F8 ? 1 : 2);
             for (int d0 = 0; d0 < D; d0 += F8 ? 16 : 8) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(v + d0 * (F8 ? 1 : 2));
@@ -200,16 +254,31 @@ __device__ __noinline__ void marked_values(const TcArgs &t, const UnitRec &u, in
                         continue;
                     for (int e = 0; e < (F8 ? 4 : 2); ++e) {
                         const int d = d0 + k * (F8 ? 4 : 2) + e;
-                        const uint32_t bits = F8 ? (wp[k] >> (8 * e)) & 0xffu : (wp[k] >> (16 * e)) & 0xffffu;
-                        if (F8 ? (bits & 0x7fu) == 0x7fu : (bits & 0x7fffu) > 0x7f80u) masks[0][d >> 5] |= 1u << (d & 31);
-                        else if (!F8 && (bits & 0x7fffu) == 0x7f80u) masks[bits >> 15 ? 2 : 1][d >> 5] |= 1u << (d & 31);
+                        const uint32_t x = F8 ? (wp[k] >> (8 * e)) & 0xffu : (wp[k] >> (16 * e)) & 0xffffu;
+                        if (F8 ? (x & 0x7fu) == 0x7fu : (x & 0x7fffu) > 0x7f80u) odd[0][d >> 5] |= 1u << (d & 31);
+                        else if (!F8 && (x & 0x7fffu) == 0x7f80u) odd[x >> 15 ? 2 : 1][d >> 5] |= 1u << (d & 31);
                     }
                 }
             }
-            uint32_t all = 0xffffffffu;
-            for (int k = 0; k < D / 32; ++k) all &= masks[0][k];
-            if (all == 0xffffffffu) return;
+            all = 0xffffffffu;
+            for (int k = 0; k < D / 32; ++k) all &= odd[0][k];
         }
+    }
+    __syncwarp();
+    for (int c0 = 0; c0 < D; c0 += 16) {
+        float o[16];
+        tc::tmem_ld16(col_o + c0, o);
+        tc::tmem_wait_ld();
+        const uint32_t nan = odd[0][c0 >> 5] >> (c0 & 31), pos = odd[1][c0 >> 5] >> (c0 & 31),
+                       neg = odd[2][c0 >> 5] >> (c0 & 31);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if ((nan >> i) & 1u) o[i] = NAN;
+            if ((pos >> i) & 1u) o[i] += INFINITY;
+            if ((neg >> i) & 1u) o[i] -= INFINITY;
+        }
+        tc::tmem_st16(col_o + c0, o);
+        tc::tmem_wait_st();
     }
 }
 
@@ -238,7 +307,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         }
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(&sh.t_full[i], 1);
-            tc::mbar_init(&sh.t_empty[i], 1);
+            tc::mbar_init(&sh.t_empty[i], 2);
             tc::mbar_init(&sh.t_ready[i], 4);
         }
         for (int i = 0; i < 3; ++i) {
@@ -246,8 +315,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             tc::mbar_init(&sh.r_empty[i], 4);
         }
         tc::mbar_init(&sh.q_full, 1);
-        tc::mbar_init(&sh.q_empty, 1);
-        tc::mbar_init(&sh.drain, 1);
+        tc::mbar_init(&sh.q_empty, 2);
+        tc::mbar_init(&sh.drain[0], 1);
+        tc::mbar_init(&sh.drain[1], 1);
         sh.abort = 0;
         tc::fence_mbar_init();
     }
@@ -262,6 +332,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     tc::tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
     tc::pdl_wait();  // the plan
+    tc::pdl_trigger();
 
     if (warp < kWarpSide) {
         tc::regs_inc<kRegsSoft>();
@@ -390,125 +461,51 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 ++n_o;
                 tc::tc_fence_after();
             }
-            uint32_t odd[3][D / 32];  // NaN, +inf, -inf dims from scrubbed V rows
-            const bool any_odd = nblk > 0 && u.marked != 0 && have && chosen;
-            if (any_odd) {
-                for (int k = 0; k < 3; ++k)
-                    for (int i = 0; i < D / 32; ++i) odd[k][i] = 0;
-                marked_values<D, F8>(t, u, lim, bits, odd);
-            }
+            if (nblk > 0 && u.marked != 0) take_marked<D, F8>(t, u, have && chosen ? lim : 0, bits, col_o);
             const bool split = u.pieces > 1;
-            const int64_t tok = u.tok0 + j_tok;
-            const int64_t obase = tok * a.o_s0 + static_cast<int64_t>(u.h * t.G + g) * a.o_s1;
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
-            const bool vec = a.o_s2 == 1 && (reinterpret_cast<uintptr_t>(out + obase) & 15) == 0;
-            float *part = reinterpret_cast<float *>(t.ws + t.lay.partials) +
-                          (static_cast<int64_t>(u.part) * 256 + tile * kRows + r) * (D + 2);
-            const float f = (l == 0.f && m_run == -INFINITY) ? 0.f : a.v_scale / l;
+            const bool none = nblk == 0 || m_run == -INFINITY;  // no key of this piece was read
+            const int64_t prow = static_cast<int64_t>(u.part) * 256 + tile * kRows + r;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (u.tok0 + j_tok) * a.o_s0 +
+                                 static_cast<int64_t>(u.h * t.G + g) * a.o_s1;
+            const bool vec = a.o_s2 == 1 && (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+            const float f = none ? 0.f : a.v_scale / l;
 #pragma unroll 1
-            for (int ch = 0; ch < D / 16; ++ch) {
-                float o[16];
+            for (int c0 = 0; c0 < D; c0 += 64) {
+                float o[64];
                 if (nblk > 0) {
-                    tc::tmem_ld16(col_o + ch * 16, o);
+                    tmem_ld32(col_o + c0, o);
+                    tmem_ld32(col_o + c0 + 32, o + 32);
                     tc::tmem_wait_ld();
-                }
-                if (nblk == 0 || (!split && m_run == -INFINITY)) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = 0.f;
-                }
-                if (any_odd) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int d = ch * 16 + i;
-                        const bool nan = (odd[0][d >> 5] >> (d & 31)) & 1u, pos = (odd[1][d >> 5] >> (d & 31)) & 1u,
-                                   neg = (odd[2][d >> 5] >> (d & 31)) & 1u;
-                        if (nan || (pos && neg)) o[i] = NAN;
-                        else if (pos) o[i] += INFINITY;
-                        else if (neg) o[i] -= INFINITY;
+                    if (c0 + 64 == D) {  // the next unit's products may overwrite O
+                        tc::tc_fence_before();
+                        warp_arrive(&sh.o_free[tile], lane);
                     }
-                }
-                if (!have) continue;
-                if (split) {
-                    float2 *dst = reinterpret_cast<float2 *>(part + ch * 16);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dst[i] = make_float2(o[2 * i], o[2 * i + 1]);
-                } else if (vec) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = pack2(o[2 * i] * f, o[2 * i + 1] * f, true);
-                    uint4 *dst = reinterpret_cast<uint4 *>(out + obase + ch * 16);
-                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    for (int i = 0; i < 64; ++i) o[i] = none ? 0.f : o[i];
                 } else {
+                    // defined on every path: a register that is not would
+                    // stay reserved through the block loop
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) out[obase + (ch * 16 + i) * a.o_s2] = __float2bfloat16_rn(o[i] * f);
+                    for (int i = 0; i < 64; ++i) o[i] = 0.f;
                 }
-            }
-            if (nblk > 0) {
-                tc::tc_fence_before();
-                warp_arrive(&sh.o_free[tile], lane);
-            }
-            if (split) {
-                if (have) *reinterpret_cast<float2 *>(part + D) = make_float2(m_run, l);
-                // the last piece to finish joins them all, in order; each of
-                // the tile's four warps counts, and joins, for its own rows
-                __threadfence();
-                __syncwarp();
-                int32_t *ticket = reinterpret_cast<int32_t *>(t.ws + t.lay.tickets) + u.ticket + tile;
-                int last = 0;
-                if (lane == 0) {
-                    last = atomicAdd(ticket, 1 << (8 * quad));
-                    last = ((last >> (8 * quad)) & 0xff) == u.pieces - 1;
-                }
-                last = __shfl_sync(0xffffffffu, last, 0);
-                if (last) {
-                    __threadfence();
-                    const float *p0 = reinterpret_cast<const float *>(t.ws + t.lay.partials) +
-                                      (static_cast<int64_t>(u.part0) * 256 + tile * kRows + r) * (D + 2);
-                    const int64_t step = 256 * (D + 2);
-                    float M = -INFINITY;
-                    if (have)
-                        for (int k = 0; k < u.pieces; ++k) M = fmaxf(M, __ldcg(p0 + k * step + D));
-                    float L = 0.f;
-                    if (have)
-                        for (int k = 0; k < u.pieces; ++k) {
-                            const float m = __ldcg(p0 + k * step + D);
-                            if (m != -INFINITY) L = fmaf(__ldcg(p0 + k * step + D + 1), tc::ex2(m - M), L);
-                        }
-                    const float fj = M == -INFINITY ? 0.f : a.v_scale / L;
-#pragma unroll 1
-                    for (int ch = 0; ch < D / 16; ++ch) {
-                        if (!have) break;
-                        float o[16];
+                if (have && split) {
+                    float *part = reinterpret_cast<float *>(t.ws + t.lay.partials) + prow * D + c0;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = 0.f;
-                        for (int k = 0; k < u.pieces; ++k) {
-                            const float m = __ldcg(p0 + k * step + D);
-                            if (m == -INFINITY) continue;
-                            const float w = tc::ex2(m - M);
-                            const float2 *src = reinterpret_cast<const float2 *>(p0 + k * step + ch * 16);
+                    for (int i = 0; i < 64; i += 8) store32(part + i, reinterpret_cast<const uint32_t *>(o + i));
+                } else if (have && vec) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float2 x = __ldcg(src + i);
-                                o[2 * i] = fmaf(x.x, w, o[2 * i]);
-                                o[2 * i + 1] = fmaf(x.y, w, o[2 * i + 1]);
-                            }
-                        }
-                        if (vec) {
-                            uint32_t w[8];
+                    for (int i = 0; i < 64; i += 16) {
+                        uint32_t w[8];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) w[i] = pack2(o[2 * i] * fj, o[2 * i + 1] * fj, true);
-                            uint4 *dst = reinterpret_cast<uint4 *>(out + obase + ch * 16);
-                            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                out[obase + (ch * 16 + i) * a.o_s2] = __float2bfloat16_rn(o[i] * fj);
-                        }
+                        for (int k = 0; k < 8; ++k) w[k] = pack2(o[i + 2 * k] * f, o[i + 2 * k + 1] * f, true);
+                        store32(out + c0 + i, w);
                     }
+                } else if (have) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) out[(c0 + i) * a.o_s2] = __float2bfloat16_rn(o[i] * f);
                 }
             }
+            if (have && split) reinterpret_cast<float2 *>(t.ws + t.lay.stats)[prow] = make_float2(m_run, l);
             warp_arrive(&sh.u_empty[n & 1], lane);
         }
     } else {
@@ -709,87 +706,116 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         tc::mbar_wait(F8 ? &sh.r_full[y % ring] : &sh.t_full[y % ring], (y / ring) & 1);
                 }
             }
-        } else if (warp == kWarpMma) {
-            // ------------------------------------------------ MMA issuer
-            if (lane == 0) {
-                const uint32_t idesc_s = tc::idesc_f16_m128(kKeys, kBf16);
-                const uint32_t idesc_o = tc::idesc_f16_m128(D, kBf16) | (1u << 16);  // B (V) MN-major
-                const uint32_t aQ = tc::smem_u32(smem + S::kOffQ), aT = tc::smem_u32(smem + S::kOffTile);
-                uint32_t x = 0, nq = 0;          // tiles consumed, units with products
-                uint32_t n_p[2] = {0, 0}, n_o[2] = {0, 0};
-                bool ok = true;
-                auto tile_wait = [&](uint32_t y, bool v) {
-                    uint64_t *bar = (F8 || v) ? &sh.t_ready[y % S::kTiles] : &sh.t_full[y % S::kTiles];
-                    return wait_or_abort(sh, bar, (y / S::kTiles) & 1);
-                };
-                auto qk = [&](int i, uint32_t y) {
-                    const uint32_t q = aQ + i * S::kTileQ, k = aT + (y % S::kTiles) * S::kTile;
+        } else if (warp == kWarpMma || warp == kWarpMma1) {
+            // ----------------------------------------------- MMA issuers
+            // One warp per tile: a product takes 512 tensor cycles and the
+            // pipe's queue holds few instructions, so what a warp does between
+            // two products (waits, commits: 100 to 300 cycles) would leave the
+            // pipe idle if the other tile's products did not fill it.  The
+            // whole warp waits and counts, one elected lane issues.
+            const int i = warp == kWarpMma ? 0 : 1;
+            const uint32_t idesc_s = tc::idesc_f16_m128(kKeys, kBf16);
+            const uint32_t idesc_o = tc::idesc_f16_m128(D, kBf16) | (1u << 16);  // B (V) MN-major
+            const uint32_t q_low = desc_low(tc::smem_u32(smem + S::kOffQ + i * S::kTileQ), 16);
+            const uint32_t t_low = desc_low(tc::smem_u32(smem + S::kOffTile), 0);
+            const uint32_t col_s = tmem + kColS + i * 128, col_o = tmem + kColO + i * 128;
+            uint32_t k_slot = 0, k_par = 0, v_slot = 0, v_par = 0;  // ring places of the next K and V tile
+            uint32_t nq = 0, n_p = 0, n_o = 0;                      // units with products, P and O tiles so far
+            bool ok = true;
+            auto step = [&](uint32_t &slot, uint32_t &par) {
+                if (++slot == S::kTiles) {
+                    slot = 0;
+                    par ^= 1;
+                }
+            };
+            step(v_slot, v_par);  // tiles come K, V, K, V, ...
+            auto wait_k = [&] { return warp_wait(sh, F8 ? &sh.t_ready[k_slot] : &sh.t_full[k_slot], k_par); };
+            auto wait_v = [&] { return warp_wait(sh, &sh.t_ready[v_slot], v_par); };
+            // S = Q K^T; `last`: the unit's last use of the queries
+            auto qk = [&](bool last) {
+                const uint32_t k = t_low + k_slot * (S::kTile >> 4) + (1u << 16);
+                tc::tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         // 16 dims a step: 32 bytes into a 128-byte row, the next 64 dims one box on
-                        const uint32_t off = (ks >> 2) * kBox + (ks & 3) * 32;
-                        tc::mma_f16(tmem + kColS + i * 128, tc::smem_desc(q + off, 16, 1024, tc::kSw128),
-                                    tc::smem_desc(k + off, 16, 1024, tc::kSw128), idesc_s, ks > 0);
+                        const uint32_t off = ((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
+                        mma_ss(col_s, q_low + off, k + off, idesc_s, ks > 0);
                     }
                     tc::mma_commit(&sh.s_full[i]);
-                };
-                auto pv = [&](int i, uint32_t y, bool add) {
-                    const uint32_t v = aT + (y % S::kTiles) * S::kTile;
+                    tc::mma_commit(&sh.t_empty[k_slot]);
+                    if (last) tc::mma_commit(&sh.q_empty);
+                }
+                __syncwarp();
+                step(k_slot, k_par);
+                step(k_slot, k_par);
+            };
+            // O (+)= P V; `last`: O is complete
+            auto pv = [&](bool add, bool last) {
+                const uint32_t v = t_low + v_slot * (S::kTile >> 4) + (static_cast<uint32_t>(kBox >> 4) << 16);
+                tc::tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < kKeys / 16; ++ks)
                         // P: 16 keys = 8 columns of 16-bit pairs; V: two 8-key groups, the next 64 dims one box on
-                        tc::mma_f16_tmem_a(tmem + kColO + i * 128, tmem + kColS + i * 128 + ks * 8,
-                                           tc::smem_desc(v + ks * 2048, kBox, 1024, tc::kSw128), idesc_o, add || ks > 0);
-                };
-                for (uint32_t n = 0; ok; ++n) {
-                    UnitRec &u = sh.unit[n & 1];
-                    ok = wait_or_abort(sh, &sh.u_full[n & 1], (n >> 1) & 1);
-                    if (!ok || u.nblk < 0) break;
-                    const int nblk = u.nblk, tiles = 1 + u.two;
-                    if (nblk > 0) {
-                        ok = (F8 ? wait_or_abort(sh, &sh.q_ready[nq & 1], (nq >> 1) & 1) : wait_or_abort(sh, &sh.q_full, nq & 1)) &&
-                             tile_wait(x, false);
-                        if (!ok) break;
-                        tc::tc_fence_after();
-                        for (int i = 0; i < tiles; ++i) qk(i, x);
-                        tc::mma_commit(&sh.t_empty[x % S::kTiles]);
-                        if (nblk == 1) tc::mma_commit(&sh.q_empty);
-                        for (int j = 0; j < nblk && ok; ++j) {
-                            const uint32_t yk = x + 2, yv = x + 1;  // K of block j + 1, V of block j
-                            for (int i = 0; i < tiles; ++i) {
-                                if (j == 0 && n_o[i] > 0) ok = wait_or_abort(sh, &sh.o_free[i], (n_o[i] - 1) & 1);
-                                ok = ok && wait_or_abort(sh, &sh.p_full[i], n_p[i] & 1) && (i > 0 || tile_wait(yv, true));
-                                if (!ok) break;
-                                ++n_p[i];
-                                tc::tc_fence_after();
-                                pv(i, yv, j > 0);
-                                if (i == tiles - 1) tc::mma_commit(&sh.t_empty[yv % S::kTiles]);
-                                if (j == nblk - 1) {
-                                    tc::mma_commit(&sh.o_full[i]);
-                                    ++n_o[i];
-                                    continue;
-                                }
-                                if (i == 0) {
-                                    ok = tile_wait(yk, false);
-                                    if (!ok) break;
-                                    tc::tc_fence_after();
-                                }
-                                qk(i, yk);
-                                if (i == tiles - 1) {
-                                    tc::mma_commit(&sh.t_empty[yk % S::kTiles]);
-                                    if (j == nblk - 2) tc::mma_commit(&sh.q_empty);
-                                }
-                            }
-                            x += 2;
-                        }
-                        ++nq;
-                    }
-                    if (ok) tc::mbar_arrive(&sh.u_empty[n & 1]);
+                        mma_ts(col_o, col_s + ks * 8, v + ks * (2048 >> 4), idesc_o, ks > 0 || add);
+                    if (last) tc::mma_commit(&sh.o_full[i]);
+                    tc::mma_commit(&sh.t_empty[v_slot]);
                 }
-                // every issued product completes before tensor memory is released
-                tc::mma_commit(&sh.drain);
-                tc::mbar_wait(&sh.drain, 0);
+                __syncwarp();
+                step(v_slot, v_par);
+                step(v_slot, v_par);
+            };
+            for (uint32_t n = 0; ok; ++n) {
+                UnitRec &u = sh.unit[n & 1];
+                ok = warp_wait(sh, &sh.u_full[n & 1], (n >> 1) & 1);
+                if (!ok || u.nblk < 0) break;
+                const int nblk = u.nblk;
+                if (i == 0 || u.two) {
+                    if (nblk > 0)
+                        ok = (F8 ? warp_wait(sh, &sh.q_ready[nq & 1], (nq >> 1) & 1) : warp_wait(sh, &sh.q_full, nq & 1)) &&
+                             wait_k();
+                    if (!ok) break;
+                    if (nblk > 0) qk(nblk == 1);
+                    for (int j = 0; j < nblk; ++j) {
+                        const bool last = j == nblk - 1;
+                        ok = wait_v() && (j > 0 || n_o == 0 || warp_wait(sh, &sh.o_free[i], (n_o - 1) & 1)) &&
+                             warp_wait(sh, &sh.p_full[i], n_p & 1);
+                        if (!ok) break;
+                        ++n_p;
+                        pv(j > 0, last);
+                        if (last) {
+                            ++n_o;
+                            break;
+                        }
+                        ok = wait_k();
+                        if (!ok) break;
+                        qk(j == nblk - 2);
+                    }
+                } else if (nblk > 0) {
+                    // no second tile: its issuer only lets the pages go
+                    ok = F8 ? warp_wait(sh, &sh.q_ready[nq & 1], (nq >> 1) & 1) : warp_wait(sh, &sh.q_full, nq & 1);
+                    if (ok && lane == 0) tc::mbar_arrive(&sh.q_empty);
+                    for (int j = 0; j < nblk && ok; ++j) {
+                        ok = wait_k() && wait_v();
+                        if (ok && lane == 0) {
+                            tc::mbar_arrive(&sh.t_empty[k_slot]);
+                            tc::mbar_arrive(&sh.t_empty[v_slot]);
+                        }
+                        for (int r = 0; r < 2; ++r) {
+                            step(k_slot, k_par);
+                            step(v_slot, v_par);
+                        }
+                    }
+                }
+                if (!ok) break;
+                if (nblk > 0) ++nq;
+                warp_arrive(&sh.u_empty[n & 1], lane);
             }
+            // every issued product completes before tensor memory is released
+            if (elect_one()) tc::mma_commit(&sh.drain[i]);
+            __syncwarp();
+            tc::mbar_wait(&sh.drain[i], 0);
         } else if (warp == kWarpSched) {
             // ---------------------------------------------- units, page lists
             const ChunkPair *pairs = reinterpret_cast<const ChunkPair *>(t.ws + t.lay.pairs);
@@ -889,9 +915,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     u.qrow0 = qrow0;
                     u.qrow_end = qrow_end;
                     u.pieces = pr.pieces;
-                    u.part0 = h * hd->head_parts + pr.part0;
-                    u.part = u.part0 + piece;
-                    u.ticket = 2 * (h * n_pairs + lo);
+                    u.part = h * hd->head_parts + pr.part0 + piece;
                     u.bt_row = table_row;
                     u.marked = 0;
                     id = static_cast<int32_t>(gridDim.x) + atomicAdd(&hd->next_unit, 1);
@@ -907,6 +931,70 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     tc::tc_fence_after();
     if (threadIdx.x == 0 && aborted(sh)) atomicOr(&hd->status, 1);
     if (warp == kWarpMma) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the pieces of split pairs: one warp per query row, a lane per D / 32
+// dims, in piece order.  The pieces' loads do not depend on one another, so a
+// row costs about one memory latency however many pieces it has; joined by the
+// last piece's softmax warps instead, thread by thread, the rows of 10 pieces
+// took 150 us.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ TcArgs t) {
+    tc::pdl_wait();
+    const ChunkArgs &a = t.a;
+    const ChunkHeader *hd = reinterpret_cast<const ChunkHeader *>(t.ws + t.lay.header);
+    const ChunkPair *pairs = reinterpret_cast<const ChunkPair *>(t.ws + t.lay.pairs);
+    const int32_t *splits = reinterpret_cast<const int32_t *>(t.ws + t.lay.splits);
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = static_cast<int64_t>(hd->n_splits) * a.Hkv * 256;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+    constexpr int kPer = D / 32;
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); k < rows; k += step) {
+        const int r = static_cast<int>(k & 255);
+        const int h = static_cast<int>((k >> 8) % a.Hkv);
+        const ChunkPair pr = pairs[splits[(k >> 8) / a.Hkv]];
+        const int j = (r >> 7) * t.lay.tt + (r & 127) / t.G, g = (r & 127) % t.G;
+        if ((r & 127) >= t.lay.tt * t.G || j >= pr.nt) continue;
+        const int64_t row0 = (static_cast<int64_t>(h) * hd->head_parts + pr.part0) * 256 + r;
+        const float2 *stats = reinterpret_cast<const float2 *>(t.ws + t.lay.stats) + row0;
+        // lane l holds pieces l and l + 32
+        const float2 none = make_float2(-INFINITY, 0.f);
+        const float2 s0 = lane < pr.pieces ? stats[lane * 256] : none;
+        const float2 s1 = lane + 32 < pr.pieces ? stats[(lane + 32) * 256] : none;
+        float M = fmaxf(s0.x, s1.x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        const float w0 = s0.x == -INFINITY ? 0.f : tc::ex2(s0.x - M), w1 = s1.x == -INFINITY ? 0.f : tc::ex2(s1.x - M);
+        float L = (w0 == 0.f ? 0.f : s0.y * w0) + (w1 == 0.f ? 0.f : s1.y * w1);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+        float o[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+        const float *src = reinterpret_cast<const float *>(t.ws + t.lay.partials) + row0 * D + lane * kPer;
+#pragma unroll 8
+        for (int p = 0; p < pr.pieces; ++p) {
+            float x[kPer];
+            if (kPer == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(src + static_cast<int64_t>(p) * 256 * D);
+            else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(src + static_cast<int64_t>(p) * 256 * D);
+            const float w = __shfl_sync(0xffffffffu, p < 32 ? w0 : w1, p & 31);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) o[i] = fmaf(x[i], w, o[i]);
+        }
+        const float f = M == -INFINITY ? 0.f : a.v_scale / L;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + static_cast<int64_t>(pr.tok0 + j) * a.o_s0 +
+                             static_cast<int64_t>(h * t.G + g) * a.o_s1;
+        if (a.o_s2 == 1 && (reinterpret_cast<uintptr_t>(out) & 7) == 0) {
+            uint32_t w[kPer / 2];
+#pragma unroll
+            for (int i = 0; i < kPer / 2; ++i) w[i] = pack2(o[2 * i] * f, o[2 * i + 1] * f, true);
+            if (kPer == 4) reinterpret_cast<uint2 *>(out)[lane] = make_uint2(w[0], w[kPer / 2 - 1]);
+            else reinterpret_cast<uint32_t *>(out)[lane] = w[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) out[(lane * kPer + i) * a.o_s2] = __float2bfloat16_rn(o[i] * f);
+        }
+    }
 }
 
 // [rows, heads, D] tensor as a 3-D map: boxes of `dims` dims x `heads_box`
@@ -985,7 +1073,12 @@ cudaError_t launch(const ChunkArgs &a, void *ws, cudaStream_t stream, bool *used
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, F8>, mq, mk, mv, t);
     if (e != cudaSuccess) return e;
-    count_launches(2);
+    cfg.gridDim = dim3(4 * p.ctas);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, chunk_join_kernel<D>, t);
+    if (e != cudaSuccess) return e;
+    count_launches(3);
     *used = true;
     return cudaSuccess;
 }
