@@ -11,10 +11,11 @@
 //          (running max, sum, unnormalised output) that a kernel behind the
 //          attention kernel joins, in piece order
 //
-// Units are numbered head by head, pairs of the longest sequences first, and
-// within a head the pieces of a sequence's pairs lie next to each other: the
-// CTAs that run at one time read the same pages, so a page comes from HBM
-// once per head and from L2 for the other pairs.
+// Units are numbered sequence by sequence, the longest first, and within a
+// sequence head by head: CTAs claim them in that order, so the units that are
+// claimed last are short ones, and the pairs that run at one time read the
+// same pages, so a page comes from HBM once per head and from L2 for the
+// other pairs.
 #pragma once
 
 #include <stdint.h>
@@ -28,10 +29,9 @@ struct ChunkHeader {
     int32_t next_unit;  // units claimed beyond the first one of each CTA
     int32_t n_pairs;
     int32_t n_units;    // of all heads
-    int32_t head_units; // of one head
     int32_t head_parts; // partial slots of one head
     int32_t n_splits;   // pairs in more than one piece
-    int32_t reserved[57];
+    int32_t reserved[58];
 };
 static_assert(sizeof(ChunkHeader) == 256, "header is one 256-byte line");
 
@@ -40,12 +40,15 @@ struct ChunkPair {
     int32_t i0;      // first token of the pair within its chunk
     int32_t nt;      // tokens
     int32_t cost;    // key blocks expected
-    int32_t unit0;   // first unit within a head
+    int32_t unit0;   // first unit within a head, over all sequences
     int32_t pieces;
     int32_t part0;   // first partial slot within a head (split pairs)
     int32_t tok0;    // first query token
+    int32_t seq0;    // unit0 of the sequence's first pair
+    int32_t seq_units;  // units of the sequence within a head
+    int32_t reserved[2];
 };
-static_assert(sizeof(ChunkPair) == 32, "pair record is 32 bytes");
+static_assert(sizeof(ChunkPair) == 48, "pair record is 48 bytes");
 
 constexpr int kChunkMaxParts = 608;  // partial slots: four pieces per SM of a 152-SM device
 

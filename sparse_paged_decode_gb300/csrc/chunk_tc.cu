@@ -107,7 +107,7 @@ struct Shared {
     uint64_t q_full, q_empty, q_ready[2];
     uint64_t t_full[4], t_empty[4], t_ready[4];
     uint64_t r_full[3], r_empty[3];
-    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];  // by tile; P by halves of a block's keys
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
@@ -136,6 +136,54 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The same, and the largest of the 32 values (a NaN among them is passed over).
+__device__ __forceinline__ float tmem_ld32_max(uint32_t taddr, float *v) {
+    uint32_t r[32], top;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(top)
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+    return __uint_as_float(top);
+}
+
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// Pairs of fp32 in one 64-bit register: two fused multiply-adds, or sums, to
+// an instruction, each rounded as the single ones are.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+    return x;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t x;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
+    return x;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t x;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+    return x;
 }
 
 // Matrix descriptors of the 128-byte-swizzled operands (128 rows or keys of
@@ -301,7 +349,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             tc::mbar_init(&sh.u_empty[i], kUnitReleases);
             tc::mbar_init(&sh.q_ready[i], 4);
             tc::mbar_init(&sh.s_full[i], 1);
-            tc::mbar_init(&sh.p_full[i], 4);
+            tc::mbar_init(&sh.p_full[i][0], 4);
+            tc::mbar_init(&sh.p_full[i][1], 4);
             tc::mbar_init(&sh.o_full[i], 1);
             tc::mbar_init(&sh.o_free[i], 4);
         }
@@ -381,9 +430,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 if (!ok) break;
                 ++n_s;
                 tc::tc_fence_after();
-                float s[kKeys];
+                float s[kKeys], top[4];
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) tmem_ld32(col_s + ch * 32, s + ch * 32);
+                for (int ch = 0; ch < 4; ++ch) top[ch] = tmem_ld32_max(col_s + ch * 32, s + ch * 32);
                 const int kb = u.kb[j];
                 int left = lim - kb * kKeys;  // keys of the block that the row reads
                 if (u.mixed) {
@@ -395,17 +444,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 }
                 seen |= left > 0;
                 tc::tmem_wait_ld();
+                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 if (left < kKeys) {
+                    mx = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < kKeys; ++i)
-                        if (i >= left) s[i] = -INFINITY;
+                    for (int i = 0; i < kKeys; ++i) {
+                        s[i] = i < left ? s[i] : -INFINITY;
+                        mx = fmaxf(mx, s[i]);
+                    }
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < kKeys; i += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[i + k]), s[i + 4 + k]);
-                const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const float bm = mx * c;
                 // raise the offset if the block's maximum runs more than
                 // 2^kRaise above it (or the row had none yet)
                 float alpha = 1.f;
@@ -427,24 +475,30 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     }
                 }
                 const float m_eff = (m_run == -INFINITY) ? 0.f : m_run;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t c2 = pair(c, c), m2 = pair(-m_eff, -m_eff);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t pk[32];
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float p0 = tc::ex2(fmaf(s[half * 64 + 2 * i], c, -m_eff));
-                        const float p1 = tc::ex2(fmaf(s[half * 64 + 2 * i + 1], c, -m_eff));
-                        sum[i & 1] += p0;
-                        sum[2 + (i & 1)] += p1;
+                    for (int i = 0; i < 16; ++i) {
+                        float x0, x1;
+                        unpair(fma2(pair(s[ch * 32 + 2 * i], s[ch * 32 + 2 * i + 1]), c2, m2), x0, x1);
+                        const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
+                        sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
                         pk[i] = pack2(p0, p1, kBf16);
                     }
-                    tc::tmem_st32u(col_s + half * 32, pk);
+                    tmem_st16u(col_s + ch * 16, pk);
+                    if (ch & 1) {
+                        // half of the keys: their product need not wait for the others'
+                        tc::tmem_wait_st();
+                        tc::tc_fence_before();
+                        warp_arrive(&sh.p_full[tile][ch >> 1], lane);
+                    }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tc::tmem_wait_st();
-                tc::tc_fence_before();
-                warp_arrive(&sh.p_full[tile], lane);
+                float l0, l1;
+                unpair(add2(sum[0], sum[1]), l0, l1);
+                l += l0 + l1;
             }
             if (!ok) break;
             // a row that reads keys whose logits are all -inf (or NaN) has no
@@ -584,14 +638,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                                 w[ch] = *reinterpret_cast<const uint4 *>(
                                     src + ((ch ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4));
                             if (kv == 1 && scrub) {
+                                uint32_t bad = 0;  // bit 7 of a byte: 127 + 1, a NaN
 #pragma unroll
                                 for (int ch = 0; ch < D / 16; ++ch) {
-                                    uint32_t *wp = reinterpret_cast<uint32_t *>(&w[ch]);
+                                    const uint32_t *wp = reinterpret_cast<const uint32_t *>(&w[ch]);
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const uint32_t bad = __vcmpeq4(wp[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);  // NaN bytes
-                                        mark |= bad != 0 && !unread;
-                                        wp[i] = unread ? 0u : wp[i] & ~bad;
+                                    for (int i = 0; i < 4; ++i) bad |= (wp[i] & 0x7f7f7f7fu) + 0x01010101u;
+                                }
+                                mark = (bad & 0x80808080u) != 0 && !unread;
+                                if (unread || mark) {
+#pragma unroll
+                                    for (int ch = 0; ch < D / 16; ++ch) {
+                                        uint32_t *wp = reinterpret_cast<uint32_t *>(&w[ch]);
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i)
+                                            wp[i] = unread ? 0u : wp[i] & ~__vcmpeq4(wp[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
                                     }
                                 }
                             }
@@ -621,22 +682,34 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                             ok = warp_wait(sh, &sh.t_full[slot], (x / S::kTiles) & 1);
                             if (!ok) break;
                             if (scrub) {
+                                uint32_t bad = 0;  // bit 15 of a half: exponent 255 + 1
+                                if (!unread) {
 #pragma unroll
-                                for (int b = 0; b < S::kBoxes; ++b)
-#pragma unroll 2
-                                    for (int ch = 0; ch < 8; ++ch) {
-                                        uint4 *at = reinterpret_cast<uint4 *>(dst + b * kBox + ((ch ^ (row & 7)) << 4));
-                                        uint4 w = *at;
-                                        uint32_t *wp = reinterpret_cast<uint32_t *>(&w);
-                                        bool change = unread;
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i) {
-                                            if (unread) { wp[i] = 0; continue; }
-                                            if (!finite_bits(wp[i], true)) { wp[i] &= 0xffff0000u; change = mark = true; }
-                                            if (!finite_bits(wp[i] >> 16, true)) { wp[i] &= 0xffffu; change = mark = true; }
+                                    for (int b = 0; b < S::kBoxes; ++b)
+#pragma unroll 4
+                                        for (int ch = 0; ch < 8; ++ch) {
+                                            const uint4 w = *reinterpret_cast<const uint4 *>(dst + b * kBox + ((ch ^ (row & 7)) << 4));
+                                            bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                                                   ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
                                         }
-                                        if (change) *at = w;
-                                    }
+                                }
+                                mark = (bad & 0x80008000u) != 0;
+                                if (unread || mark) {
+#pragma unroll
+                                    for (int b = 0; b < S::kBoxes; ++b)
+#pragma unroll 2
+                                        for (int ch = 0; ch < 8; ++ch) {
+                                            uint4 *at = reinterpret_cast<uint4 *>(dst + b * kBox + ((ch ^ (row & 7)) << 4));
+                                            uint4 w = unread ? make_uint4(0, 0, 0, 0) : *at;
+                                            uint32_t *wp = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+                                            for (int i = 0; i < 4; ++i) {
+                                                if (!finite_bits(wp[i], true)) wp[i] &= 0xffff0000u;
+                                                if (!finite_bits(wp[i] >> 16, true)) wp[i] &= 0xffffu;
+                                            }
+                                            *at = w;
+                                        }
+                                }
                                 if (mark) {
                                     atomicOr(&u.marks[kb >> 5], 1u << (kb & 31));
                                     *reinterpret_cast<volatile int32_t *>(&u.marked) = 1;
@@ -750,21 +823,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 step(k_slot, k_par);
                 step(k_slot, k_par);
             };
-            // O (+)= P V; `last`: O is complete
-            auto pv = [&](bool add, bool last) {
+            // O (+)= P V over one half of the block's keys; `last`: O is complete
+            auto pv = [&](int half, bool add, bool last) {
                 const uint32_t v = t_low + v_slot * (S::kTile >> 4) + (static_cast<uint32_t>(kBox >> 4) << 16);
                 tc::tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < kKeys / 16; ++ks)
+                    for (int k = 0; k < kKeys / 32; ++k) {
                         // P: 16 keys = 8 columns of 16-bit pairs; V: two 8-key groups, the next 64 dims one box on
+                        const int ks = half * (kKeys / 32) + k;
                         mma_ts(col_o, col_s + ks * 8, v + ks * (2048 >> 4), idesc_o, ks > 0 || add);
-                    if (last) tc::mma_commit(&sh.o_full[i]);
-                    tc::mma_commit(&sh.t_empty[v_slot]);
+                    }
+                    if (half == 1 && last) tc::mma_commit(&sh.o_full[i]);
+                    if (half == 1) tc::mma_commit(&sh.t_empty[v_slot]);
                 }
                 __syncwarp();
-                step(v_slot, v_par);
-                step(v_slot, v_par);
             };
             for (uint32_t n = 0; ok; ++n) {
                 UnitRec &u = sh.unit[n & 1];
@@ -780,10 +853,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     for (int j = 0; j < nblk; ++j) {
                         const bool last = j == nblk - 1;
                         ok = wait_v() && (j > 0 || n_o == 0 || warp_wait(sh, &sh.o_free[i], (n_o - 1) & 1)) &&
-                             warp_wait(sh, &sh.p_full[i], n_p & 1);
+                             warp_wait(sh, &sh.p_full[i][0], n_p & 1);
+                        if (!ok) break;
+                        pv(0, j > 0, last);
+                        ok = warp_wait(sh, &sh.p_full[i][1], n_p & 1);
                         if (!ok) break;
                         ++n_p;
-                        pv(j > 0, last);
+                        pv(1, true, last);
+                        step(v_slot, v_par);
+                        step(v_slot, v_par);
                         if (last) {
                             ++n_o;
                             break;
@@ -819,7 +897,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         } else if (warp == kWarpSched) {
             // ---------------------------------------------- units, page lists
             const ChunkPair *pairs = reinterpret_cast<const ChunkPair *>(t.ws + t.lay.pairs);
-            const int32_t n_units = hd->n_units, head_units = hd->head_units, n_pairs = hd->n_pairs;
+            const int32_t n_units = hd->n_units, n_pairs = hd->n_pairs;
+            auto pair_of = [&](int32_t v) {  // the pair whose units of one head hold v
+                int lo = 0, hi = n_pairs;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (pairs[mid].unit0 <= v) lo = mid; else hi = mid;
+                }
+                return lo;
+            };
             int32_t id = blockIdx.x;
             for (uint32_t n = 0;; ++n) {
                 UnitRec &u = sh.unit[n & 1];
@@ -832,13 +918,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     }
                     break;
                 }
-                const int h = id / head_units, v = id % head_units;
-                int lo = 0, hi = n_pairs;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (pairs[mid].unit0 <= v) lo = mid; else hi = mid;
-                }
-                const ChunkPair pr = pairs[lo];
+                // sequence, then head, then the unit among the sequence's
+                const ChunkPair *some = pairs + pair_of(id / a.Hkv);
+                const int32_t rest = id - some->seq0 * a.Hkv;
+                const int h = rest / some->seq_units, v = some->seq0 + rest % some->seq_units;
+                const ChunkPair pr = pairs[pair_of(v)];
                 const int piece = v - pr.unit0;
                 const int32_t table_row = a.sid[pr.b * a.sid_s0];
                 const bool in_table = table_row >= 0 && table_row < a.R;
