@@ -47,6 +47,7 @@
 #include <cuda_fp16.h>
 
 #include "chunk_plan.cuh"
+#include "f32x2.cuh"
 #include "spd_dispatch.h"
 #include "spd_internal.cuh"
 #include "tc_ptx.cuh"
@@ -163,27 +164,6 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
-}
-
-// Pairs of fp32 in one 64-bit register: two fused multiply-adds, or sums, to
-// an instruction, each rounded as the single ones are.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t x;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
-    return x;
-}
-__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t x;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
-    return x;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t x;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
-    return x;
 }
 
 // Matrix descriptors of the 128-byte-swizzled operands (128 rows or keys of

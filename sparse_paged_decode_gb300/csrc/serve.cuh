@@ -50,6 +50,7 @@ struct StoreArgs {
 };
 
 cudaError_t launch_store_generic(const StoreArgs &a, cudaStream_t stream);
+cudaError_t launch_store_vec(const StoreArgs &a, cudaStream_t stream, bool *used);
 cudaError_t dispatch_store(const StoreArgs &a, cudaStream_t stream);
 
 struct ChunkArgs {

@@ -19,7 +19,14 @@ int set_serve_policy(int stage, int policy) {
     return old;
 }
 
-cudaError_t dispatch_store(const StoreArgs &a, cudaStream_t stream) { return launch_store_generic(a, stream); }
+cudaError_t dispatch_store(const StoreArgs &a, cudaStream_t stream) {
+    if (g_serve_policy[1] == 0) {
+        bool used = false;
+        const cudaError_t e = launch_store_vec(a, stream, &used);
+        if (e != cudaSuccess || used) return e;
+    }
+    return launch_store_generic(a, stream);
+}
 
 cudaError_t dispatch_chunk(const ChunkArgs &a, void *ws, size_t ws_bytes, cudaStream_t stream) {
     (void)ws_bytes;
