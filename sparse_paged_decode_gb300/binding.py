@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -95,13 +96,15 @@ def _load():
     L.msa_prefill_block_score.restype = None
     L.spd_prefill_workspace_bytes.argtypes = [ctypes.c_int64] * 3
     L.spd_prefill_workspace_bytes.restype = sz
-    L.paged_assign_slots.argtypes = [P] * 5 + [i32] * 3 + [P] * 8 + [vp]
+    # the serving-step calls take their descriptors as packed bytes (_pack)
+    B = ctypes.c_char_p
+    L.paged_assign_slots.argtypes = [B] * 5 + [i32] * 3 + [B] * 8 + [vp]
     L.paged_assign_slots.restype = None
-    L.paged_norm_rope_store.argtypes = [P] * 11 + [f32, i32, i32, f32, f32, vp]
+    L.paged_norm_rope_store.argtypes = [B] * 11 + [f32, i32, i32, f32, f32, vp]
     L.paged_norm_rope_store.restype = None
-    L.paged_prefill_attention.argtypes = [P] * 9 + [f32, i32, f32, f32, vp, sz, vp]
+    L.paged_prefill_attention.argtypes = [B] * 9 + [f32, i32, f32, f32, vp, sz, vp]
     L.paged_prefill_attention.restype = None
-    L.paged_sparse_prefill_attention.argtypes = [P] * 9 + [i32, P, P, f32, i32, f32, f32, vp, sz, vp]
+    L.paged_sparse_prefill_attention.argtypes = [B] * 9 + [i32, B, B, f32, i32, f32, f32, vp, sz, vp]
     L.paged_sparse_prefill_attention.restype = None
     L.spd_prefill_attention_workspace_bytes.argtypes = [ctypes.c_int64] * 7
     L.spd_prefill_attention_workspace_bytes.restype = sz
@@ -161,6 +164,47 @@ def _check():
     code = lib.spd_last_error(buf, 512)
     if code != 0:
         raise SpdError(code, buf.value.decode(errors="replace"))
+
+
+_PACK = struct.Struct("=Qii4q4q").pack
+assert struct.calcsize("=Qii4q4q") == ctypes.sizeof(SpdTensor)
+_ZEROS = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+
+
+def _pack(t: Optional[torch.Tensor], name: str, device: int) -> Optional[bytes]:
+    """The descriptor of ``t`` as the bytes of an ``spd_tensor``.
+
+    The calls of a serving step pass up to sixteen tensors each and run for a
+    few microseconds on the GPU, so what a descriptor costs shows: about 1 us
+    like this, 3 us as a ctypes structure that is filled field by field."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s: dtype %s is not supported by libspd" % (name, t.dtype))
+    shape = t.shape
+    n = len(shape)
+    if n > 4:
+        raise ValueError("%s has more than 4 dims" % name)
+    if t.get_device() != device and t.numel() > 0:
+        raise ValueError("%s must be a CUDA tensor on the current device" % name)
+    zeros = _ZEROS[n]
+    return _PACK(t.data_ptr(), code, n, *shape, *zeros, *t.stride(), *zeros)
+
+
+def _place(stream):
+    """The current device's index and the raw stream of a call."""
+    device = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    if stream is None:
+        return device, (torch._C._cuda_getCurrentRawStream(device) if device >= 0 else None)
+    return device, _stream(stream)
+
+
+def _check_fast():
+    if lib.spd_last_error(None, 0) != 0:
+        _check()
 
 
 def msa_block_score(q_idx, k_idx_cache, block_table, seq_lens, req_idx, block_size, scores,
@@ -244,13 +288,14 @@ def paged_assign_slots(new_lens, prefix_lens, slot_ids, free_pages, free_count, 
     """Slots of a serving step: grow ``block_table`` [R, NB] in place from the
     end of ``free_pages`` and fill the offsets, lengths and every token's row,
     length and slot from the requests' ``new_lens`` and ``prefix_lens``."""
+    d, raw = _place(stream)
     lib.paged_assign_slots(
-        _desc(new_lens, "new_lens"), _desc(prefix_lens, "prefix_lens"), _desc(slot_ids, "slot_ids"),
-        _desc(free_pages, "free_pages"), _desc(free_count, "free_count"), int(n_pages), int(block_size),
-        int(block_size_q), _desc(block_table, "block_table"), _desc(cu_seqlens, "cu_seqlens"),
-        _desc(cu_seqblocks_q, "cu_seqblocks_q"), _desc(seq_lens, "seq_lens"), _desc(req_idx, "req_idx"),
-        _desc(token_lens, "token_lens"), _desc(slots, "slots"), _desc(free_left, "free_left"), _stream(stream))
-    _check()
+        _pack(new_lens, "new_lens", d), _pack(prefix_lens, "prefix_lens", d), _pack(slot_ids, "slot_ids", d),
+        _pack(free_pages, "free_pages", d), _pack(free_count, "free_count", d), n_pages, block_size, block_size_q,
+        _pack(block_table, "block_table", d), _pack(cu_seqlens, "cu_seqlens", d),
+        _pack(cu_seqblocks_q, "cu_seqblocks_q", d), _pack(seq_lens, "seq_lens", d), _pack(req_idx, "req_idx", d),
+        _pack(token_lens, "token_lens", d), _pack(slots, "slots", d), _pack(free_left, "free_left", d), raw)
+    _check_fast()
 
 
 def paged_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, token_lens, slots, q_out, k_cache, v_cache, eps,
@@ -259,12 +304,13 @@ def paged_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, token_lens, slot
     positions (``cos_sin`` [M, Rd]) of q and k: fill ``q_out`` [T, Hq, D] and
     write k and v into ``slots`` of the caches.  ``v`` and ``v_cache`` may be
     None together (index queries and keys)."""
+    d, raw = _place(stream)
     lib.paged_norm_rope_store(
-        _desc(q, "q"), _desc(k, "k"), _desc(v, "v"), _desc(q_weight, "q_weight"), _desc(k_weight, "k_weight"),
-        _desc(cos_sin, "cos_sin"), _desc(token_lens, "token_lens"), _desc(slots, "slots"), _desc(q_out, "q_out"),
-        _desc(k_cache, "k_cache"), _desc(v_cache, "v_cache"), float(eps), 1 if interleaved else 0, int(block_size),
-        float(k_scale), float(v_scale), _stream(stream))
-    _check()
+        _pack(q, "q", d), _pack(k, "k", d), _pack(v, "v", d), _pack(q_weight, "q_weight", d),
+        _pack(k_weight, "k_weight", d), _pack(cos_sin, "cos_sin", d), _pack(token_lens, "token_lens", d),
+        _pack(slots, "slots", d), _pack(q_out, "q_out", d), _pack(k_cache, "k_cache", d), _pack(v_cache, "v_cache", d),
+        eps, 1 if interleaved else 0, block_size, k_scale, v_scale, raw)
+    _check_fast()
 
 
 def paged_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqlens, seq_lens, prefix_lens, out,
@@ -274,13 +320,13 @@ def paged_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqle
 
     ``workspace`` is a CUDA uint8 tensor of at least
     ``prefill_attention_workspace_bytes`` bytes."""
-    ws_ptr, ws_bytes = _workspace(workspace)
+    d, raw = _place(stream)
     lib.paged_prefill_attention(
-        _desc(q, "q"), _desc(k_cache, "k_cache"), _desc(v_cache, "v_cache"), _desc(block_table, "block_table"),
-        _desc(slot_ids, "slot_ids"), _desc(cu_seqlens, "cu_seqlens"), _desc(seq_lens, "seq_lens"),
-        _desc(prefix_lens, "prefix_lens"), _desc(out, "out"), float(sm_scale), int(block_size), float(k_scale),
-        float(v_scale), ws_ptr, ws_bytes, _stream(stream))
-    _check()
+        _pack(q, "q", d), _pack(k_cache, "k_cache", d), _pack(v_cache, "v_cache", d),
+        _pack(block_table, "block_table", d), _pack(slot_ids, "slot_ids", d), _pack(cu_seqlens, "cu_seqlens", d),
+        _pack(seq_lens, "seq_lens", d), _pack(prefix_lens, "prefix_lens", d), _pack(out, "out", d), sm_scale,
+        block_size, k_scale, v_scale, *_scratch(workspace, d), raw)
+    _check_fast()
 
 
 def paged_sparse_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqlens, seq_lens, prefix_lens,
@@ -289,14 +335,22 @@ def paged_sparse_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, c
     """The same over the key blocks that ``topk_idx`` [Hkv, rows, K] lists for
     each query block of ``block_size_q`` tokens (the rows that
     msa_prefill_block_score writes)."""
-    ws_ptr, ws_bytes = _workspace(workspace)
+    d, raw = _place(stream)
     lib.paged_sparse_prefill_attention(
-        _desc(q, "q"), _desc(k_cache, "k_cache"), _desc(v_cache, "v_cache"), _desc(block_table, "block_table"),
-        _desc(slot_ids, "slot_ids"), _desc(cu_seqlens, "cu_seqlens"), _desc(seq_lens, "seq_lens"),
-        _desc(prefix_lens, "prefix_lens"), _desc(topk_idx, "topk_idx"), int(block_size_q),
-        _desc(cu_seqblocks_q, "cu_seqblocks_q"), _desc(out, "out"), float(sm_scale), int(block_size), float(k_scale),
-        float(v_scale), ws_ptr, ws_bytes, _stream(stream))
-    _check()
+        _pack(q, "q", d), _pack(k_cache, "k_cache", d), _pack(v_cache, "v_cache", d),
+        _pack(block_table, "block_table", d), _pack(slot_ids, "slot_ids", d), _pack(cu_seqlens, "cu_seqlens", d),
+        _pack(seq_lens, "seq_lens", d), _pack(prefix_lens, "prefix_lens", d), _pack(topk_idx, "topk_idx", d),
+        block_size_q, _pack(cu_seqblocks_q, "cu_seqblocks_q", d), _pack(out, "out", d), sm_scale, block_size, k_scale,
+        v_scale, *_scratch(workspace, d), raw)
+    _check_fast()
+
+
+def _scratch(ws, device):
+    if ws is None:
+        return None, 0
+    if not isinstance(ws, torch.Tensor) or ws.get_device() != device:
+        raise TypeError("workspace must be a CUDA tensor on the current device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def prefill_attention_workspace_bytes(total_q: int, Hq: int, Hkv: int, D: int, B: int, NB: int, n_rows: int = 0) -> int:

@@ -4,8 +4,16 @@ device addresses; a call that passes validation is only enqueued, so without
 a GPU it reports SPD_ERR_CUDA."""
 import pytest
 
+import ctypes
+
 from test_abi_host import (BF16, E4M3, F16, F32, I32, SPD_ERR_ALIASING, SPD_ERR_CUDA, SPD_ERR_INVALID_ARGUMENT,
                            SPD_ERR_UNSUPPORTED, SPD_ERR_WORKSPACE, SPD_OK, Fake, status)
+
+
+def raw(fake):
+    """The descriptor as the binding passes it to these calls."""
+    return None if fake is None else ctypes.string_at(ctypes.addressof(fake.d), ctypes.sizeof(fake.d))
+
 
 INVALID, UNSUPPORTED, ALIASING, WORKSPACE = SPD_ERR_INVALID_ARGUMENT, SPD_ERR_UNSUPPORTED, SPD_ERR_ALIASING, SPD_ERR_WORKSPACE
 
@@ -27,7 +35,7 @@ def assign_call(spd, n_pages=64, block_size=128, bsq=4, **over):
              bt=Fake((4, 16), I32), cu=Fake((B + 1,), I32), cub=Fake((B + 1,), I32), sl=Fake((B,), I32),
              req=Fake((T,), I32), tl=Fake((T,), I32), slots=Fake((T,), I32), left=Fake((1,), I32))
     t.update(over)
-    r = {k: (v.ref() if v is not None else None) for k, v in t.items()}
+    r = {k: raw(v) for k, v in t.items()}
     spd.lib.paged_assign_slots(r["new"], r["pre"], r["sid"], r["fp"], r["fc"], n_pages, block_size, bsq, r["bt"], r["cu"],
                                r["cub"], r["sl"], r["req"], r["tl"], r["slots"], r["left"], None)
     return status(spd)[0]
@@ -64,7 +72,7 @@ def store_call(spd, T=5, Hq=8, Hkv=2, D=64, P=4, dt=BF16, cache=E4M3, eps=1e-6, 
              wk=Fake((D,), F32), cs=Fake((100, D), F32), tl=Fake((T,), I32), slots=Fake((T,), I32),
              qo=Fake((T, Hq, D), BF16), kc=Fake((P * 128, Hkv, D), cache), vc=Fake((P * 128, Hkv, D), cache))
     t.update(over)
-    r = [t[k].ref() if t[k] is not None else None for k in ("q", "k", "v", "wq", "wk", "cs", "tl", "slots", "qo", "kc", "vc")]
+    r = [raw(t[k]) for k in ("q", "k", "v", "wq", "wk", "cs", "tl", "slots", "qo", "kc", "vc")]
     spd.lib.paged_norm_rope_store(*r, eps, 0, block_size, ks, vs, None)
     return status(spd)[0]
 
@@ -114,7 +122,7 @@ def chunk_call(spd, total_q=10, Hq=8, Hkv=2, D=64, B=2, NB=16, P=8, dt=BF16, cac
              bt=Fake((3, NB), I32), sid=Fake((B,), I32), cu=Fake((B + 1,), I32), sl=Fake((B,), I32), pre=Fake((B,), I32),
              tk=Fake((Hkv, n_rows, K), I32, strides=(0, K, 1)), cub=Fake((B + 1,), I32), out=Fake((total_q, Hq, D), BF16))
     t.update(over)
-    r = {k: (v.ref() if v is not None else None) for k, v in t.items() if k != "ws"}
+    r = {k: raw(v) for k, v in t.items() if k != "ws"}
     need = spd.lib.spd_prefill_attention_workspace_bytes(total_q, Hq, Hkv, D, B, NB, n_rows if sparse else 0)
     ws = Fake((max(need, 1) + 512,), E4M3)
     head = [r[k] for k in ("q", "k", "v", "bt", "sid", "cu", "sl", "pre")]
