@@ -64,26 +64,51 @@ constexpr int kWarpSide = 8, kWarpTma = 12, kWarpMma = 13, kWarpSched = 14, kWar
 constexpr int kBox = 128 * 128;      // 64 dims of 128 rows of a 16-bit type, bytes
 constexpr float kRaise = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
-// registers: 128 a thread at launch; the softmax warpgroups rise to 184, the
-// two others drop to 72
-constexpr uint32_t kRegsSoft = 184, kRegsOther = 72;
+// registers: 128 a thread at launch; the softmax warpgroups rise to 176, the
+// two others drop to 80
+constexpr uint32_t kRegsSoft = 176, kRegsOther = 80;
 static_assert(256 * kRegsSoft + 256 * kRegsOther <= kThreads * 128, "register split");
 constexpr uint32_t kUnitReleases = 8 + 4 + 1 + 2;  // warps that read a unit record
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;         // S_i at 128 i, O_i at 256 + 128 i
 
-template <int D, bool F8>
+// How a cache is multiplied.
+enum Mode {
+    kModeBf16,   // BF16 pages as they are, bf16 queries
+    kModeTerms,  // E4M3: K as it is against two E4M3 terms of each bf16 query, V widened to f16
+    kModeWide    // E4M3: K and V widened to f16, f16 queries
+};
+
+template <int D, Mode M>
 struct Shape {
+    static constexpr bool kF8 = M != kModeBf16;
     static constexpr int kBoxes = D / 64;
     static constexpr int kTileQ = kBoxes * kBox;  // one tile of queries
-    static constexpr int kTile = kBoxes * kBox;   // one 16-bit K or V page
-    static constexpr int kRaw = kKeys * D;        // one E4M3 page
-    static constexpr int kTiles = F8 ? 3 : 4;
-    static constexpr int kRaws = F8 ? 3 : 0;
+    static constexpr int kPage16 = kBoxes * kBox; // a K or V page of 16-bit elements
+    static constexpr int kPage8 = kKeys * D;      // one of E4M3
+    // K pages as the products read them, V pages likewise, and E4M3 pages that wait to be widened
+    static constexpr int kPageK = M == kModeTerms ? kPage8 : kPage16;
+    static constexpr int kKs = M == kModeBf16 ? 2 : (M == kModeTerms ? 3 : 1);
+    static constexpr int kVs = 2;
+    static constexpr int kRs = M == kModeBf16 ? 0 : (M == kModeTerms ? 2 : 3);
     static constexpr int kOffQ = 0;
-    static constexpr int kOffTile = kOffQ + 2 * kTileQ;
-    static constexpr int kOffRaw = kOffTile + kTiles * kTile;
-    static constexpr int kEnd = kOffRaw + kRaws * kRaw;
+    static constexpr int kOffK = kOffQ + 2 * kTileQ;
+    static constexpr int kOffV = kOffK + kKs * kPageK;
+    static constexpr int kOffRaw = kOffV + kVs * kPage16;
+    static constexpr int kEnd = kOffRaw + kRs * kPage8;
+};
+
+// A place in a ring of N slots, and the parity of its present round.
+template <int N>
+struct Ring {
+    uint32_t slot = 0, round = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            ++round;
+        }
+    }
+    __device__ __forceinline__ uint32_t parity() const { return round & 1; }
 };
 
 struct UnitRec {
@@ -105,9 +130,10 @@ struct UnitRec {
 
 struct Shared {
     uint64_t u_full[2], u_empty[2];
-    uint64_t q_full, q_empty, q_ready[2];
-    uint64_t t_full[4], t_empty[4], t_ready[4];
-    uint64_t r_full[3], r_empty[3];
+    uint64_t q_full, q_empty, q_ready[2][2];  // ready: by parity of the units with products, and tile
+    uint64_t k_full[3], k_empty[3];           // K pages for the products
+    uint64_t v_full[2], v_ready[2], v_empty[2];  // V pages: loaded (BF16), widened or scrubbed, read
+    uint64_t r_full[3], r_empty[3];           // E4M3 pages to be widened
     uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];  // by tile; P by halves of a block's keys
     uint64_t drain[2];
     uint32_t tmem_base;
@@ -174,16 +200,27 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
 constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (static_cast<uint32_t>(tc::kSw128) << 29);
 __device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
 
-// D (+)= A B, kind::f16, A and B in shared memory.
+// D (+)= A B, A and B in shared memory: kind::f16, or kind::f8f6f4 (E4M3).
+template <bool kF8>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "mov.b64 a, {%1, %4};\n\t"
-        "mov.b64 b, {%2, %4};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-        "r"(a_low), "r"(b_low), "r"(idesc), "r"(kDescHigh), "r"(add)
-        : "memory");
+    if (kF8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\t"
+            "mov.b64 a, {%1, %4};\n\t"
+            "mov.b64 b, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+            "r"(a_low), "r"(b_low), "r"(idesc), "r"(kDescHigh), "r"(add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\t"
+            "mov.b64 a, {%1, %4};\n\t"
+            "mov.b64 b, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+            "r"(a_low), "r"(b_low), "r"(idesc), "r"(kDescHigh), "r"(add)
+            : "memory");
 }
 
 // D (+)= A B, kind::f16, A in tensor memory.
@@ -254,6 +291,88 @@ __device__ __forceinline__ bool finite_bits(uint32_t x, bool bf16) {
     return (x & e) != e;
 }
 
+// The largest magnitude of one bf16 query row of D dims in its swizzled tile,
+// as the power of two that brings it to [2^top, 2^(top + 1)), and the inverse.
+template <int D>
+__device__ __forceinline__ void row_power(const uint8_t *q, int row, int top, float &up, float &down) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(q + b * kBox + ((ch ^ (row & 7)) << 4));
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+        }
+    const int e = static_cast<int>(max(m & 0xffffu, m >> 16) >> 7);  // biased exponent
+    const int shift = e == 0 ? 0 : min(top - (e - 127), 100);
+    up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+    down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+}
+
+// A bf16 query row to f16, in place, scaled by a power of two (exact for
+// elements within 2^38 of the row's largest); returns the inverse scale.
+template <int D>
+__device__ __forceinline__ float halve_query_row(uint8_t *q, int row) {
+    float up, down;
+    row_power<D>(q, row, 14, up, down);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+#pragma unroll 2
+        for (int ch = 0; ch < 8; ++ch) {
+            uint4 *at = reinterpret_cast<uint4 *>(q + b * kBox + ((ch ^ (row & 7)) << 4));
+            uint4 w = *at;
+            uint32_t *wp = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                wp[i] = tc::f32x2_to_f16x2(__uint_as_float(wp[i] << 16) * up, __uint_as_float(wp[i] & 0xffff0000u) * up);
+            *at = w;
+        }
+    return down;
+}
+
+// A bf16 query row of 128 dims as two E4M3 terms, in place: the row is scaled
+// by a power of two into [128, 256); the first term is its rounding to four
+// bits, the second what is left (four more bits: the sum is exact for elements
+// within 2^9 of the row's largest, and off by at most 2^-17 of that beyond).
+// The first terms take the row's 128 bytes of dims 0-63, the second those of
+// dims 64-127.  Returns the inverse scale.
+__device__ __forceinline__ float split_query_row(uint8_t *q, int row) {
+    float up, down;
+    row_power<128>(q, row, 7, up, down);
+    const uint64_t up2 = pair(up, up);
+    uint32_t second[32];
+#pragma unroll
+    for (int ch = 0; ch < 16; ch += 2) {
+        uint32_t first[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = ch + k;
+            const uint4 w = *reinterpret_cast<const uint4 *>(q + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4));
+            const uint32_t wp[4] = {w.x, w.y, w.z, w.w};
+            uint32_t t0[4], t1[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float lo, hi, l0, h0;
+                unpair(mul2(pair(__uint_as_float(wp[i] << 16), __uint_as_float(wp[i] & 0xffff0000u)), up2), lo, hi);
+                t0[i] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+                tc::e4m3x2_to_f32x2(static_cast<uint16_t>(t0[i]), h0, l0);
+                t1[i] = __nv_cvt_float2_to_fp8x2(make_float2(lo - l0, hi - h0), __NV_SATFINITE, __NV_E4M3);
+            }
+            first[2 * k] = t0[0] | (t0[1] << 16);
+            first[2 * k + 1] = t0[2] | (t0[3] << 16);
+            second[2 * c] = t1[0] | (t1[1] << 16);
+            second[2 * c + 1] = t1[2] | (t1[3] << 16);
+        }
+        // chunk ch / 2 of the first terms lies at or before the chunks read so far
+        *reinterpret_cast<uint4 *>(q + (((ch / 2) ^ (row & 7)) << 4)) = make_uint4(first[0], first[1], first[2], first[3]);
+    }
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch)
+        *reinterpret_cast<uint4 *>(q + kBox + ((ch ^ (row & 7)) << 4)) =
+            make_uint4(second[4 * ch], second[4 * ch + 1], second[4 * ch + 2], second[4 * ch + 3]);
+    return down;
+}
+
 // Elements of the marked blocks' V rows that this row reads (keys below lim, of
 // its own selection where row_bits is given) and that are not finite, added to
 // the row's O in tensor memory, where the products saw zeros in their place.
@@ -310,12 +429,12 @@ __device__ __noinline__ void take_marked(const TcArgs &t, const UnitRec &u, int3
     }
 }
 
-template <int D, bool F8>
+template <int D, Mode M>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TcArgs t) {
-    using S = Shape<D, F8>;
-    constexpr bool kBf16 = !F8;
+    using S = Shape<D, M>;
+    constexpr bool F8 = S::kF8, kBf16 = !F8;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Shared &sh = *reinterpret_cast<Shared *>(smem + S::kEnd);
@@ -327,19 +446,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sh.u_full[i], 1);
             tc::mbar_init(&sh.u_empty[i], kUnitReleases);
-            tc::mbar_init(&sh.q_ready[i], 4);
             tc::mbar_init(&sh.s_full[i], 1);
-            tc::mbar_init(&sh.p_full[i][0], 4);
-            tc::mbar_init(&sh.p_full[i][1], 4);
             tc::mbar_init(&sh.o_full[i], 1);
             tc::mbar_init(&sh.o_free[i], 4);
-        }
-        for (int i = 0; i < 4; ++i) {
-            tc::mbar_init(&sh.t_full[i], 1);
-            tc::mbar_init(&sh.t_empty[i], 2);
-            tc::mbar_init(&sh.t_ready[i], 4);
+            for (int k = 0; k < 2; ++k) {
+                tc::mbar_init(&sh.q_ready[i][k], 4);
+                tc::mbar_init(&sh.p_full[i][k], 4);
+            }
+            tc::mbar_init(&sh.v_full[i], 1);
+            tc::mbar_init(&sh.v_ready[i], 4);
+            tc::mbar_init(&sh.v_empty[i], 2);
         }
         for (int i = 0; i < 3; ++i) {
+            tc::mbar_init(&sh.k_full[i], M == kModeWide ? 4 : 1);  // its widening warps, or the copy
+            tc::mbar_init(&sh.k_empty[i], 2);
             tc::mbar_init(&sh.r_full[i], 1);
             tc::mbar_init(&sh.r_empty[i], 4);
         }
@@ -398,7 +518,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             }
             float c = t.c;
             if (F8 && nblk > 0) {
-                if (!warp_wait(sh, &sh.q_ready[iq & 1], (iq >> 1) & 1)) break;
+                if (!warp_wait(sh, &sh.q_ready[iq & 1][tile], (iq >> 1) & 1)) break;
                 c *= sh.row_factor[iq & 1][tile * kRows + r];
             }
             float m_run = -INFINITY, l = 0.f;
@@ -547,158 +667,137 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         if (warp < kWarpTma) {
             // ------------------------------------------- widen and scrub
             const int row = (warp - kWarpSide) * 32 + lane;  // key of the page; query row of each tile
-            uint32_t x = 0;                                  // 16-bit tiles so far (K, V, K, V, ...)
-            uint32_t nq = 0;                                 // units with products
+            Ring<S::kKs> rk;
+            Ring<S::kVs> rv;
+            Ring<F8 ? S::kRs : 1> rr;
+            uint32_t nq = 0;  // units with products
+            // one E4M3 page of 16-byte chunks w to f16, into the 16-bit page at `page16`
+            auto widen = [&](const uint4 *w, uint8_t *page16) {
+#pragma unroll
+                for (int ch = 0; ch < D / 16; ++ch) {
+                    uint32_t h[8];
+                    const uint32_t *wp = reinterpret_cast<const uint32_t *>(&w[ch]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tc::e4m3x4_to_f16x4(wp[i], h[2 * i], h[2 * i + 1]);
+                    uint8_t *box = page16 + (ch >> 2) * kBox + row * 128;
+                    const int c0 = (2 * ch) & 7;
+                    *reinterpret_cast<uint4 *>(box + ((c0 ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4 *>(box + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+                tc::fence_proxy_async();
+            };
+            auto load_raw = [&](uint4 *w) {
+                const uint8_t *src = smem + S::kOffRaw + rr.slot * S::kPage8 + row * D;
+#pragma unroll
+                for (int ch = 0; ch < D / 16; ++ch)
+                    w[ch] = *reinterpret_cast<const uint4 *>(src + ((ch ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4));
+            };
             for (uint32_t n = 0;; ++n) {
                 UnitRec &u = sh.unit[n & 1];
                 if (!warp_wait(sh, &sh.u_full[n & 1], (n >> 1) & 1) || u.nblk < 0) break;
                 const int nblk = u.nblk;
                 bool ok = true;
                 if (F8 && nblk > 0) {
-                    // queries to f16, in place, scaled by a power of two per row
                     ok = warp_wait(sh, &sh.q_full, nq & 1);
                     if (!ok) break;
                     for (int tile = 0; tile < 1 + u.two; ++tile) {
                         float factor = 1.f;
-                        if (!t.q_f16) {
-                            uint8_t *q = smem + S::kOffQ + tile * S::kTileQ + row * 128;
-                            uint32_t top = 0;
-#pragma unroll
-                            for (int b = 0; b < S::kBoxes; ++b)
-#pragma unroll
-                                for (int ch = 0; ch < 8; ++ch) {
-                                    const uint4 w = *reinterpret_cast<const uint4 *>(q + b * kBox + ((ch ^ (row & 7)) << 4));
-                                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
-                                                                 __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-                                }
-                            const int e = static_cast<int>(max(top & 0xffffu, top >> 16) >> 7);  // biased exponent
-                            const int shift = e == 0 ? 0 : min(14 - (e - 127), 100);
-                            const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-                            factor = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
-#pragma unroll
-                            for (int b = 0; b < S::kBoxes; ++b)
-#pragma unroll 2
-                                for (int ch = 0; ch < 8; ++ch) {
-                                    uint4 *at = reinterpret_cast<uint4 *>(q + b * kBox + ((ch ^ (row & 7)) << 4));
-                                    uint4 w = *at;
-                                    uint32_t *wp = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        wp[i] = tc::f32x2_to_f16x2(__uint_as_float(wp[i] << 16) * up,
-                                                                   __uint_as_float(wp[i] & 0xffff0000u) * up);
-                                    *at = w;
-                                }
-                        }
+                        if (M == kModeTerms) factor = split_query_row(smem + S::kOffQ + tile * S::kTileQ + row * 128, row);
+                        else if (!t.q_f16) factor = halve_query_row<D>(smem + S::kOffQ + tile * S::kTileQ + row * 128, row);
                         sh.row_factor[nq & 1][tile * kRows + row] = factor;
+                        tc::fence_proxy_async();
+                        warp_arrive(&sh.q_ready[nq & 1][tile], lane);
                     }
-                    tc::fence_proxy_async();
-                    warp_arrive(&sh.q_ready[nq & 1], lane);
                     ++nq;
                 }
-                for (int j = 0; j < nblk && ok; ++j) {
+                for (int j = 0; j < nblk; ++j) {
                     const int kb = u.kb[j];
                     // V of a block that some row does not read in full
                     const bool scrub = u.mixed || (kb + 1) * kKeys > u.lim_lo;
                     const bool unread = kb * kKeys + row >= u.lim_hi;  // by every row
                     bool mark = false;
-#pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv, ++x) {
-                        const int slot = x % S::kTiles;
-                        uint8_t *dst = smem + S::kOffTile + slot * S::kTile + row * 128;
-                        if (F8) {
-                            const int rs = x % 3;
-                            ok = warp_wait(sh, &sh.r_full[rs], (x / 3) & 1);
-                            if (ok && x >= static_cast<uint32_t>(S::kTiles))
-                                ok = warp_wait(sh, &sh.t_empty[slot], ((x / S::kTiles) - 1) & 1);
-                            if (!ok) break;
-                            const uint8_t *src = smem + S::kOffRaw + rs * S::kRaw + row * D;
-                            uint4 w[D / 16];
-#pragma unroll
-                            for (int ch = 0; ch < D / 16; ++ch)
-                                w[ch] = *reinterpret_cast<const uint4 *>(
-                                    src + ((ch ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4));
-                            if (kv == 1 && scrub) {
-                                uint32_t bad = 0;  // bit 7 of a byte: 127 + 1, a NaN
-#pragma unroll
-                                for (int ch = 0; ch < D / 16; ++ch) {
-                                    const uint32_t *wp = reinterpret_cast<const uint32_t *>(&w[ch]);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) bad |= (wp[i] & 0x7f7f7f7fu) + 0x01010101u;
-                                }
-                                mark = (bad & 0x80808080u) != 0 && !unread;
-                                if (unread || mark) {
-#pragma unroll
-                                    for (int ch = 0; ch < D / 16; ++ch) {
-                                        uint32_t *wp = reinterpret_cast<uint32_t *>(&w[ch]);
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i)
-                                            wp[i] = unread ? 0u : wp[i] & ~__vcmpeq4(wp[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                    }
-                                }
-                            }
+                    if (M == kModeWide) {
+                        ok = warp_wait(sh, &sh.r_full[rr.slot], rr.parity()) &&
+                             (rk.round == 0 || warp_wait(sh, &sh.k_empty[rk.slot], rk.parity() ^ 1));
+                        if (!ok) break;
+                        uint4 w[D / 16];
+                        load_raw(w);
+                        warp_arrive(&sh.r_empty[rr.slot], lane);
+                        widen(w, smem + S::kOffK + rk.slot * S::kPageK);
+                        warp_arrive(&sh.k_full[rk.slot], lane);
+                        rr.next();
+                        rk.next();
+                    }
+                    if (F8) {
+                        ok = warp_wait(sh, &sh.r_full[rr.slot], rr.parity()) &&
+                             (rv.round == 0 || warp_wait(sh, &sh.v_empty[rv.slot], rv.parity() ^ 1));
+                        if (!ok) break;
+                        uint4 w[D / 16];
+                        load_raw(w);
+                        warp_arrive(&sh.r_empty[rr.slot], lane);
+                        if (scrub) {
+                            uint32_t bad = 0;  // bit 7 of a byte: 127 + 1, a NaN
 #pragma unroll
                             for (int ch = 0; ch < D / 16; ++ch) {
-                                uint32_t h[8];
                                 const uint32_t *wp = reinterpret_cast<const uint32_t *>(&w[ch]);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) tc::e4m3x4_to_f16x4(wp[i], h[2 * i], h[2 * i + 1]);
-                                uint8_t *box = dst + (ch >> 2) * kBox;
-                                const int c0 = (2 * ch) & 7;
-                                *reinterpret_cast<uint4 *>(box + ((c0 ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                                *reinterpret_cast<uint4 *>(box + (((c0 + 1) ^ (row & 7)) << 4)) =
-                                    make_uint4(h[4], h[5], h[6], h[7]);
+                                for (int i = 0; i < 4; ++i) bad |= (wp[i] & 0x7f7f7f7fu) + 0x01010101u;
                             }
-                            if (mark) {
-                                atomicOr(&u.marks[kb >> 5], 1u << (kb & 31));
-                                *reinterpret_cast<volatile int32_t *>(&u.marked) = 1;
+                            mark = (bad & 0x80808080u) != 0 && !unread;
+                            if (unread || mark) {
+#pragma unroll
+                                for (int ch = 0; ch < D / 16; ++ch) {
+                                    uint32_t *wp = reinterpret_cast<uint32_t *>(&w[ch]);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        wp[i] = unread ? 0u : wp[i] & ~__vcmpeq4(wp[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                }
+                            }
+                        }
+                        widen(w, smem + S::kOffV + rv.slot * S::kPage16);
+                        rr.next();
+                    } else {
+                        ok = warp_wait(sh, &sh.v_full[rv.slot], rv.parity());
+                        if (!ok) break;
+                        uint8_t *dst = smem + S::kOffV + rv.slot * S::kPage16 + row * 128;
+                        if (scrub) {
+                            uint32_t bad = 0;  // bit 15 of a half: exponent 255 + 1
+                            if (!unread) {
+#pragma unroll
+                                for (int b = 0; b < S::kBoxes; ++b)
+#pragma unroll 4
+                                    for (int ch = 0; ch < 8; ++ch) {
+                                        const uint4 w = *reinterpret_cast<const uint4 *>(dst + b * kBox + ((ch ^ (row & 7)) << 4));
+                                        bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                                               ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+                                    }
+                            }
+                            mark = (bad & 0x80008000u) != 0;
+                            if (unread || mark) {
+#pragma unroll
+                                for (int b = 0; b < S::kBoxes; ++b)
+#pragma unroll 2
+                                    for (int ch = 0; ch < 8; ++ch) {
+                                        uint4 *at = reinterpret_cast<uint4 *>(dst + b * kBox + ((ch ^ (row & 7)) << 4));
+                                        uint4 w = unread ? make_uint4(0, 0, 0, 0) : *at;
+                                        uint32_t *wp = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            if (!finite_bits(wp[i], true)) wp[i] &= 0xffff0000u;
+                                            if (!finite_bits(wp[i] >> 16, true)) wp[i] &= 0xffffu;
+                                        }
+                                        *at = w;
+                                    }
                             }
                             tc::fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0) {
-                                tc::mbar_arrive(&sh.r_empty[rs]);
-                                tc::mbar_arrive(&sh.t_ready[slot]);
-                            }
-                        } else if (kv == 1) {
-                            ok = warp_wait(sh, &sh.t_full[slot], (x / S::kTiles) & 1);
-                            if (!ok) break;
-                            if (scrub) {
-                                uint32_t bad = 0;  // bit 15 of a half: exponent 255 + 1
-                                if (!unread) {
-#pragma unroll
-                                    for (int b = 0; b < S::kBoxes; ++b)
-#pragma unroll 4
-                                        for (int ch = 0; ch < 8; ++ch) {
-                                            const uint4 w = *reinterpret_cast<const uint4 *>(dst + b * kBox + ((ch ^ (row & 7)) << 4));
-                                            bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
-                                                   ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
-                                        }
-                                }
-                                mark = (bad & 0x80008000u) != 0;
-                                if (unread || mark) {
-#pragma unroll
-                                    for (int b = 0; b < S::kBoxes; ++b)
-#pragma unroll 2
-                                        for (int ch = 0; ch < 8; ++ch) {
-                                            uint4 *at = reinterpret_cast<uint4 *>(dst + b * kBox + ((ch ^ (row & 7)) << 4));
-                                            uint4 w = unread ? make_uint4(0, 0, 0, 0) : *at;
-                                            uint32_t *wp = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-                                            for (int i = 0; i < 4; ++i) {
-                                                if (!finite_bits(wp[i], true)) wp[i] &= 0xffff0000u;
-                                                if (!finite_bits(wp[i] >> 16, true)) wp[i] &= 0xffffu;
-                                            }
-                                            *at = w;
-                                        }
-                                }
-                                if (mark) {
-                                    atomicOr(&u.marks[kb >> 5], 1u << (kb & 31));
-                                    *reinterpret_cast<volatile int32_t *>(&u.marked) = 1;
-                                }
-                                tc::fence_proxy_async();
-                            }
-                            warp_arrive(&sh.t_ready[slot], lane);
                         }
                     }
+                    if (mark) {
+                        atomicOr(&u.marks[kb >> 5], 1u << (kb & 31));
+                        *reinterpret_cast<volatile int32_t *>(&u.marked) = 1;
+                    }
+                    warp_arrive(&sh.v_ready[rv.slot], lane);
+                    rv.next();
                 }
                 if (!ok) break;
                 warp_arrive(&sh.u_empty[n & 1], lane);
@@ -706,9 +805,23 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         } else if (warp == kWarpTma) {
             // ------------------------------------------------- TMA loads
             if (lane == 0) {
-                uint32_t x = 0;  // K and V pages so far
+                Ring<S::kKs> rk;
+                Ring<S::kVs> rv;
+                Ring<F8 ? S::kRs : 1> rr;
                 uint32_t nq = 0;
                 bool ok = true;
+                // the next page of a ring, once its slot's last round has been read
+                auto room = [&](const auto &ring, uint64_t *empty) {
+                    return !aborted(sh) && (ring.round == 0 || wait_or_abort(sh, &empty[ring.slot], ring.parity() ^ 1));
+                };
+                auto copy8 = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *full, int h, int slot0) {
+                    tc::mbar_arrive_expect_tx(full, S::kPage8);
+                    tc::tma_load_3d(dst, map, full, 0, h, slot0);
+                };
+                auto copy16 = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *full, int h, int slot0) {
+                    tc::mbar_arrive_expect_tx(full, S::kPage16);
+                    for (int b = 0; b < S::kBoxes; ++b) tc::tma_load_3d(dst + b * kBox, map, full, 64 * b, h, slot0);
+                };
                 for (uint32_t n = 0; ok; ++n) {
                     UnitRec &u = sh.unit[n & 1];
                     ok = wait_or_abort(sh, &sh.u_full[n & 1], (n >> 1) & 1);
@@ -716,26 +829,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     const int nblk = u.nblk;
                     for (int j = 0; j < nblk && ok; ++j) {
                         const int slot0 = u.page[j] * kKeys;
-                        for (int kv = 0; kv < 2; ++kv, ++x) {
-                            const CUtensorMap *map = kv == 0 ? &tmap_k : &tmap_v;
-                            if (F8) {
-                                const int rs = x % 3;
-                                ok = !aborted(sh) && (x < 3 || wait_or_abort(sh, &sh.r_empty[rs], ((x / 3) - 1) & 1));
-                                if (!ok) break;
-                                tc::mbar_arrive_expect_tx(&sh.r_full[rs], S::kRaw);
-                                tc::tma_load_3d(smem + S::kOffRaw + rs * S::kRaw, map, &sh.r_full[rs], 0, u.h, slot0);
-                            } else {
-                                const int slot = x % S::kTiles;
-                                ok = !aborted(sh) && (x < static_cast<uint32_t>(S::kTiles) ||
-                                                      wait_or_abort(sh, &sh.t_empty[slot], ((x / S::kTiles) - 1) & 1));
-                                if (!ok) break;
-                                tc::mbar_arrive_expect_tx(&sh.t_full[slot], S::kTile);
-                                for (int b = 0; b < S::kBoxes; ++b)
-                                    tc::tma_load_3d(smem + S::kOffTile + slot * S::kTile + b * kBox, map, &sh.t_full[slot],
-                                                    64 * b, u.h, slot0);
-                            }
+                        if (M == kModeWide) {
+                            ok = room(rr, sh.r_empty);
+                            if (!ok) break;
+                            copy8(&tmap_k, smem + S::kOffRaw + rr.slot * S::kPage8, &sh.r_full[rr.slot], u.h, slot0);
+                            rr.next();
+                        } else {
+                            ok = room(rk, sh.k_empty);
+                            if (!ok) break;
+                            uint8_t *dst = smem + S::kOffK + rk.slot * S::kPageK;
+                            if (M == kModeTerms) copy8(&tmap_k, dst, &sh.k_full[rk.slot], u.h, slot0);
+                            else copy16(&tmap_k, dst, &sh.k_full[rk.slot], u.h, slot0);
+                            rk.next();
                         }
-                        if (j == 0 && ok) {
+                        if (j == 0) {
                             // the queries, once the last unit's products have read theirs
                             ok = nq == 0 || wait_or_abort(sh, &sh.q_empty, (nq - 1) & 1);
                             if (!ok) break;
@@ -747,6 +854,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                                                     u.h * t.G, u.tok0 + i * t.lay.tt);
                             ++nq;
                         }
+                        if (F8) {
+                            ok = room(rr, sh.r_empty);
+                            if (!ok) break;
+                            copy8(&tmap_v, smem + S::kOffRaw + rr.slot * S::kPage8, &sh.r_full[rr.slot], u.h, slot0);
+                            rr.next();
+                        } else {
+                            ok = room(rv, sh.v_empty);
+                            if (!ok) break;
+                            copy16(&tmap_v, smem + S::kOffV + rv.slot * S::kPage16, &sh.v_full[rv.slot], u.h, slot0);
+                            rv.next();
+                        }
                     }
                     if (ok) tc::mbar_arrive(&sh.u_empty[n & 1]);
                 }
@@ -754,9 +872,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 // an abort can one still be in flight
                 if (!ok) {
                     if (nq > 0) tc::mbar_wait(&sh.q_full, (nq - 1) & 1);
-                    const uint32_t ring = F8 ? 3 : S::kTiles;
-                    for (uint32_t y = x > ring ? x - ring : 0; y < x; ++y)
-                        tc::mbar_wait(F8 ? &sh.r_full[y % ring] : &sh.t_full[y % ring], (y / ring) & 1);
+                    auto landed = [&](const auto &ring, uint64_t *full, int slots) {
+                        for (int i = 0; i < slots; ++i) {
+                            // the last round of slot i that was begun
+                            const uint32_t rounds = ring.round + (static_cast<uint32_t>(i) < ring.slot ? 1 : 0);
+                            if (rounds > 0) tc::mbar_wait(&full[i], (rounds - 1) & 1);
+                        }
+                    };
+                    if (M != kModeWide) landed(rk, sh.k_full, S::kKs);
+                    if (F8) landed(rr, sh.r_full, S::kRs);
+                    else landed(rv, sh.v_full, S::kVs);
                 }
             }
         } else if (warp == kWarpMma || warp == kWarpMma1) {
@@ -767,45 +892,49 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             // pipe idle if the other tile's products did not fill it.  The
             // whole warp waits and counts, one elected lane issues.
             const int i = warp == kWarpMma ? 0 : 1;
-            const uint32_t idesc_s = tc::idesc_f16_m128(kKeys, kBf16);
+            const uint32_t idesc_s = M == kModeTerms ? tc::idesc_m128(kKeys, false, false) : tc::idesc_f16_m128(kKeys, kBf16);
             const uint32_t idesc_o = tc::idesc_f16_m128(D, kBf16) | (1u << 16);  // B (V) MN-major
             const uint32_t q_low = desc_low(tc::smem_u32(smem + S::kOffQ + i * S::kTileQ), 16);
-            const uint32_t t_low = desc_low(tc::smem_u32(smem + S::kOffTile), 0);
+            const uint32_t k_low = desc_low(tc::smem_u32(smem + S::kOffK), 16);
+            const uint32_t v_low = desc_low(tc::smem_u32(smem + S::kOffV), kBox);
             const uint32_t col_s = tmem + kColS + i * 128, col_o = tmem + kColO + i * 128;
-            uint32_t k_slot = 0, k_par = 0, v_slot = 0, v_par = 0;  // ring places of the next K and V tile
-            uint32_t nq = 0, n_p = 0, n_o = 0;                      // units with products, P and O tiles so far
+            Ring<S::kKs> rk;
+            Ring<S::kVs> rv;
+            uint32_t nq = 0, n_p = 0, n_o = 0;  // units with products, P and O tiles so far
             bool ok = true;
-            auto step = [&](uint32_t &slot, uint32_t &par) {
-                if (++slot == S::kTiles) {
-                    slot = 0;
-                    par ^= 1;
-                }
+            auto wait_k = [&] { return warp_wait(sh, &sh.k_full[rk.slot], rk.parity()); };
+            auto wait_v = [&] { return warp_wait(sh, &sh.v_ready[rv.slot], rv.parity()); };
+            auto wait_q = [&] {
+                return F8 ? warp_wait(sh, &sh.q_ready[nq & 1][i], (nq >> 1) & 1) : warp_wait(sh, &sh.q_full, nq & 1);
             };
-            step(v_slot, v_par);  // tiles come K, V, K, V, ...
-            auto wait_k = [&] { return warp_wait(sh, F8 ? &sh.t_ready[k_slot] : &sh.t_full[k_slot], k_par); };
-            auto wait_v = [&] { return warp_wait(sh, &sh.t_ready[v_slot], v_par); };
             // S = Q K^T; `last`: the unit's last use of the queries
             auto qk = [&](bool last) {
-                const uint32_t k = t_low + k_slot * (S::kTile >> 4) + (1u << 16);
+                const uint32_t k = k_low + rk.slot * (S::kPageK >> 4);
                 tc::tc_fence_after();
                 if (elect_one()) {
+                    if (M == kModeTerms) {
+                        // 32 dims a step, 32 bytes into a 128-byte row; the second terms one box on
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        // 16 dims a step: 32 bytes into a 128-byte row, the next 64 dims one box on
-                        const uint32_t off = ((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
-                        mma_ss(col_s, q_low + off, k + off, idesc_s, ks > 0);
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_ss<true>(col_s, q_low + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, k + (ks & 3) * 2, idesc_s, ks > 0);
+                    } else {
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            // 16 dims a step: 32 bytes into a 128-byte row, the next 64 dims one box on
+                            const uint32_t off = ((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
+                            mma_ss<false>(col_s, q_low + off, k + off, idesc_s, ks > 0);
+                        }
                     }
                     tc::mma_commit(&sh.s_full[i]);
-                    tc::mma_commit(&sh.t_empty[k_slot]);
+                    tc::mma_commit(&sh.k_empty[rk.slot]);
                     if (last) tc::mma_commit(&sh.q_empty);
                 }
                 __syncwarp();
-                step(k_slot, k_par);
-                step(k_slot, k_par);
+                rk.next();
             };
             // O (+)= P V over one half of the block's keys; `last`: O is complete
             auto pv = [&](int half, bool add, bool last) {
-                const uint32_t v = t_low + v_slot * (S::kTile >> 4) + (static_cast<uint32_t>(kBox >> 4) << 16);
+                const uint32_t v = v_low + rv.slot * (S::kPage16 >> 4);
                 tc::tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -815,9 +944,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         mma_ts(col_o, col_s + ks * 8, v + ks * (2048 >> 4), idesc_o, ks > 0 || add);
                     }
                     if (half == 1 && last) tc::mma_commit(&sh.o_full[i]);
-                    if (half == 1) tc::mma_commit(&sh.t_empty[v_slot]);
+                    if (half == 1) tc::mma_commit(&sh.v_empty[rv.slot]);
                 }
                 __syncwarp();
+                if (half == 1) rv.next();
             };
             for (uint32_t n = 0; ok; ++n) {
                 UnitRec &u = sh.unit[n & 1];
@@ -825,9 +955,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 if (!ok || u.nblk < 0) break;
                 const int nblk = u.nblk;
                 if (i == 0 || u.two) {
-                    if (nblk > 0)
-                        ok = (F8 ? warp_wait(sh, &sh.q_ready[nq & 1], (nq >> 1) & 1) : warp_wait(sh, &sh.q_full, nq & 1)) &&
-                             wait_k();
+                    if (nblk > 0) ok = wait_q() && wait_k();
                     if (!ok) break;
                     if (nblk > 0) qk(nblk == 1);
                     for (int j = 0; j < nblk; ++j) {
@@ -840,8 +968,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         if (!ok) break;
                         ++n_p;
                         pv(1, true, last);
-                        step(v_slot, v_par);
-                        step(v_slot, v_par);
                         if (last) {
                             ++n_o;
                             break;
@@ -852,18 +978,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     }
                 } else if (nblk > 0) {
                     // no second tile: its issuer only lets the pages go
-                    ok = F8 ? warp_wait(sh, &sh.q_ready[nq & 1], (nq >> 1) & 1) : warp_wait(sh, &sh.q_full, nq & 1);
+                    ok = warp_wait(sh, &sh.q_full, nq & 1);
                     if (ok && lane == 0) tc::mbar_arrive(&sh.q_empty);
                     for (int j = 0; j < nblk && ok; ++j) {
                         ok = wait_k() && wait_v();
                         if (ok && lane == 0) {
-                            tc::mbar_arrive(&sh.t_empty[k_slot]);
-                            tc::mbar_arrive(&sh.t_empty[v_slot]);
+                            tc::mbar_arrive(&sh.k_empty[rk.slot]);
+                            tc::mbar_arrive(&sh.v_empty[rv.slot]);
                         }
-                        for (int r = 0; r < 2; ++r) {
-                            step(k_slot, k_par);
-                            step(v_slot, v_par);
-                        }
+                        rk.next();
+                        rv.next();
                     }
                 }
                 if (!ok) break;
@@ -1084,9 +1208,10 @@ bool map_ok(const void *base, int es, int64_t s0, int64_t s1, int64_t n0, int64_
     return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (n1 <= 1 || legal(s1)) && (n0 <= 1 || legal(s0));
 }
 
-template <int D, bool F8>
+template <int D, Mode M>
 cudaError_t launch(const ChunkArgs &a, void *ws, cudaStream_t stream, bool *used) {
-    using S = Shape<D, F8>;
+    using S = Shape<D, M>;
+    constexpr bool F8 = S::kF8;
     constexpr int kSmem = S::kEnd + 1024 + static_cast<int>(sizeof(Shared));
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
     const int G = a.Hq / a.Hkv;
@@ -1102,7 +1227,7 @@ cudaError_t launch(const ChunkArgs &a, void *ws, cudaStream_t stream, bool *used
         !make_map(&mk, kv_type, es, a.k, D, a.Hkv, slots, ks1, a.k_s0, F8 ? D : 64, 1, kKeys) ||
         !make_map(&mv, kv_type, es, a.v, D, a.Hkv, slots, vs1, a.v_s0, F8 ? D : 64, 1, kKeys))
         return cudaSuccess;
-    const void *func = reinterpret_cast<const void *>(chunk_tc_kernel<D, F8>);
+    const void *func = reinterpret_cast<const void *>(chunk_tc_kernel<D, M>);
     cudaError_t e = opt_in_smem(func, kSmem);
     if (e != cudaSuccess) return e;
 
@@ -1135,7 +1260,7 @@ cudaError_t launch(const ChunkArgs &a, void *ws, cudaStream_t stream, bool *used
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, F8>, mq, mk, mv, t);
+    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, M>, mq, mk, mv, t);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(4 * p.ctas);
     cfg.blockDim = dim3(256);
@@ -1161,8 +1286,10 @@ cudaError_t launch_chunk_tc(const ChunkArgs &a, void *ws, cudaStream_t stream, b
     if (a.P < 1 || a.q_s2 != 1 || !map_ok(a.q, 2, a.q_s0, a.q_s1, a.total_q, a.Hq) ||
         !map_ok(a.k, es, a.k_s0, a.k_s1, a.P * kKeys, a.Hkv) || !map_ok(a.v, es, a.v_s0, a.v_s1, a.P * kKeys, a.Hkv))
         return cudaSuccess;
-    if (f8) return a.D == 128 ? launch<128, true>(a, ws, stream, used) : launch<64, true>(a, ws, stream, used);
-    return a.D == 128 ? launch<128, false>(a, ws, stream, used) : launch<64, false>(a, ws, stream, used);
+    if (!f8) return a.D == 128 ? launch<128, kModeBf16>(a, ws, stream, used) : launch<64, kModeBf16>(a, ws, stream, used);
+    // 64-dim terms would need rows of 64 bytes, f16 queries a third term: those are multiplied as f16
+    if (a.D == 128 && a.q_dt == SPD_BF16) return launch<128, kModeTerms>(a, ws, stream, used);
+    return a.D == 128 ? launch<128, kModeWide>(a, ws, stream, used) : launch<64, kModeWide>(a, ws, stream, used);
 }
 
 }  // namespace spd
