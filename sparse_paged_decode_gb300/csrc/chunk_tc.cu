@@ -59,6 +59,7 @@ namespace {
 
 constexpr int kRows = 128;           // query rows of a tile (M)
 constexpr int kKeys = kBlock;        // keys of a block (N of S, K of P V)
+constexpr int kHalf = kKeys / 2;     // keys of a softmax step
 constexpr int kThreads = 512;
 constexpr int kWarpSide = 8, kWarpTma = 12, kWarpMma = 13, kWarpSched = 14, kWarpMma1 = 15;
 constexpr int kBox = 128 * 128;      // 64 dims of 128 rows of a 16-bit type, bytes
@@ -135,6 +136,7 @@ struct Shared {
     uint64_t v_full[2], v_ready[2], v_empty[2];  // V pages: loaded (BF16), widened or scrubbed, read
     uint64_t r_full[3], r_empty[3];           // E4M3 pages to be widened
     uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];  // by tile; P by halves of a block's keys
+    uint64_t pv_half[2];                      // the products of a block's first half are done
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
@@ -181,6 +183,19 @@ __device__ __forceinline__ float tmem_ld32_max(uint32_t taddr, float *v) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
     return __uint_as_float(top);
+}
+
+// Waits for the loads issued so far; the 33 registers of one of them pass
+// through, so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_wait_ld32(float *v, float &top) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                   "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                   "+f"(v[30]), "+f"(v[31]), "+f"(top)
+                 :
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
@@ -448,6 +463,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             tc::mbar_init(&sh.u_empty[i], kUnitReleases);
             tc::mbar_init(&sh.s_full[i], 1);
             tc::mbar_init(&sh.o_full[i], 1);
+            tc::mbar_init(&sh.pv_half[i], 1);
             tc::mbar_init(&sh.o_free[i], 4);
             for (int k = 0; k < 2; ++k) {
                 tc::mbar_init(&sh.q_ready[i][k], 4);
@@ -522,6 +538,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 c *= sh.row_factor[iq & 1][tile * kRows + r];
             }
             float m_run = -INFINITY, l = 0.f;
+            float threshold = -INFINITY;  // logits above it raise the offset
+            const uint64_t c2 = pair(c, c);
+            uint64_t m2 = 0;              // minus the offset, twice (0 while the row has none)
             bool seen = false, ok = true;
             int word_at = -1;
             uint32_t word = 0;
@@ -530,9 +549,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 if (!ok) break;
                 ++n_s;
                 tc::tc_fence_after();
-                float s[kKeys], top[4];
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) top[ch] = tmem_ld32_max(col_s + ch * 32, s + ch * 32);
+                float s[2][kHalf], top[4];
+                top[0] = tmem_ld32_max(col_s, s[0]);
+                top[1] = tmem_ld32_max(col_s + 32, s[0] + 32);
                 const int kb = u.kb[j];
                 int left = lim - kb * kKeys;  // keys of the block that the row reads
                 if (u.mixed) {
@@ -542,63 +561,102 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     }
                     if (!chosen || !((word >> (kb & 31)) & 1u)) left = 0;
                 }
+                if ((u.mixed || (kb + 1) * kKeys > u.lim_lo) && __all_sync(0xffffffffu, left <= 0)) {
+                    // none of the warp's rows reads the block (another query
+                    // block's selection, or keys behind the first tile): P = 0
+                    tc::tmem_wait_ld();
+                    uint32_t zero[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) zero[i] = 0;
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) tmem_st16u(col_s + ch * 16, zero);
+                    tc::tmem_wait_st();
+                    tc::tc_fence_before();
+                    warp_arrive(&sh.p_full[tile][0], lane);
+                    warp_arrive(&sh.p_full[tile][1], lane);
+                    continue;
+                }
                 seen |= left > 0;
-                tc::tmem_wait_ld();
-                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                if (left < kKeys) {
-                    mx = -INFINITY;
+                // A block is taken in two halves of 64 keys, each a step of the
+                // online softmax of its own: the second half's logits arrive
+                // while the first half's exponentials are computed.
+                tmem_wait_ld32(s[0], top[0]);
+                tmem_wait_ld32(s[0] + 32, top[1]);
 #pragma unroll
-                    for (int i = 0; i < kKeys; ++i) {
-                        s[i] = i < left ? s[i] : -INFINITY;
-                        mx = fmaxf(mx, s[i]);
+                for (int h = 0; h < 2; ++h) {
+                    float *x = s[h];
+                    if (h == 1) {
+                        tmem_wait_ld32(s[1], top[2]);
+                        tmem_wait_ld32(s[1] + 32, top[3]);
+                        left -= kHalf;
                     }
-                }
-                const float bm = mx * c;
-                // raise the offset if the block's maximum runs more than
-                // 2^kRaise above it (or the row had none yet)
-                float alpha = 1.f;
-                if (bm != -INFINITY && bm > m_run + kRaise) {
-                    alpha = (m_run == -INFINITY) ? 0.f : tc::ex2(m_run - bm);
-                    m_run = bm;
-                    l *= alpha;
-                }
-                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    // S(j) is there, so the products of block j - 1 are done
+                    float mx = fmaxf(top[2 * h], top[2 * h + 1]);
+                    if (__any_sync(0xffffffffu, left < kHalf || mx > threshold)) {
+                        if (left < kHalf) {
+                            mx = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < kHalf; ++i) {
+                                x[i] = i < left ? x[i] : -INFINITY;
+                                mx = fmaxf(mx, x[i]);
+                            }
+                        }
+                        // raise the offset if the half's maximum runs more than
+                        // 2^kRaise above it (or the row had none yet)
+                        const bool raise = mx > threshold;
+                        float alpha = 1.f;
+                        if (raise) {
+                            const float bm = mx * c;
+                            alpha = tc::ex2(m_run - bm);  // 0 for a row that had none
+                            m_run = bm;
+                            l *= alpha;
+                            threshold = (m_run + kRaise) / c;
+                            m2 = pair(-m_run, -m_run);
+                        }
+                        if ((j > 0 || h == 1) && __any_sync(0xffffffffu, raise)) {
+                            // S(j) is there, so the products of block j - 1 are
+                            // done; those of this block's first half may not be
+                            if (h == 1) {
+                                ok = warp_wait(sh, &sh.pv_half[tile], (n_s - 1) & 1);
+                                if (!ok) break;
+                                tc::tc_fence_after();
+                            }
 #pragma unroll 1
-                    for (int ch = 0; ch < D / 16; ++ch) {
-                        float o[16];
-                        tc::tmem_ld16(col_o + ch * 16, o);
-                        tc::tmem_wait_ld();
+                            for (int ch = 0; ch < D / 16; ++ch) {
+                                float o[16];
+                                tc::tmem_ld16(col_o + ch * 16, o);
+                                tc::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                        tc::tmem_st16(col_o + ch * 16, o);
+                                for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                                tc::tmem_st16(col_o + ch * 16, o);
+                            }
+                        }
                     }
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int ch = 0; ch < 2; ++ch) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float x0, x1;
+                            unpair(fma2(pair(x[ch * 32 + 2 * i], x[ch * 32 + 2 * i + 1]), c2, m2), x0, x1);
+                            const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
+                            sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
+                            pk[i] = pack2(p0, p1, kBf16);
+                        }
+                        tmem_st16u(col_s + h * 32 + ch * 16, pk);
+                        if (h == 0 && ch == 0) {
+                            top[2] = tmem_ld32_max(col_s + 64, s[1]);
+                            top[3] = tmem_ld32_max(col_s + 96, s[1] + 32);
+                        }
+                    }
+                    tc::tmem_wait_st();
+                    tc::tc_fence_before();
+                    warp_arrive(&sh.p_full[tile][h], lane);
+                    float l0, l1;
+                    unpair(add2(sum[0], sum[1]), l0, l1);
+                    l += l0 + l1;
                 }
-                const float m_eff = (m_run == -INFINITY) ? 0.f : m_run;
-                const uint64_t c2 = pair(c, c), m2 = pair(-m_eff, -m_eff);
-                uint64_t sum[2] = {0, 0};
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float x0, x1;
-                        unpair(fma2(pair(s[ch * 32 + 2 * i], s[ch * 32 + 2 * i + 1]), c2, m2), x0, x1);
-                        const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
-                        sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
-                        pk[i] = pack2(p0, p1, kBf16);
-                    }
-                    tmem_st16u(col_s + ch * 16, pk);
-                    if (ch & 1) {
-                        // half of the keys: their product need not wait for the others'
-                        tc::tmem_wait_st();
-                        tc::tc_fence_before();
-                        warp_arrive(&sh.p_full[tile][ch >> 1], lane);
-                    }
-                }
-                float l0, l1;
-                unpair(add2(sum[0], sum[1]), l0, l1);
-                l += l0 + l1;
+                if (!ok) break;
             }
             if (!ok) break;
             // a row that reads keys whose logits are all -inf (or NaN) has no
@@ -943,6 +1001,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         const int ks = half * (kKeys / 32) + k;
                         mma_ts(col_o, col_s + ks * 8, v + ks * (2048 >> 4), idesc_o, ks > 0 || add);
                     }
+                    if (half == 0) tc::mma_commit(&sh.pv_half[i]);
                     if (half == 1 && last) tc::mma_commit(&sh.o_full[i]);
                     if (half == 1) tc::mma_commit(&sh.v_empty[rv.slot]);
                 }
