@@ -207,6 +207,24 @@ def _check_fast():
         _check()
 
 
+def _load_marshal():
+    """The compiled marshalling of the serving-step calls (csrc/marshal.cpp),
+    or None where it was not built: the calls then go through _pack."""
+    try:
+        from . import _marshal
+    except ImportError:
+        return None
+    _marshal.bind(LIB_PATH, _check)
+    return _marshal
+
+
+_fast = _load_marshal()
+
+
+def _raw(stream):
+    return None if stream is None else _stream(stream)
+
+
 def msa_block_score(q_idx, k_idx_cache, block_table, seq_lens, req_idx, block_size, scores,
                     idx_scale, stream=None) -> None:
     """Stage 1: fill ``scores`` [Hi, T, NB] with block-max index scores."""
@@ -288,6 +306,11 @@ def paged_assign_slots(new_lens, prefix_lens, slot_ids, free_pages, free_count, 
     """Slots of a serving step: grow ``block_table`` [R, NB] in place from the
     end of ``free_pages`` and fill the offsets, lengths and every token's row,
     length and slot from the requests' ``new_lens`` and ``prefix_lens``."""
+    if _fast is not None:
+        _fast.paged_assign_slots(new_lens, prefix_lens, slot_ids, free_pages, free_count, n_pages, block_size,
+            block_size_q, block_table, cu_seqlens, cu_seqblocks_q, seq_lens, req_idx, token_lens, slots,
+            free_left, _raw(stream))
+        return
     d, raw = _place(stream)
     lib.paged_assign_slots(
         _pack(new_lens, "new_lens", d), _pack(prefix_lens, "prefix_lens", d), _pack(slot_ids, "slot_ids", d),
@@ -304,6 +327,10 @@ def paged_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, token_lens, slot
     positions (``cos_sin`` [M, Rd]) of q and k: fill ``q_out`` [T, Hq, D] and
     write k and v into ``slots`` of the caches.  ``v`` and ``v_cache`` may be
     None together (index queries and keys)."""
+    if _fast is not None:
+        _fast.paged_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, token_lens, slots, q_out, k_cache,
+            v_cache, eps, 1 if interleaved else 0, block_size, k_scale, v_scale, _raw(stream))
+        return
     d, raw = _place(stream)
     lib.paged_norm_rope_store(
         _pack(q, "q", d), _pack(k, "k", d), _pack(v, "v", d), _pack(q_weight, "q_weight", d),
@@ -320,6 +347,10 @@ def paged_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqle
 
     ``workspace`` is a CUDA uint8 tensor of at least
     ``prefill_attention_workspace_bytes`` bytes."""
+    if _fast is not None:
+        _fast.paged_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqlens, seq_lens,
+            prefix_lens, out, sm_scale, block_size, k_scale, v_scale, workspace, _raw(stream))
+        return
     d, raw = _place(stream)
     lib.paged_prefill_attention(
         _pack(q, "q", d), _pack(k_cache, "k_cache", d), _pack(v_cache, "v_cache", d),
@@ -335,6 +366,11 @@ def paged_sparse_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, c
     """The same over the key blocks that ``topk_idx`` [Hkv, rows, K] lists for
     each query block of ``block_size_q`` tokens (the rows that
     msa_prefill_block_score writes)."""
+    if _fast is not None:
+        _fast.paged_sparse_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqlens, seq_lens,
+            prefix_lens, topk_idx, block_size_q, cu_seqblocks_q, out, sm_scale, block_size, k_scale, v_scale,
+            workspace, _raw(stream))
+        return
     d, raw = _place(stream)
     lib.paged_sparse_prefill_attention(
         _pack(q, "q", d), _pack(k_cache, "k_cache", d), _pack(v_cache, "v_cache", d),

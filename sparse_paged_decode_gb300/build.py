@@ -3,6 +3,8 @@
 Each ``csrc/*.cu`` compiles to an object in ``_build/`` (in parallel), then
 the objects link into ``libspd.so`` next to this file with the CUDA runtime
 linked statically.  A stamp of the sources and flags skips up-to-date builds.
+``csrc/marshal.cpp`` becomes the CPython module ``_marshal.so`` with the host
+compiler, against the torch that is installed.
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libspd.so")
+MARSHAL_PATH = os.path.join(HERE, "_marshal.so")  # CPython module: torch tensors to the serving-step calls
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -72,9 +75,60 @@ def _stamp(names=None) -> str:
     return h.hexdigest()
 
 
+def build_marshal(force: bool = False) -> bool:
+    """Compile the marshalling module; False where the toolchain cannot (no
+    Python or torch headers): the binding then describes the tensors itself,
+    which takes more host time and changes nothing else."""
+    import sys
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(CSRC, "marshal.cpp")
+    stamp_path = os.path.join(BUILD_DIR, "marshal.stamp")
+    h = hashlib.sha256()
+    for path in (src, os.path.join(INCLUDE, "spd.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    h.update(("%s %s" % (torch.__version__, sys.version)).encode())
+    if not force and os.path.exists(MARSHAL_PATH) and os.path.exists(stamp_path):
+        with open(stamp_path) as f:
+            if f.read() == h.hexdigest():
+                return True
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = MARSHAL_PATH + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, src, "-I", INCLUDE,
+           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           "-L", os.path.join(root, "lib"), "-Wl,-rpath," + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-ldl", "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        print("marshal.cpp not built: %s" % e)
+        return False
+    if r.returncode != 0:
+        print("marshal.cpp not built:\n%s" % r.stderr[-2000:])
+        return False
+    os.replace(tmp, MARSHAL_PATH)
+    with open(stamp_path, "w") as f:
+        f.write(h.hexdigest())
+    return True
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libspd.so; returns its path."""
+    """Compile and link libspd.so and the marshalling module; returns the
+    library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        marshal = ex.submit(build_marshal, force)
+        path = _build_library(force, verbose)
+        marshal.result()
+    return path
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     stamp_path = os.path.join(BUILD_DIR, "stamp")
     stamp = _stamp()
     if not force and os.path.exists(LIB_PATH) and os.path.exists(stamp_path):

@@ -758,9 +758,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 if (F8 && nblk > 0) {
                     ok = warp_wait(sh, &sh.q_full, nq & 1);
                     if (!ok) break;
-                    for (int tile = 0; tile < 1 + u.two; ++tile) {
+                    // a tile that is not there is ready too: its barrier keeps
+                    // step with the units
+                    for (int tile = 0; tile < 2; ++tile) {
                         float factor = 1.f;
-                        if (M == kModeTerms) factor = split_query_row(smem + S::kOffQ + tile * S::kTileQ + row * 128, row);
+                        if (tile == 1 && !u.two) factor = 0.f;
+                        else if (M == kModeTerms) factor = split_query_row(smem + S::kOffQ + tile * S::kTileQ + row * 128, row);
                         else if (!t.q_f16) factor = halve_query_row<D>(smem + S::kOffQ + tile * S::kTileQ + row * 128, row);
                         sh.row_factor[nq & 1][tile * kRows + row] = factor;
                         tc::fence_proxy_async();

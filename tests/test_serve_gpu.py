@@ -531,6 +531,21 @@ def test_prefill_attention_graph_replay(spd, bq, cache):
         assert torch.equal(out2.view(torch.int16), eager[1].view(torch.int16))
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "e4m3_f16", "bf16", "e4m3_d64"])
+@pytest.mark.parametrize("bq", [0, 16], ids=["dense", "bq16"])
+def test_prefill_attention_many_units(spd, bq, kind):
+    """Several units to a CTA, in turn with one tile of query rows and with
+    two, without pages and with many, split and whole."""
+    r = random.Random(11)
+    chunks = [r.choice((1, 3, 9, 16, 17, 30, 33, 60)) for _ in range(60)]
+    prefix = [r.choice((0, 0, 5, 130, 700, 1300)) for _ in chunks]
+    s = chunk_inputs(chunks, prefix, 64, 8, 64 if kind == "e4m3_d64" else 128, F16 if kind == "e4m3_f16" else BF16,
+                     BF16 if kind == "bf16" else E4M3, 101, bq=bq, topk=3)
+    for b in (3, 17, 40):  # requests without a page-table row: their units have no pages
+        s["rows"][b] = -1
+    run_chunk(spd, s, what="many units")
+
+
 def test_prefill_attention_long_splits(spd):
     """Few rows over a long cache: the keys are split over many CTAs and joined."""
     for cache in (E4M3, BF16):
@@ -574,6 +589,32 @@ def test_far_pages_of_a_large_cache(spd):
                               i32([1, 2, 3]), q_out, near, None, 1e-6, False, BS, 0.02, 1.0)
     torch.cuda.synchronize()
     assert torch.equal(kc.view(torch.uint8)[st["slots"].long().to(DEV)], near.view(torch.uint8)[1:4])
+
+
+def test_both_ways_of_marshalling(spd, monkeypatch):
+    """The compiled module and the Python descriptors pass the same call."""
+    from sparse_paged_decode_gb300 import binding
+
+    if binding._fast is None:
+        pytest.skip("the marshalling module is not built here")
+    args = (i32([70, 80, 90]), i32([200, 0, 60]), i32([2, 0, 1]), i32(list(range(30))), i32([30]), 64, 5,
+            torch.arange(64, dtype=I32, device=DEV).view(4, 16), 240)
+    st = store_inputs(30, 8, 2, 128, 64, 50, BF16, E4M3, 6)
+    ch = chunk_inputs([40, 7], [200, 0], 8, 2, 128, BF16, E4M3, 7, bq=16, topk=2)
+    got = []
+    for way in (binding._fast, None):
+        monkeypatch.setattr(binding, "_fast", way)
+        s = dict(st, kc=st["kc"].clone(), vc=st["vc"].clone())
+        got.append([*run_assign(spd, *args, strided=True), run_store(spd, s, BF16, ks=0.1, vs=0.1), s["kc"].view(torch.uint8),
+                    s["vc"].view(torch.uint8), run_chunk(spd, ch), run_chunk(spd, dict(ch, bq=0, topk=None))])
+        with pytest.raises(binding.SpdError):
+            spd.paged_assign_slots(*args[:5], -1, BS, 5, *got[-1][:8])
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        spd.paged_assign_slots(*args[:5], 64, BS, 5, *got[-1][:8], stream=side)
+        side.synchronize()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
 
 
 # ------------------------------------------------------------ the whole step

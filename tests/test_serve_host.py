@@ -193,8 +193,16 @@ def test_prefill_attention_workspace_sizes(spd):
         assert size(*bad) == 0, bad
 
 
-def test_binding_refuses_what_is_not_on_the_gpu(spd):
+@pytest.mark.parametrize("compiled", [True, False])
+def test_binding_refuses_what_is_not_on_the_gpu(spd, compiled, monkeypatch):
+    """Both ways that the binding marshals, the compiled module and the
+    Python descriptors, refuse alike."""
     import torch
+
+    if compiled and spd._fast is None:
+        pytest.skip("the marshalling module is not built here")
+    if not compiled:
+        monkeypatch.setattr(spd, "_fast", None)
 
     x = torch.zeros(3, dtype=torch.int32)
     with pytest.raises(ValueError):
@@ -203,3 +211,12 @@ def test_binding_refuses_what_is_not_on_the_gpu(spd):
         spd.paged_norm_rope_store(*[x] * 11, 1e-6, False, 128, 1.0, 1.0, stream=0)
     with pytest.raises(TypeError):
         spd.paged_prefill_attention(*[x.double()] * 9, 1.0, 128, 1.0, 1.0, None, stream=0)
+    with pytest.raises(TypeError):
+        spd.paged_prefill_attention(*["x"] * 9, 1.0, 128, 1.0, 1.0, None, stream=0)
+    with pytest.raises(ValueError):
+        spd.paged_prefill_attention(*[torch.zeros((0,) * 5)] * 9, 1.0, 128, 1.0, 1.0, None, stream=0)
+    with pytest.raises(TypeError):
+        spd.paged_prefill_attention(*[torch.zeros(0)] * 9, 1.0, 128, 1.0, 1.0, x, stream=0)
+    with pytest.raises(spd.SpdError) as e:  # past the binding: refused by the library
+        spd.paged_prefill_attention(*[torch.zeros(0)] * 9, 1.0, 128, 1.0, 1.0, None, stream=0)
+    assert e.value.code == INVALID
