@@ -349,42 +349,45 @@ __device__ __forceinline__ float halve_query_row(uint8_t *q, int row) {
 // by a power of two into [128, 256); the first term is its rounding to four
 // bits, the second what is left (four more bits: the sum is exact for elements
 // within 2^9 of the row's largest, and off by at most 2^-17 of that beyond).
-// The first terms take the row's 128 bytes of dims 0-63, the second those of
-// dims 64-127.  Returns the inverse scale.
+// 32 dims, one step of the product, take 64 bytes as bf16: their first terms
+// go into the first 32 of these, their second terms into the others, so no
+// group waits for another.  Returns the inverse scale.
 __device__ __forceinline__ float split_query_row(uint8_t *q, int row) {
     float up, down;
     row_power<128>(q, row, 7, up, down);
     const uint64_t up2 = pair(up, up);
-    uint32_t second[32];
+#pragma unroll 1
+    for (int g = 0; g < 4; ++g) {
+        uint8_t *box = q + (g >> 1) * kBox;
+        uint32_t t0[8], t1[8];
 #pragma unroll
-    for (int ch = 0; ch < 16; ch += 2) {
-        uint32_t first[4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int c = ch + k;
-            const uint4 w = *reinterpret_cast<const uint4 *>(q + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4));
+        for (int c = 0; c < 4; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(box + ((((g & 1) * 4 + c) ^ (row & 7)) << 4));
             const uint32_t wp[4] = {w.x, w.y, w.z, w.w};
-            uint32_t t0[4], t1[4];
+            uint32_t a[4], b[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float lo, hi, l0, h0;
+                float lo, hi;
                 unpair(mul2(pair(__uint_as_float(wp[i] << 16), __uint_as_float(wp[i] & 0xffff0000u)), up2), lo, hi);
-                t0[i] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-                tc::e4m3x2_to_f32x2(static_cast<uint16_t>(t0[i]), h0, l0);
-                t1[i] = __nv_cvt_float2_to_fp8x2(make_float2(lo - l0, hi - h0), __NV_SATFINITE, __NV_E4M3);
+                const __half2 h = __floats2half2_rn(lo, hi);  // eight bits of a value below 256: exact
+                a[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+                const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(a[i]), __NV_E4M3);
+                b[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(h, __half2(back))), __NV_SATFINITE,
+                                                  __NV_E4M3);
             }
-            first[2 * k] = t0[0] | (t0[1] << 16);
-            first[2 * k + 1] = t0[2] | (t0[3] << 16);
-            second[2 * c] = t1[0] | (t1[1] << 16);
-            second[2 * c + 1] = t1[2] | (t1[3] << 16);
+            t0[2 * c] = a[0] | (a[1] << 16);
+            t0[2 * c + 1] = a[2] | (a[3] << 16);
+            t1[2 * c] = b[0] | (b[1] << 16);
+            t1[2 * c + 1] = b[2] | (b[3] << 16);
         }
-        // chunk ch / 2 of the first terms lies at or before the chunks read so far
-        *reinterpret_cast<uint4 *>(q + (((ch / 2) ^ (row & 7)) << 4)) = make_uint4(first[0], first[1], first[2], first[3]);
-    }
 #pragma unroll
-    for (int ch = 0; ch < 8; ++ch)
-        *reinterpret_cast<uint4 *>(q + kBox + ((ch ^ (row & 7)) << 4)) =
-            make_uint4(second[4 * ch], second[4 * ch + 1], second[4 * ch + 2], second[4 * ch + 3]);
+        for (int c = 0; c < 2; ++c) {
+            *reinterpret_cast<uint4 *>(box + ((((g & 1) * 4 + c) ^ (row & 7)) << 4)) =
+                make_uint4(t0[4 * c], t0[4 * c + 1], t0[4 * c + 2], t0[4 * c + 3]);
+            *reinterpret_cast<uint4 *>(box + ((((g & 1) * 4 + 2 + c) ^ (row & 7)) << 4)) =
+                make_uint4(t1[4 * c], t1[4 * c + 1], t1[4 * c + 2], t1[4 * c + 3]);
+        }
+    }
     return down;
 }
 
@@ -974,10 +977,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 tc::tc_fence_after();
                 if (elect_one()) {
                     if (M == kModeTerms) {
-                        // 32 dims a step, 32 bytes into a 128-byte row; the second terms one box on
+                        // 32 dims a step: 32 bytes into K's row, 64 into the queries', the second terms 32 on
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_ss<true>(col_s, q_low + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, k + (ks & 3) * 2, idesc_s, ks > 0);
+                            mma_ss<true>(col_s, q_low + (ks >> 2) * (kBox >> 4) + ((ks >> 1) & 1) * (64 >> 4) + (ks & 1) * (32 >> 4),
+                                         k + (ks >> 1) * (32 >> 4), idesc_s, ks > 0);
                     } else {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
@@ -1064,11 +1068,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             // ---------------------------------------------- units, page lists
             const ChunkPair *pairs = reinterpret_cast<const ChunkPair *>(t.ws + t.lay.pairs);
             const int32_t n_units = hd->n_units, n_pairs = hd->n_pairs;
-            auto pair_of = [&](int32_t v) {  // the pair whose units of one head hold v
-                int lo = 0, hi = n_pairs;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (pairs[mid].unit0 <= v) lo = mid; else hi = mid;
+            // the pair whose units of one head hold v, by 32-way search
+            auto pair_of = [&](int32_t v) {
+                int lo = 0, span = n_pairs;
+                while (span > 1) {
+                    const int step = (span + 31) / 32, at = lo + lane * step;
+                    const bool below = lane * step < span && pairs[at].unit0 <= v;
+                    const int last = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // lane 0 is below
+                    const int from = max(last, 0) * step;
+                    lo += from;
+                    span = min(step, span - from);
                 }
                 return lo;
             };
