@@ -65,9 +65,9 @@ constexpr int kWarpSide = 8, kWarpTma = 12, kWarpMma = 13, kWarpSched = 14, kWar
 constexpr int kBox = 128 * 128;      // 64 dims of 128 rows of a 16-bit type, bytes
 constexpr float kRaise = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
-// registers: 128 a thread at launch; the softmax warpgroups rise to 176, the
-// two others drop to 80
-constexpr uint32_t kRegsSoft = 176, kRegsOther = 80;
+// registers: 128 a thread at launch; the softmax warpgroups rise to 168, the
+// two others drop to 88
+constexpr uint32_t kRegsSoft = 168, kRegsOther = 88;
 static_assert(256 * kRegsSoft + 256 * kRegsOther <= kThreads * 128, "register split");
 constexpr uint32_t kUnitReleases = 8 + 4 + 1 + 2;  // warps that read a unit record
 constexpr uint32_t kTmemCols = 512;
@@ -732,26 +732,54 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             Ring<S::kVs> rv;
             Ring<F8 ? S::kRs : 1> rr;
             uint32_t nq = 0;  // units with products
-            // one E4M3 page of 16-byte chunks w to f16, into the 16-bit page at `page16`
-            auto widen = [&](const uint4 *w, uint8_t *page16) {
+            // this thread's key of the next E4M3 page to f16, into the 16-bit
+            // page at `page16`, 64 dims at a time; with `scrub` zeros where no
+            // row reads it, and in place of NaN: returns whether there was one
+            auto widen = [&](uint8_t *page16, bool scrub, bool unread) {
+                const uint8_t *src = smem + S::kOffRaw + rr.slot * S::kPage8 + row * D;
+                uint32_t any = 0;
+#pragma unroll 1
+                for (int b = 0; b < S::kBoxes; ++b) {
+                    uint4 w[4];
 #pragma unroll
-                for (int ch = 0; ch < D / 16; ++ch) {
-                    uint32_t h[8];
-                    const uint32_t *wp = reinterpret_cast<const uint32_t *>(&w[ch]);
+                    for (int ch = 0; ch < 4; ++ch)
+                        w[ch] = *reinterpret_cast<const uint4 *>(
+                            src + (((4 * b + ch) ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4));
+                    if (scrub) {
+                        uint32_t bad = 0;  // bit 7 of a byte: 127 + 1, a NaN
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) tc::e4m3x4_to_f16x4(wp[i], h[2 * i], h[2 * i + 1]);
-                    uint8_t *box = page16 + (ch >> 2) * kBox + row * 128;
-                    const int c0 = (2 * ch) & 7;
-                    *reinterpret_cast<uint4 *>(box + ((c0 ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4 *>(box + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                        for (int ch = 0; ch < 4; ++ch) {
+                            const uint32_t *wp = reinterpret_cast<const uint32_t *>(&w[ch]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) bad |= (wp[i] & 0x7f7f7f7fu) + 0x01010101u;
+                        }
+                        bad &= 0x80808080u;
+                        any |= bad;
+                        if (unread || bad != 0) {
+#pragma unroll
+                            for (int ch = 0; ch < 4; ++ch) {
+                                uint32_t *wp = reinterpret_cast<uint32_t *>(&w[ch]);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    wp[i] = unread ? 0u : wp[i] & ~__vcmpeq4(wp[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            }
+                        }
+                    }
+                    uint8_t *box = page16 + b * kBox + row * 128;
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t h[8];
+                        const uint32_t *wp = reinterpret_cast<const uint32_t *>(&w[ch]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) tc::e4m3x4_to_f16x4(wp[i], h[2 * i], h[2 * i + 1]);
+                        *reinterpret_cast<uint4 *>(box + (((2 * ch) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4 *>(box + (((2 * ch + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
                 }
                 tc::fence_proxy_async();
-            };
-            auto load_raw = [&](uint4 *w) {
-                const uint8_t *src = smem + S::kOffRaw + rr.slot * S::kPage8 + row * D;
-#pragma unroll
-                for (int ch = 0; ch < D / 16; ++ch)
-                    w[ch] = *reinterpret_cast<const uint4 *>(src + ((ch ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4));
+                warp_arrive(&sh.r_empty[rr.slot], lane);
+                rr.next();
+                return any != 0 && !unread;
             };
             for (uint32_t n = 0;; ++n) {
                 UnitRec &u = sh.unit[n & 1];
@@ -784,42 +812,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         ok = warp_wait(sh, &sh.r_full[rr.slot], rr.parity()) &&
                              (rk.round == 0 || warp_wait(sh, &sh.k_empty[rk.slot], rk.parity() ^ 1));
                         if (!ok) break;
-                        uint4 w[D / 16];
-                        load_raw(w);
-                        warp_arrive(&sh.r_empty[rr.slot], lane);
-                        widen(w, smem + S::kOffK + rk.slot * S::kPageK);
+                        widen(smem + S::kOffK + rk.slot * S::kPageK, false, false);
                         warp_arrive(&sh.k_full[rk.slot], lane);
-                        rr.next();
                         rk.next();
                     }
                     if (F8) {
                         ok = warp_wait(sh, &sh.r_full[rr.slot], rr.parity()) &&
                              (rv.round == 0 || warp_wait(sh, &sh.v_empty[rv.slot], rv.parity() ^ 1));
                         if (!ok) break;
-                        uint4 w[D / 16];
-                        load_raw(w);
-                        warp_arrive(&sh.r_empty[rr.slot], lane);
-                        if (scrub) {
-                            uint32_t bad = 0;  // bit 7 of a byte: 127 + 1, a NaN
-#pragma unroll
-                            for (int ch = 0; ch < D / 16; ++ch) {
-                                const uint32_t *wp = reinterpret_cast<const uint32_t *>(&w[ch]);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) bad |= (wp[i] & 0x7f7f7f7fu) + 0x01010101u;
-                            }
-                            mark = (bad & 0x80808080u) != 0 && !unread;
-                            if (unread || mark) {
-#pragma unroll
-                                for (int ch = 0; ch < D / 16; ++ch) {
-                                    uint32_t *wp = reinterpret_cast<uint32_t *>(&w[ch]);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        wp[i] = unread ? 0u : wp[i] & ~__vcmpeq4(wp[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                }
-                            }
-                        }
-                        widen(w, smem + S::kOffV + rv.slot * S::kPage16);
-                        rr.next();
+                        mark = widen(smem + S::kOffV + rv.slot * S::kPage16, scrub, unread);
                     } else {
                         ok = warp_wait(sh, &sh.v_full[rv.slot], rv.parity());
                         if (!ok) break;
