@@ -21,6 +21,7 @@
 #include "chunk_plan.cuh"
 #include "spd_dispatch.h"
 #include "spd_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace spd {
 
@@ -28,20 +29,9 @@ namespace {
 
 constexpr int kPlanT = 1024;
 constexpr int kMaxRanked = 1024;  // sequences that are ordered by length
+constexpr int kSmemPairs = 2048;  // pairs whose lengths and places fit shared memory
 constexpr int kMaxPieces = 64;
 constexpr float kUnitBlocks = 3.f;
-
-struct Seq {
-    int32_t n, limit;  // tokens, and keys its last token reads
-};
-
-// Tokens of sequence b (offsets clipped to the batch).
-__device__ __forceinline__ int32_t seq_tokens(const ChunkArgs &a, int b, int32_t *start) {
-    const int32_t lo = min(max(a.cu[b * a.cu_s0], 0), a.total_q);
-    const int32_t hi = min(max(a.cu[(b + 1) * a.cu_s0], 0), a.total_q);
-    *start = lo;
-    return max(hi - lo, 0);
-}
 
 // Exclusive prefix sum over the CTA and the total.
 __device__ __forceinline__ int32_t scan_cta(int32_t x, int32_t *sums, int32_t *total) {
@@ -66,10 +56,14 @@ __device__ __forceinline__ int32_t scan_cta(int32_t x, int32_t *sums, int32_t *t
     return incl - x + (warp > 0 ? before : 0);
 }
 
+// Everything the steps share lies in shared memory: the batch's metadata is
+// read once, the pair records are written once, and between the two no step
+// waits for global memory.  (Batches of more than kSmemPairs pairs keep the
+// two arrays that a pair has in the workspace instead.)
 __device__ void plan_batch(const ChunkPlanArgs &p) {
-    extern __shared__ int32_t dyn[];  // order [B], pair offsets in that order [B + 1]
+    extern __shared__ int32_t dyn[];
     __shared__ int32_t sums[32];
-    __shared__ int32_t limits[kMaxRanked];
+    __shared__ int32_t small[2 * kSmemPairs];
     __shared__ float best_est[32];
     __shared__ int32_t best_u[32];
     __shared__ int32_t cmax_s;
@@ -77,22 +71,34 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     ChunkHeader *hd = reinterpret_cast<ChunkHeader *>(p.ws + p.lay.header);
     ChunkPair *pairs = reinterpret_cast<ChunkPair *>(p.ws + p.lay.pairs);
-    int32_t *order = dyn, *poff = dyn + a.B;
+    int32_t *splits = reinterpret_cast<int32_t *>(p.ws + p.lay.splits);
+    // per sequence: first token, tokens, cached keys, keys in all; order by
+    // length, and pair offsets in that order
+    int32_t *start = dyn, *n_tok = start + a.B, *pre = n_tok + a.B, *cap = pre + a.B, *order = cap + a.B, *poff = order + a.B;
     const int pair_tokens = 2 * p.lay.tt;
+
+    for (int b = tid; b < a.B; b += kPlanT) {
+        const int32_t lo = min(max(a.cu[b * a.cu_s0], 0), a.total_q);
+        const int32_t hi = min(max(a.cu[(b + 1) * a.cu_s0], 0), a.total_q);
+        const int32_t r = a.sid[b * a.sid_s0];
+        start[b] = lo;
+        n_tok[b] = max(hi - lo, 0);
+        pre[b] = min(max(a.pre[b * a.pre_s0], -(1 << 30)), 1 << 30);
+        cap[b] = r >= 0 && r < a.R ? min(a.sl[b * a.sl_s0], a.NB * kBlock) : 0;
+    }
+    if (tid == 0) cmax_s = 0;
+    __syncthreads();
+    auto limit = [&](int b, int32_t i) { return max(min(pre[b] + i + 1, cap[b]), 0); };
 
     // order of the sequences: by keys read, descending, ties by index
     if (a.B <= kMaxRanked) {
-        int32_t mine = 0;
         if (tid < a.B) {
-            int32_t start;
-            const int32_t n = seq_tokens(a, tid, &start);
-            mine = n > 0 ? chunk_limit(a, tid, n - 1) : -1;
-            limits[tid] = mine;
-        }
-        __syncthreads();
-        if (tid < a.B) {
+            const int32_t mine = n_tok[tid] > 0 ? limit(tid, n_tok[tid] - 1) : -1;
             int rank = 0;
-            for (int o = 0; o < a.B; ++o) rank += limits[o] > mine || (limits[o] == mine && o < tid);
+            for (int o = 0; o < a.B; ++o) {
+                const int32_t other = n_tok[o] > 0 ? limit(o, n_tok[o] - 1) : -1;
+                rank += other > mine || (other == mine && o < tid);
+            }
             order[rank] = tid;
         }
     } else {
@@ -104,52 +110,47 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
     int32_t carry = 0;
     for (int base = 0; base < a.B; base += kPlanT) {
         const int k = base + tid;
-        int32_t np = 0, start, total;
-        if (k < a.B) np = (seq_tokens(a, order[k], &start) + pair_tokens - 1) / pair_tokens;
+        int32_t np = 0, total;
+        if (k < a.B) np = (n_tok[order[k]] + pair_tokens - 1) / pair_tokens;
         const int32_t at = scan_cta(np, sums, &total);
         if (k < a.B) poff[k] = carry + at;
         carry += total;
     }
-    if (tid == 0) {
-        poff[a.B] = carry;
-        cmax_s = 0;
-    }
+    if (tid == 0) poff[a.B] = carry;
     __syncthreads();
     // offsets that decrease could name more pairs than the workspace holds
-    const int32_t n_pairs = min(static_cast<int64_t>(carry), p.lay.pair_cap);
-    int32_t cmax = 0;
-    for (int q = tid; q < n_pairs; q += kPlanT) {
+    const int32_t n_pairs = static_cast<int32_t>(min(static_cast<int64_t>(carry), p.lay.pair_cap));
+    int32_t *costs = n_pairs <= kSmemPairs ? small : reinterpret_cast<int32_t *>(p.ws + p.lay.pair_tmp);
+    int32_t *unit0 = n_pairs <= kSmemPairs ? small + kSmemPairs : costs + p.lay.pair_cap;
+    // the place of pair q in the order, and its first token and tokens there
+    auto place = [&](int q, int32_t &i0, int32_t &nt) {
         int lo = 0, hi = a.B;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (poff[mid] <= q) lo = mid; else hi = mid;
         }
-        const int b = order[lo];
-        int32_t start;
-        const int32_t n = seq_tokens(a, b, &start);
-        ChunkPair r;
-        r.b = b;
-        const int64_t i0 = (static_cast<int64_t>(q) - poff[lo]) * pair_tokens;
-        const bool inside = i0 >= 0 && i0 < n;  // always, unless the offsets decrease
-        r.i0 = inside ? static_cast<int32_t>(i0) : 0;
-        r.nt = inside ? min(pair_tokens, n - r.i0) : 0;
-        r.tok0 = start + r.i0;
-        int64_t cost = r.nt > 0 ? (chunk_limit(a, b, r.i0 + r.nt - 1) + kBlock - 1) / kBlock : 0;
-        if (a.tk != nullptr) {
-            const int64_t rows = (r.i0 + r.nt - 1) / a.bsq - r.i0 / a.bsq + 1;
+        const int32_t n = n_tok[order[lo]];
+        const int64_t at = (static_cast<int64_t>(q) - poff[lo]) * pair_tokens;
+        const bool inside = at >= 0 && at < n;  // always, unless the offsets decrease
+        i0 = inside ? static_cast<int32_t>(at) : 0;
+        nt = inside ? min(pair_tokens, n - i0) : 0;
+        return lo;
+    };
+    int32_t cmax = 0;
+    for (int q = tid; q < n_pairs; q += kPlanT) {
+        int32_t i0, nt;
+        const int b = order[place(q, i0, nt)];
+        int64_t cost = nt > 0 ? (limit(b, i0 + nt - 1) + kBlock - 1) / kBlock : 0;
+        if (a.tk != nullptr && nt > 0) {
+            const int64_t rows = (i0 + nt - 1) / a.bsq - i0 / a.bsq + 1;
             cost = min(cost, rows * a.K);
         }
-        r.cost = static_cast<int32_t>(cost);
-        r.unit0 = r.pieces = r.part0 = 0;
-        r.seq0 = poff[lo];  // for now the pair indexes that the sequence spans
-        r.seq_units = min(poff[lo + 1], n_pairs);
-        r.reserved[0] = r.reserved[1] = 0;
-        pairs[q] = r;
-        cmax = max(cmax, r.cost);
+        costs[q] = static_cast<int32_t>(cost);
+        cmax = max(cmax, static_cast<int32_t>(cost));
     }
     cmax = __reduce_max_sync(0xffffffffu, cmax);
     if (lane == 0) atomicMax(&cmax_s, cmax);
-    __syncthreads();  // pairs are read below by other threads of this CTA only
+    __syncthreads();
     cmax = max(cmax_s, 1);
 
     // piece length
@@ -161,7 +162,7 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
         float parts = 0.f, work = 0.f, longest = 0.f;
         for (int base = 0; base < n_pairs; base += 32) {
             const int q = base + lane;
-            const int32_t c = q < n_pairs ? pairs[q].cost : 0;
+            const int32_t c = q < n_pairs ? costs[q] : 0;
             const int32_t k = q < n_pairs ? max((c + U - 1) / U, 1) : 0;
             int32_t incl = k;
 #pragma unroll
@@ -209,32 +210,41 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
         }
     }
 
-    // unit and partial ranges
-    int32_t ucarry = 0, pcarry = 0, scarry = 0;
-    int32_t *splits = reinterpret_cast<int32_t *>(p.ws + p.lay.splits);
+    // unit ranges, then the records
+    auto pieces_of = [&](int q) { return max((costs[q] + U - 1) / U, 1); };
+    int32_t ucarry = 0;
     for (int base = 0; base < n_pairs; base += kPlanT) {
         const int q = base + tid;
-        int32_t k = 0, utotal, ptotal, stotal;
-        if (q < n_pairs) k = max((pairs[q].cost + U - 1) / U, 1);
-        const int32_t ku = scan_cta(k, sums, &utotal);
+        int32_t total;
+        const int32_t at = scan_cta(q < n_pairs ? pieces_of(q) : 0, sums, &total);
+        if (q < n_pairs) unit0[q] = ucarry + at;
+        ucarry += total;
+    }
+    __syncthreads();
+    int32_t pcarry = 0, scarry = 0;
+    for (int base = 0; base < n_pairs; base += kPlanT) {
+        const int q = base + tid;
+        const int32_t k = q < n_pairs ? pieces_of(q) : 0;
+        int32_t ptotal, stotal;
         const int32_t kp = scan_cta(k > 1 ? k : 0, sums, &ptotal);
         const int32_t ks = scan_cta(k > 1 ? 1 : 0, sums, &stotal);
-        if (k > 1) splits[scarry + ks] = q;
         if (q < n_pairs) {
-            pairs[q].unit0 = ucarry + ku;
-            pairs[q].pieces = k;
-            pairs[q].part0 = pcarry + kp;
+            ChunkPair r;
+            const int at = place(q, r.i0, r.nt);
+            r.b = order[at];
+            r.tok0 = start[r.b] + r.i0;
+            r.cost = costs[q];
+            r.unit0 = unit0[q];
+            r.pieces = k;
+            r.part0 = pcarry + kp;
+            r.seq0 = unit0[min(max(poff[at], 0), n_pairs - 1)];
+            r.seq_units = (poff[at + 1] < n_pairs ? unit0[max(poff[at + 1], 0)] : ucarry) - r.seq0;
+            r.reserved[0] = r.reserved[1] = 0;
+            pairs[q] = r;
+            if (k > 1) splits[scarry + ks] = q;
         }
-        ucarry += utotal;
         pcarry += ptotal;
         scarry += stotal;
-    }
-    // the sequences' unit ranges, from their first pairs'
-    __syncthreads();
-    for (int q = tid; q < n_pairs; q += kPlanT) {
-        const int32_t next = pairs[q].seq_units, u0 = pairs[pairs[q].seq0].unit0;
-        pairs[q].seq0 = u0;
-        pairs[q].seq_units = (next < n_pairs ? pairs[next].unit0 : ucarry) - u0;
     }
     if (tid == 0) {
         hd->status = 0;
@@ -247,6 +257,7 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
 }
 
 __global__ void __launch_bounds__(kPlanT) chunk_plan_kernel(const __grid_constant__ ChunkPlanArgs p) {
+
     if (blockIdx.x == 0) {
         plan_batch(p);
         return;
@@ -291,10 +302,15 @@ __global__ void __launch_bounds__(kPlanT) chunk_plan_kernel(const __grid_constan
 }  // namespace
 
 cudaError_t launch_chunk_plan(const ChunkPlanArgs &p, cudaStream_t stream) {
-    const int bytes = (2 * p.a.B + 1) * static_cast<int>(sizeof(int32_t));
+    const int bytes = (6 * p.a.B + 1) * static_cast<int>(sizeof(int32_t));
     cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(chunk_plan_kernel), bytes);
     if (e != cudaSuccess) return e;
-    chunk_plan_kernel<<<device_sm_count(), kPlanT, bytes, stream>>>(p);
+    // beside the planning CTA, one for about every 32 selection rows, or 64
+    // output rows that may have to be zeroed
+    int64_t others = (static_cast<int64_t>(p.a.total_q) + 63) / 64;
+    if (p.a.tk != nullptr) others += (static_cast<int64_t>(p.heads_built) * p.a.n_rows + 31) / 32;
+    const int64_t most = device_sm_count() > 1 ? device_sm_count() - 1 : 1;
+    chunk_plan_kernel<<<static_cast<unsigned>(1 + (others < most ? others : most)), kPlanT, bytes, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -54,7 +54,7 @@ constexpr int kChunkMaxParts = 608;  // partial slots: four pieces per SM of a 1
 
 // Byte layout of the workspace for capacities.
 struct ChunkLayout {
-    size_t header, pairs, splits, bitmaps, stats, partials, total;
+    size_t header, pairs, splits, pair_tmp, bitmaps, stats, partials, total;
     int64_t pair_cap, part_cap;
     int tt, words;
 
@@ -73,6 +73,7 @@ struct ChunkLayout {
         header = off;   off += align(sizeof(ChunkHeader));
         pairs = off;    off += align(sizeof(ChunkPair) * (size_t)pair_cap);
         splits = off;   off += align(sizeof(int32_t) * (size_t)pair_cap);
+        pair_tmp = off; off += align(sizeof(int32_t) * 2 * (size_t)pair_cap);
         bitmaps = off;  off += align(sizeof(uint32_t) * (size_t)Hkv * (size_t)n_rows * (size_t)words);
         stats = off;    off += align(sizeof(float) * 2 * (size_t)part_cap * 256);
         partials = off; off += align(sizeof(float) * (size_t)part_cap * 256 * (size_t)D);
