@@ -145,6 +145,8 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
             const int64_t rows = (i0 + nt - 1) / a.bsq - i0 / a.bsq + 1;
             cost = min(cost, rows * a.K);
         }
+        // one tile of rows: two pages at a time, for a little more than one
+        if (nt <= p.lay.tt) cost = (3 * cost + 4) / 5;
         costs[q] = static_cast<int32_t>(cost);
         cmax = max(cmax, static_cast<int32_t>(cost));
     }

@@ -22,6 +22,12 @@
 // f16 by a power of two per row (exact for elements within 2^38 of their row's
 // largest), which the row's logit factor takes back.
 //
+// A pair of one tile of rows (a short chunk, or the end of one) is worked on by
+// both tiles all the same: each holds the rows, takes every other page and
+// keeps sums of its own, and the first tile joins them at the end (the second
+// one's O lies in the same tensor-memory lanes).  A page then takes half as
+// long, which is what a few rows over a long cache wait for.
+//
 // Softmax: c = sm_scale * k_scale * log2(e) > 0.  The exponent offset m of a
 // row is raised only when a block's maximum exceeds it by more than 2^kRaise
 // (then the row's O is rescaled in tensor memory), so p <= 2^kRaise; p is
@@ -115,7 +121,8 @@ struct Ring {
 struct UnitRec {
     int32_t nblk;        // key blocks; -1: no more units
     int32_t tok0, i0, nt;  // first query token, its index in the chunk, tokens
-    int32_t h, two;      // kv head; the second tile has rows
+    int32_t h, tiles;    // kv head; tiles at work
+    int32_t dual;        // one tile of rows: both tiles hold them and take every other page
     int32_t pre, cap;    // a row's limit is min(pre + i + 1, cap), at least 0
     int32_t lim_lo;      // limits of the first and the last token
     int32_t lim_hi;
@@ -140,6 +147,8 @@ struct Shared {
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
+    uint64_t dual_ready;              // the second tile's sums of a dual unit
+    float2 dual_stats[kRows];         // its rows' exponent offsets and sums
     float row_factor[2][2 * kRows];  // by parity of the units with products: what the queries' scaling takes from the logits
     UnitRec unit[2];
 };
@@ -482,6 +491,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             tc::mbar_init(&sh.r_full[i], 1);
             tc::mbar_init(&sh.r_empty[i], 4);
         }
+        tc::mbar_init(&sh.dual_ready, 4);
         tc::mbar_init(&sh.q_full, 1);
         tc::mbar_init(&sh.q_empty, 2);
         tc::mbar_init(&sh.drain[0], 1);
@@ -510,19 +520,22 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t col_s = tmem + lane_base + kColS + tile * 128;
         const uint32_t col_o = tmem + lane_base + kColO + tile * 128;
-        const int j_tok = tile * t.lay.tt + r / t.G, g = r % t.G;  // token within the pair, head within the group
+        const int tile_tok = r / t.G, g = r % t.G;  // token within the tile, head within the group
         const bool in_tile = r < t.lay.tt * t.G;
         uint32_t n_s = 0, n_o = 0;  // S buffers seen, O tiles seen
-        uint32_t nq = 0;            // units with products
+        uint32_t nq = 0, n_dual = 0;  // units with products, dual units
         for (uint32_t n = 0;; ++n) {
             UnitRec &u = sh.unit[n & 1];
             if (!warp_wait(sh, &sh.u_full[n & 1], (n >> 1) & 1) || u.nblk < 0) break;
             const int nblk = u.nblk;
+            const bool dual = u.dual != 0;
+            const int j_tok = tile_tok + (dual ? 0 : tile * t.lay.tt);  // token within the pair
+            const int first = dual ? tile : 0, stride = dual ? 2 : 1;    // this tile's pages
             const bool have = in_tile && j_tok < u.nt;
             const int32_t lim = have ? row_limit(u, u.i0 + j_tok) : 0;
             const uint32_t iq = nq;
             if (nblk > 0) ++nq;
-            if (tile == 1 && !u.two) {
+            if (tile >= u.tiles) {
                 warp_arrive(&sh.u_empty[n & 1], lane);
                 continue;
             }
@@ -547,7 +560,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             bool seen = false, ok = true;
             int word_at = -1;
             uint32_t word = 0;
-            for (int j = 0; j < nblk; ++j) {
+            for (int j = first; j < nblk; j += stride) {
                 ok = warp_wait(sh, &sh.s_full[tile], n_s & 1);
                 if (!ok) break;
                 ++n_s;
@@ -615,7 +628,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                             threshold = (m_run + kRaise) / c;
                             m2 = pair(-m_run, -m_run);
                         }
-                        if ((j > 0 || h == 1) && __any_sync(0xffffffffu, raise)) {
+                        if ((j > first || h == 1) && __any_sync(0xffffffffu, raise)) {
                             // S(j) is there, so the products of block j - 1 are
                             // done; those of this block's first half may not be
                             if (h == 1) {
@@ -676,6 +689,29 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 ++n_o;
                 tc::tc_fence_after();
             }
+            float w_own = 1.f, w_other = 0.f;  // weights of the two tiles' O in a dual unit
+            if (dual) {
+                if (tile == 1) {
+                    // the first tile joins: the same rows lie in the same lanes
+                    sh.dual_stats[r] = make_float2(m_run, l);
+                    tc::tc_fence_before();
+                    warp_arrive(&sh.dual_ready, lane);
+                    warp_arrive(&sh.u_empty[n & 1], lane);
+                    continue;
+                }
+                ok = warp_wait(sh, &sh.dual_ready, n_dual & 1);
+                if (!ok) break;
+                ++n_dual;
+                tc::tc_fence_after();
+                const float2 other = sh.dual_stats[r];
+                const float m = fmaxf(m_run, other.x);
+                if (m != -INFINITY) {
+                    w_own = tc::ex2(m_run - m);
+                    w_other = tc::ex2(other.x - m);
+                    l = l * w_own + other.y * w_other;  // a NaN stays one, whatever its weight
+                    m_run = m;
+                }
+            }
             if (nblk > 0 && u.marked != 0) take_marked<D, F8>(t, u, have && chosen ? lim : 0, bits, col_o);
             const bool split = u.pieces > 1;
             const bool none = nblk == 0 || m_run == -INFINITY;  // no key of this piece was read
@@ -691,9 +727,18 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     tmem_ld32(col_o + c0, o);
                     tmem_ld32(col_o + c0 + 32, o + 32);
                     tc::tmem_wait_ld();
+                    if (dual) {
+                        float x[64];
+                        tmem_ld32(col_o + 128 + c0, x);
+                        tmem_ld32(col_o + 128 + c0 + 32, x + 32);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) o[i] = fmaf(o[i], w_own, x[i] * w_other);
+                    }
                     if (c0 + 64 == D) {  // the next unit's products may overwrite O
                         tc::tc_fence_before();
                         warp_arrive(&sh.o_free[tile], lane);
+                        if (dual) warp_arrive(&sh.o_free[1], lane);
                     }
 #pragma unroll
                     for (int i = 0; i < 64; ++i) o[i] = none ? 0.f : o[i];
@@ -793,7 +838,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     // step with the units
                     for (int tile = 0; tile < 2; ++tile) {
                         float factor = 1.f;
-                        if (tile == 1 && !u.two) factor = 0.f;
+                        if (tile >= u.tiles) factor = 0.f;
                         else if (M == kModeTerms) factor = split_query_row(smem + S::kOffQ + tile * S::kTileQ + row * 128, row);
                         else if (!t.q_f16) factor = halve_query_row<D>(smem + S::kOffQ + tile * S::kTileQ + row * 128, row);
                         sh.row_factor[nq & 1][tile * kRows + row] = factor;
@@ -911,12 +956,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                             // the queries, once the last unit's products have read theirs
                             ok = nq == 0 || wait_or_abort(sh, &sh.q_empty, (nq - 1) & 1);
                             if (!ok) break;
-                            const int tiles = 1 + u.two;
+                            const int tiles = u.tiles;
                             tc::mbar_arrive_expect_tx(&sh.q_full, tiles * S::kBoxes * 128 * t.G * t.lay.tt);
                             for (int i = 0; i < tiles; ++i)
                                 for (int b = 0; b < S::kBoxes; ++b)
                                     tc::tma_load_3d(smem + S::kOffQ + i * S::kTileQ + b * kBox, &tmap_q, &sh.q_full, 64 * b,
-                                                    u.h * t.G, u.tok0 + i * t.lay.tt);
+                                                    u.h * t.G, u.tok0 + (u.dual ? 0 : i * t.lay.tt));
                             ++nq;
                         }
                         if (F8) {
@@ -1021,28 +1066,55 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 ok = warp_wait(sh, &sh.u_full[n & 1], (n >> 1) & 1);
                 if (!ok || u.nblk < 0) break;
                 const int nblk = u.nblk;
-                if (i == 0 || u.two) {
-                    if (nblk > 0) ok = wait_q() && wait_k();
-                    if (!ok) break;
-                    if (nblk > 0) qk(nblk == 1);
-                    for (int j = 0; j < nblk; ++j) {
-                        const bool last = j == nblk - 1;
-                        ok = wait_v() && (j > 0 || n_o == 0 || warp_wait(sh, &sh.o_free[i], (n_o - 1) & 1)) &&
+                if (i < u.tiles) {
+                    const int first = u.dual ? i : 0, stride = u.dual ? 2 : 1;
+                    // pages of the other tile only pass by
+                    int k_at = 0, v_at = 0;  // next K and V page in the rings
+                    auto pass_k = [&](int to) {
+                        for (; k_at < to && ok; ++k_at) {
+                            ok = wait_k();
+                            if (ok && lane == 0) tc::mbar_arrive(&sh.k_empty[rk.slot]);
+                            rk.next();
+                        }
+                    };
+                    auto pass_v = [&](int to) {
+                        for (; v_at < to && ok; ++v_at) {
+                            ok = wait_v();
+                            if (ok && lane == 0) tc::mbar_arrive(&sh.v_empty[rv.slot]);
+                            rv.next();
+                        }
+                    };
+                    if (nblk > 0) {
+                        pass_k(first);
+                        ok = ok && wait_q() && wait_k();
+                        if (!ok) break;
+                        qk(first + stride >= nblk);
+                        ++k_at;
+                    }
+                    for (int j = first; j < nblk; j += stride) {
+                        const bool last = j + stride >= nblk;
+                        pass_v(j);
+                        ok = ok && wait_v() && (j > first || n_o == 0 || warp_wait(sh, &sh.o_free[i], (n_o - 1) & 1)) &&
                              warp_wait(sh, &sh.p_full[i][0], n_p & 1);
                         if (!ok) break;
-                        pv(0, j > 0, last);
+                        pv(0, j > first, last);
                         ok = warp_wait(sh, &sh.p_full[i][1], n_p & 1);
                         if (!ok) break;
                         ++n_p;
                         pv(1, true, last);
+                        ++v_at;
                         if (last) {
                             ++n_o;
                             break;
                         }
-                        ok = wait_k();
+                        pass_k(j + stride);
+                        ok = ok && wait_k();
                         if (!ok) break;
-                        qk(j == nblk - 2);
+                        qk(j + 2 * stride >= nblk);
+                        ++k_at;
                     }
+                    pass_k(nblk);
+                    pass_v(nblk);
                 } else if (nblk > 0) {
                     // no second tile: its issuer only lets the pages go
                     ok = warp_wait(sh, &sh.q_full, nq & 1);
@@ -1165,7 +1237,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     u.i0 = pr.i0;
                     u.nt = pr.nt;
                     u.h = h;
-                    u.two = pr.nt > t.lay.tt;
+                    u.dual = pr.nt <= t.lay.tt && count >= 2;
+                    u.tiles = u.dual || pr.nt > t.lay.tt ? 2 : 1;
                     u.pre = pre;
                     u.cap = cap;
                     u.lim_lo = lim_lo;
@@ -1225,7 +1298,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
         const float w0 = s0.x == -INFINITY ? 0.f : tc::ex2(s0.x - M), w1 = s1.x == -INFINITY ? 0.f : tc::ex2(s1.x - M);
-        float L = (w0 == 0.f ? 0.f : s0.y * w0) + (w1 == 0.f ? 0.f : s1.y * w1);
+        float L = s0.y * w0 + s1.y * w1;  // a NaN stays one, whatever its weight
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
         float o[kPer];
