@@ -1266,11 +1266,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     if (warp == kWarpMma) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the pieces of split pairs: one warp per query row, a lane per D / 32
-// dims, in piece order.  The pieces' loads do not depend on one another, so a
-// row costs about one memory latency however many pieces it has; joined by the
-// last piece's softmax warps instead, thread by thread, the rows of 10 pieces
-// took 150 us.
+// Joins the pieces of split pairs, in piece order: a warp takes kJoinRows
+// neighbouring rows of one head at a time.  A share of the lanes finds each
+// row's offset and sum from the pieces' statistics; then the rows' partials, a
+// lane per D / 32 dims, are added with no load waiting for another, so a group
+// costs a few memory latencies however many pieces it has.  (Joined by the last
+// piece's softmax warps, thread by thread, the rows of 10 pieces took 150 us.)
+constexpr int kJoinRows = 2;
+constexpr int kJoinLanes = 32 / kJoinRows;
+
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ TcArgs t) {
     tc::pdl_wait();
@@ -1279,53 +1283,69 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
     const ChunkPair *pairs = reinterpret_cast<const ChunkPair *>(t.ws + t.lay.pairs);
     const int32_t *splits = reinterpret_cast<const int32_t *>(t.ws + t.lay.splits);
     const int lane = threadIdx.x & 31;
-    const int64_t rows = static_cast<int64_t>(hd->n_splits) * a.Hkv * 256;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+    constexpr int kGroups = 256 / kJoinRows;  // of a pair and head
+    const int64_t groups = static_cast<int64_t>(hd->n_splits) * a.Hkv * kGroups;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
     constexpr int kPer = D / 32;
-    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); k < rows; k += step) {
-        const int r = static_cast<int>(k & 255);
-        const int h = static_cast<int>((k >> 8) % a.Hkv);
-        const ChunkPair pr = pairs[splits[(k >> 8) / a.Hkv]];
-        const int j = (r >> 7) * t.lay.tt + (r & 127) / t.G, g = (r & 127) % t.G;
-        if ((r & 127) >= t.lay.tt * t.G || j >= pr.nt) continue;
-        const int64_t row0 = (static_cast<int64_t>(h) * hd->head_parts + pr.part0) * 256 + r;
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); k < groups; k += stride) {
+        const int r0 = static_cast<int>(k % kGroups) * kJoinRows;
+        const int h = static_cast<int>((k / kGroups) % a.Hkv);
+        const ChunkPair pr = pairs[splits[k / kGroups / a.Hkv]];
+        auto token = [&](int r) {  // of the pair, or -1 where the row holds none
+            const int j = (r >> 7) * t.lay.tt + (r & 127) / t.G;
+            return (r & 127) < t.lay.tt * t.G && j < pr.nt ? j : -1;
+        };
+        if (token(r0) < 0) continue;  // rows fill a tile from its first on
+        const int64_t row0 = (static_cast<int64_t>(h) * hd->head_parts + pr.part0) * 256 + r0;
         const float2 *stats = reinterpret_cast<const float2 *>(t.ws + t.lay.stats) + row0;
-        // lane l holds pieces l and l + 32
-        const float2 none = make_float2(-INFINITY, 0.f);
-        const float2 s0 = lane < pr.pieces ? stats[lane * 256] : none;
-        const float2 s1 = lane + 32 < pr.pieces ? stats[(lane + 32) * 256] : none;
-        float M = fmaxf(s0.x, s1.x);
+        const float *parts = reinterpret_cast<const float *>(t.ws + t.lay.partials) + row0 * D + lane * kPer;
+        // offset and sum of the lane's row
+        const int own = lane / kJoinLanes;
+        const bool mine = token(r0 + own) >= 0;
+        float M = -INFINITY, L = 0.f;
+        for (int p = lane % kJoinLanes; p < pr.pieces; p += kJoinLanes)
+            if (mine) M = fmaxf(M, stats[p * 256 + own].x);
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        const float w0 = s0.x == -INFINITY ? 0.f : tc::ex2(s0.x - M), w1 = s1.x == -INFINITY ? 0.f : tc::ex2(s1.x - M);
-        float L = s0.y * w0 + s1.y * w1;  // a NaN stays one, whatever its weight
+        for (int d = kJoinLanes / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        for (int p = lane % kJoinLanes; p < pr.pieces; p += kJoinLanes)
+            if (mine && M != -INFINITY) {
+                const float2 s = stats[p * 256 + own];
+                L += s.y * tc::ex2(s.x - M);  // a NaN stays one, whatever its weight
+            }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-        float o[kPer];
+        for (int d = kJoinLanes / 2; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-        const float *src = reinterpret_cast<const float *>(t.ws + t.lay.partials) + row0 * D + lane * kPer;
-#pragma unroll 8
-        for (int p = 0; p < pr.pieces; ++p) {
-            float x[kPer];
-            if (kPer == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(src + static_cast<int64_t>(p) * 256 * D);
-            else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(src + static_cast<int64_t>(p) * 256 * D);
-            const float w = __shfl_sync(0xffffffffu, p < 32 ? w0 : w1, p & 31);
+        for (int i = 0; i < kJoinRows; ++i) {
+            const int j = token(r0 + i);
+            const float m = __shfl_sync(0xffffffffu, M, kJoinLanes * i), l = __shfl_sync(0xffffffffu, L, kJoinLanes * i);
+            if (j < 0) continue;
+            float o[kPer];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) o[i] = fmaf(x[i], w, o[i]);
-        }
-        const float f = M == -INFINITY ? 0.f : a.v_scale / L;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + static_cast<int64_t>(pr.tok0 + j) * a.o_s0 +
-                             static_cast<int64_t>(h * t.G + g) * a.o_s1;
-        if (a.o_s2 == 1 && (reinterpret_cast<uintptr_t>(out) & 7) == 0) {
-            uint32_t w[kPer / 2];
+            for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+#pragma unroll 4
+            for (int p = 0; p < pr.pieces; ++p) {
+                const float w = m == -INFINITY ? 0.f : tc::ex2(stats[p * 256 + i].x - m);
+                const float *src = parts + (static_cast<int64_t>(p) * 256 + i) * D;
+                float x[kPer];
+                if (kPer == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(src);
+                else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(src);
 #pragma unroll
-            for (int i = 0; i < kPer / 2; ++i) w[i] = pack2(o[2 * i] * f, o[2 * i + 1] * f, true);
-            if (kPer == 4) reinterpret_cast<uint2 *>(out)[lane] = make_uint2(w[0], w[kPer / 2 - 1]);
-            else reinterpret_cast<uint32_t *>(out)[lane] = w[0];
-        } else {
+                for (int e = 0; e < kPer; ++e) o[e] = fmaf(x[e], w, o[e]);
+            }
+            const float f = m == -INFINITY ? 0.f : a.v_scale / l;
+            const int g = ((r0 + i) & 127) % t.G;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + static_cast<int64_t>(pr.tok0 + j) * a.o_s0 +
+                                 static_cast<int64_t>(h * t.G + g) * a.o_s1;
+            if (a.o_s2 == 1 && (reinterpret_cast<uintptr_t>(out) & 7) == 0) {
+                uint32_t w[kPer / 2];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) out[(lane * kPer + i) * a.o_s2] = __float2bfloat16_rn(o[i] * f);
+                for (int e = 0; e < kPer / 2; ++e) w[e] = pack2(o[2 * e] * f, o[2 * e + 1] * f, true);
+                if (kPer == 4) reinterpret_cast<uint2 *>(out)[lane] = make_uint2(w[0], w[kPer / 2 - 1]);
+                else reinterpret_cast<uint32_t *>(out)[lane] = w[0];
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) out[(lane * kPer + e) * a.o_s2] = __float2bfloat16_rn(o[e] * f);
+            }
         }
     }
 }
@@ -1407,7 +1427,7 @@ cudaError_t launch(const ChunkArgs &a, void *ws, cudaStream_t stream, bool *used
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, M>, mq, mk, mv, t);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(4 * p.ctas);
+    cfg.gridDim = dim3(8 * p.ctas);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, chunk_join_kernel<D>, t);
