@@ -71,9 +71,9 @@ constexpr int kWarpSide = 8, kWarpTma = 12, kWarpMma = 13, kWarpSched = 14, kWar
 constexpr int kBox = 128 * 128;      // 64 dims of 128 rows of a 16-bit type, bytes
 constexpr float kRaise = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
-// registers: 128 a thread at launch; the softmax warpgroups rise to 168, the
-// two others drop to 88
-constexpr uint32_t kRegsSoft = 168, kRegsOther = 88;
+// registers: 128 a thread at launch; the softmax warpgroups rise to 152, the
+// two others drop to 104
+constexpr uint32_t kRegsSoft = 152, kRegsOther = 104;
 static_assert(256 * kRegsSoft + 256 * kRegsOther <= kThreads * 128, "register split");
 constexpr uint32_t kUnitReleases = 8 + 4 + 1 + 2;  // warps that read a unit record
 constexpr uint32_t kTmemCols = 512;
@@ -142,8 +142,9 @@ struct Shared {
     uint64_t k_full[3], k_empty[3];           // K pages for the products
     uint64_t v_full[2], v_ready[2], v_empty[2];  // V pages: loaded (BF16), widened or scrubbed, read
     uint64_t r_full[3], r_empty[3];           // E4M3 pages to be widened
-    uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];  // by tile; P by halves of a block's keys
-    uint64_t pv_half[2];                      // the products of a block's first half are done
+    uint64_t s_full[2][2], p_full[2][2];      // by tile and half of a page's keys
+    uint64_t pv_done[2];                      // by tile: the product of one more half is done
+    uint64_t o_full[2], o_free[2];
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
@@ -473,12 +474,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sh.u_full[i], 1);
             tc::mbar_init(&sh.u_empty[i], kUnitReleases);
-            tc::mbar_init(&sh.s_full[i], 1);
             tc::mbar_init(&sh.o_full[i], 1);
-            tc::mbar_init(&sh.pv_half[i], 1);
+            tc::mbar_init(&sh.pv_done[i], 1);
             tc::mbar_init(&sh.o_free[i], 4);
             for (int k = 0; k < 2; ++k) {
                 tc::mbar_init(&sh.q_ready[i][k], 4);
+                tc::mbar_init(&sh.s_full[i][k], 1);
                 tc::mbar_init(&sh.p_full[i][k], 4);
             }
             tc::mbar_init(&sh.v_full[i], 1);
@@ -560,16 +561,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             bool seen = false, ok = true;
             int word_at = -1;
             uint32_t word = 0;
-            for (int j = first; j < nblk; j += stride) {
-                ok = warp_wait(sh, &sh.s_full[tile], n_s & 1);
-                if (!ok) break;
-                ++n_s;
-                tc::tc_fence_after();
-                float s[2][kHalf], top[4];
-                top[0] = tmem_ld32_max(col_s, s[0]);
-                top[1] = tmem_ld32_max(col_s + 32, s[0] + 32);
+            // Half a page, 64 keys, is a step of the online softmax.  Its logits
+            // lie in one of two buffers, and its P goes over them.
+            for (int j = first; j < nblk && ok; j += stride, ++n_s) {
                 const int kb = u.kb[j];
-                int left = lim - kb * kKeys;  // keys of the block that the row reads
+                int left = lim - kb * kKeys;  // keys of the page that the row reads
                 if (u.mixed) {
                     if (bits != nullptr && (kb >> 5) != word_at) {
                         word_at = kb >> 5;
@@ -577,92 +573,80 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     }
                     if (!chosen || !((word >> (kb & 31)) & 1u)) left = 0;
                 }
-                if ((u.mixed || (kb + 1) * kKeys > u.lim_lo) && __all_sync(0xffffffffu, left <= 0)) {
-                    // none of the warp's rows reads the block (another query
-                    // block's selection, or keys behind the first tile): P = 0
-                    tc::tmem_wait_ld();
-                    uint32_t zero[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) zero[i] = 0;
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) tmem_st16u(col_s + ch * 16, zero);
-                    tc::tmem_wait_st();
-                    tc::tc_fence_before();
-                    warp_arrive(&sh.p_full[tile][0], lane);
-                    warp_arrive(&sh.p_full[tile][1], lane);
-                    continue;
-                }
                 seen |= left > 0;
-                // A block is taken in two halves of 64 keys, each a step of the
-                // online softmax of its own: the second half's logits arrive
-                // while the first half's exponentials are computed.
-                tmem_wait_ld32(s[0], top[0]);
-                tmem_wait_ld32(s[0] + 32, top[1]);
+                const bool partial = u.mixed || (kb + 1) * kKeys > u.lim_lo;  // some row does not read it all
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float *x = s[h];
-                    if (h == 1) {
-                        tmem_wait_ld32(s[1], top[2]);
-                        tmem_wait_ld32(s[1] + 32, top[3]);
-                        left -= kHalf;
-                    }
-                    float mx = fmaxf(top[2 * h], top[2 * h + 1]);
-                    if (__any_sync(0xffffffffu, left < kHalf || mx > threshold)) {
-                        if (left < kHalf) {
-                            mx = -INFINITY;
+                    ok = warp_wait(sh, &sh.s_full[tile][h], n_s & 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    float x[kHalf], top[2];
+                    top[0] = tmem_ld32_max(col_s + h * kHalf, x);
+                    top[1] = tmem_ld32_max(col_s + h * kHalf + 32, x + 32);
+                    if (h == 1) left -= kHalf;
+                    tmem_wait_ld32(x, top[0]);
+                    tmem_wait_ld32(x + 32, top[1]);
+                    uint64_t sum[2] = {0, 0};
+                    if (partial && __all_sync(0xffffffffu, left <= 0)) {
+                        // none of the warp's rows reads these keys (another
+                        // query block's selection, or keys behind the first
+                        // tile): P = 0
+                        uint32_t zero[16];
 #pragma unroll
-                            for (int i = 0; i < kHalf; ++i) {
-                                x[i] = i < left ? x[i] : -INFINITY;
-                                mx = fmaxf(mx, x[i]);
+                        for (int i = 0; i < 16; ++i) zero[i] = 0;
+#pragma unroll
+                        for (int ch = 0; ch < 2; ++ch) tmem_st16u(col_s + h * kHalf + ch * 16, zero);
+                    } else {
+                        float mx = fmaxf(top[0], top[1]);
+                        if (__any_sync(0xffffffffu, left < kHalf || mx > threshold)) {
+                            if (left < kHalf) {
+                                mx = -INFINITY;
+#pragma unroll
+                                for (int i = 0; i < kHalf; ++i) {
+                                    x[i] = i < left ? x[i] : -INFINITY;
+                                    mx = fmaxf(mx, x[i]);
+                                }
                             }
-                        }
-                        // raise the offset if the half's maximum runs more than
-                        // 2^kRaise above it (or the row had none yet)
-                        const bool raise = mx > threshold;
-                        float alpha = 1.f;
-                        if (raise) {
-                            const float bm = mx * c;
-                            alpha = tc::ex2(m_run - bm);  // 0 for a row that had none
-                            m_run = bm;
-                            l *= alpha;
-                            threshold = (m_run + kRaise) / c;
-                            m2 = pair(-m_run, -m_run);
-                        }
-                        if ((j > first || h == 1) && __any_sync(0xffffffffu, raise)) {
-                            // S(j) is there, so the products of block j - 1 are
-                            // done; those of this block's first half may not be
-                            if (h == 1) {
-                                ok = warp_wait(sh, &sh.pv_half[tile], (n_s - 1) & 1);
+                            // raise the offset if the step's maximum runs more
+                            // than 2^kRaise above it (or the row had none yet)
+                            const bool raise = mx > threshold;
+                            float alpha = 1.f;
+                            if (raise) {
+                                const float bm = mx * c;
+                                alpha = tc::ex2(m_run - bm);  // 0 for a row that had none
+                                m_run = bm;
+                                l *= alpha;
+                                threshold = (m_run + kRaise) / c;
+                                m2 = pair(-m_run, -m_run);
+                            }
+                            if ((j > first || h == 1) && __any_sync(0xffffffffu, raise)) {
+                                // the step before's product may still add to O
+                                ok = warp_wait(sh, &sh.pv_done[tile], h ^ 1);
                                 if (!ok) break;
                                 tc::tc_fence_after();
-                            }
 #pragma unroll 1
-                            for (int ch = 0; ch < D / 16; ++ch) {
-                                float o[16];
-                                tc::tmem_ld16(col_o + ch * 16, o);
-                                tc::tmem_wait_ld();
+                                for (int ch = 0; ch < D / 16; ++ch) {
+                                    float o[16];
+                                    tc::tmem_ld16(col_o + ch * 16, o);
+                                    tc::tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                                tc::tmem_st16(col_o + ch * 16, o);
+                                    for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                                    tc::tmem_st16(col_o + ch * 16, o);
+                                }
                             }
                         }
-                    }
-                    uint64_t sum[2] = {0, 0};
 #pragma unroll
-                    for (int ch = 0; ch < 2; ++ch) {
-                        uint32_t pk[16];
+                        for (int ch = 0; ch < 2; ++ch) {
+                            uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float x0, x1;
-                            unpair(fma2(pair(x[ch * 32 + 2 * i], x[ch * 32 + 2 * i + 1]), c2, m2), x0, x1);
-                            const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
-                            sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
-                            pk[i] = pack2(p0, p1, kBf16);
-                        }
-                        tmem_st16u(col_s + h * 32 + ch * 16, pk);
-                        if (h == 0 && ch == 0) {
-                            top[2] = tmem_ld32_max(col_s + 64, s[1]);
-                            top[3] = tmem_ld32_max(col_s + 96, s[1] + 32);
+                            for (int i = 0; i < 16; ++i) {
+                                float x0, x1;
+                                unpair(fma2(pair(x[ch * 32 + 2 * i], x[ch * 32 + 2 * i + 1]), c2, m2), x0, x1);
+                                const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
+                                sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
+                                pk[i] = pack2(p0, p1, kBf16);
+                            }
+                            tmem_st16u(col_s + h * kHalf + ch * 16, pk);
                         }
                     }
                     tc::tmem_wait_st();
@@ -672,7 +656,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     unpair(add2(sum[0], sum[1]), l0, l1);
                     l += l0 + l1;
                 }
-                if (!ok) break;
             }
             if (!ok) break;
             // a row that reads keys whose logits are all -inf (or NaN) has no
@@ -1002,7 +985,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             // pipe idle if the other tile's products did not fill it.  The
             // whole warp waits and counts, one elected lane issues.
             const int i = warp == kWarpMma ? 0 : 1;
-            const uint32_t idesc_s = M == kModeTerms ? tc::idesc_m128(kKeys, false, false) : tc::idesc_f16_m128(kKeys, kBf16);
+            const uint32_t idesc_s = M == kModeTerms ? tc::idesc_m128(kHalf, false, false) : tc::idesc_f16_m128(kHalf, kBf16);
             const uint32_t idesc_o = tc::idesc_f16_m128(D, kBf16) | (1u << 16);  // B (V) MN-major
             const uint32_t q_low = desc_low(tc::smem_u32(smem + S::kOffQ + i * S::kTileQ), 16);
             const uint32_t k_low = desc_low(tc::smem_u32(smem + S::kOffK), 16);
@@ -1017,45 +1000,44 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             auto wait_q = [&] {
                 return F8 ? warp_wait(sh, &sh.q_ready[nq & 1][i], (nq >> 1) & 1) : warp_wait(sh, &sh.q_full, nq & 1);
             };
-            // S = Q K^T; `last`: the unit's last use of the queries
-            auto qk = [&](bool last) {
-                const uint32_t k = k_low + rk.slot * (S::kPageK >> 4);
+            // S = Q K^T over one half of the page's keys; `last`: the unit's last use of the queries
+            auto qk = [&](int half, bool last) {
+                const uint32_t k = k_low + rk.slot * (S::kPageK >> 4) + half * (kHalf * 128 >> 4);
                 tc::tc_fence_after();
                 if (elect_one()) {
                     if (M == kModeTerms) {
                         // 32 dims a step: 32 bytes into K's row, 64 into the queries', the second terms 32 on
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_ss<true>(col_s, q_low + (ks >> 2) * (kBox >> 4) + ((ks >> 1) & 1) * (64 >> 4) + (ks & 1) * (32 >> 4),
+                            mma_ss<true>(col_s + half * kHalf,
+                                         q_low + (ks >> 2) * (kBox >> 4) + ((ks >> 1) & 1) * (64 >> 4) + (ks & 1) * (32 >> 4),
                                          k + (ks >> 1) * (32 >> 4), idesc_s, ks > 0);
                     } else {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
                             // 16 dims a step: 32 bytes into a 128-byte row, the next 64 dims one box on
                             const uint32_t off = ((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
-                            mma_ss<false>(col_s, q_low + off, k + off, idesc_s, ks > 0);
+                            mma_ss<false>(col_s + half * kHalf, q_low + off, k + off, idesc_s, ks > 0);
                         }
                     }
-                    tc::mma_commit(&sh.s_full[i]);
-                    tc::mma_commit(&sh.k_empty[rk.slot]);
+                    tc::mma_commit(&sh.s_full[i][half]);
+                    if (half == 1) tc::mma_commit(&sh.k_empty[rk.slot]);
                     if (last) tc::mma_commit(&sh.q_empty);
                 }
                 __syncwarp();
-                rk.next();
+                if (half == 1) rk.next();
             };
-            // O (+)= P V over one half of the block's keys; `last`: O is complete
+            // O (+)= P V over one half of the page's keys; `last`: O is complete
             auto pv = [&](int half, bool add, bool last) {
-                const uint32_t v = v_low + rv.slot * (S::kPage16 >> 4);
+                const uint32_t v = v_low + rv.slot * (S::kPage16 >> 4) + half * (kHalf * 128 >> 4);
                 tc::tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kKeys / 32; ++k) {
+                    for (int ks = 0; ks < kHalf / 16; ++ks)
                         // P: 16 keys = 8 columns of 16-bit pairs; V: two 8-key groups, the next 64 dims one box on
-                        const int ks = half * (kKeys / 32) + k;
-                        mma_ts(col_o, col_s + ks * 8, v + ks * (2048 >> 4), idesc_o, ks > 0 || add);
-                    }
-                    if (half == 0) tc::mma_commit(&sh.pv_half[i]);
-                    if (half == 1 && last) tc::mma_commit(&sh.o_full[i]);
+                        mma_ts(col_o, col_s + half * kHalf + ks * 8, v + ks * (2048 >> 4), idesc_o, ks > 0 || add);
+                    tc::mma_commit(&sh.pv_done[i]);
+                    if (last) tc::mma_commit(&sh.o_full[i]);
                     if (half == 1) tc::mma_commit(&sh.v_empty[rv.slot]);
                 }
                 __syncwarp();
@@ -1088,30 +1070,32 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         pass_k(first);
                         ok = ok && wait_q() && wait_k();
                         if (!ok) break;
-                        qk(first + stride >= nblk);
+                        qk(0, false);
+                        qk(1, first + stride >= nblk);
                         ++k_at;
                     }
-                    for (int j = first; j < nblk; j += stride) {
+                    for (int j = first; j < nblk && ok; j += stride) {
                         const bool last = j + stride >= nblk;
                         pass_v(j);
-                        ok = ok && wait_v() && (j > first || n_o == 0 || warp_wait(sh, &sh.o_free[i], (n_o - 1) & 1)) &&
-                             warp_wait(sh, &sh.p_full[i][0], n_p & 1);
-                        if (!ok) break;
-                        pv(0, j > first, last);
-                        ok = warp_wait(sh, &sh.p_full[i][1], n_p & 1);
-                        if (!ok) break;
-                        ++n_p;
-                        pv(1, true, last);
-                        ++v_at;
-                        if (last) {
-                            ++n_o;
-                            break;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (h == 0) ok = ok && wait_v() && (j > first || n_o == 0 || warp_wait(sh, &sh.o_free[i], (n_o - 1) & 1));
+                            ok = ok && warp_wait(sh, &sh.p_full[i][h], n_p & 1);
+                            if (!ok) break;
+                            pv(h, j > first || h > 0, h == 1 && last);
+                            if (last) continue;
+                            // the next page's half into the buffer that this half's P leaves
+                            if (h == 0) {
+                                pass_k(j + stride);
+                                ok = ok && wait_k();
+                                if (!ok) break;
+                            }
+                            qk(h, h == 1 && j + 2 * stride >= nblk);
                         }
-                        pass_k(j + stride);
-                        ok = ok && wait_k();
-                        if (!ok) break;
-                        qk(j + 2 * stride >= nblk);
-                        ++k_at;
+                        ++n_p;
+                        ++v_at;
+                        if (last) ++n_o;
+                        else ++k_at;
                     }
                     pass_k(nblk);
                     pass_v(nblk);
