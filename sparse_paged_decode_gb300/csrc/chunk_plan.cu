@@ -142,8 +142,12 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
         const int b = order[place(q, i0, nt)];
         int64_t cost = nt > 0 ? (limit(b, i0 + nt - 1) + kBlock - 1) / kBlock : 0;
         if (a.tk != nullptr && nt > 0) {
-            const int64_t rows = (i0 + nt - 1) / a.bsq - i0 / a.bsq + 1;
-            cost = min(cost, rows * a.K);
+            // each tile takes the blocks that its query blocks list, at most
+            // all that there are; two tiles side by side
+            const int32_t nt0 = min(nt, p.lay.tt);
+            const int64_t c0 = min(cost, static_cast<int64_t>((i0 + nt0 - 1) / a.bsq - i0 / a.bsq + 1) * a.K);
+            const int64_t c1 = min(cost, static_cast<int64_t>((i0 + nt - 1) / a.bsq - (i0 + nt0) / a.bsq + 1) * a.K);
+            cost = nt > nt0 ? (c0 + c1 + 1) / 2 : c0;
         }
         // one tile of rows: two pages at a time, for a little more than one
         if (nt <= p.lay.tt) cost = (3 * cost + 4) / 5;

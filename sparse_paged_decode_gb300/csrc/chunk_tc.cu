@@ -118,21 +118,24 @@ struct Ring {
     __device__ __forceinline__ uint32_t parity() const { return round & 1; }
 };
 
+constexpr int kTakeShift = 14;
+constexpr uint32_t kBlockMask = (1u << kTakeShift) - 1;
+
 struct UnitRec {
     int32_t nblk;        // key blocks; -1: no more units
     int32_t tok0, i0, nt;  // first query token, its index in the chunk, tokens
     int32_t h, tiles;    // kv head; tiles at work
     int32_t dual;        // one tile of rows: both tiles hold them and take every other page
+    int32_t own[2];      // pages that each tile takes
     int32_t pre, cap;    // a row's limit is min(pre + i + 1, cap), at least 0
     int32_t lim_lo;      // limits of the first and the last token
     int32_t lim_hi;
-    int32_t mixed;       // rows of several query blocks: each tests its own bitmap
+    int32_t mixed;       // bit per tile: rows of several query blocks, each tests its own bitmap
     int32_t qrow0, qrow_end;  // selection row of the sequence's first token, and the end of its rows
     int32_t pieces, part;     // pieces of the pair; partial slot of this one
-    int32_t bt_row;      // page-table row
     int32_t marked;      // some V element of a scrubbed block is not finite
     int32_t page[kMaxNB];
-    uint16_t kb[kMaxNB];
+    uint16_t kb[kMaxNB];  // key block, and from kTakeShift on a bit per tile that takes it
     uint32_t marks[kMaxNB / 32];  // key blocks that hold such elements
 };
 
@@ -406,17 +409,20 @@ __device__ __forceinline__ float split_query_row(uint8_t *q, int row) {
 // the row's O in tensor memory, where the products saw zeros in their place.
 // A warp-collective, and a rare, call.
 template <int D, bool F8>
-__device__ __noinline__ void take_marked(const TcArgs &t, const UnitRec &u, int32_t lim, const uint32_t *row_bits,
-                                         uint32_t col_o) {
+__device__ __noinline__ void take_marked(const TcArgs &t, const UnitRec &u, int tile, int32_t lim,
+                                         const uint32_t *row_bits, uint32_t col_o) {
     const ChunkArgs &a = t.a;
     uint32_t odd[3][D / 32];  // NaN, +inf, -inf dims
     for (int k = 0; k < 3; ++k)
         for (int i = 0; i < D / 32; ++i) odd[k][i] = 0;
     uint32_t all = 0;  // all dims NaN: nothing more to find
-    for (int kb = 0; kb * kKeys < lim && all != 0xffffffffu; ++kb) {
-        if (!((u.marks[kb >> 5] >> (kb & 31)) & 1u)) continue;
+    for (int at = 0; at < u.nblk && all != 0xffffffffu; ++at) {
+        const uint32_t entry = u.kb[at];
+        const int kb = entry & kBlockMask;
+        if (kb * kKeys >= lim || !((u.marks[kb >> 5] >> (kb & 31)) & 1u)) continue;
+        if (!u.dual && !((entry >> (kTakeShift + tile)) & 1u)) continue;  // only the other tile's rows read it
         if (row_bits != nullptr && !((row_bits[kb >> 5] >> (kb & 31)) & 1u)) continue;
-        const int64_t page = a.bt[u.bt_row * a.bt_s0 + kb * a.bt_s1];
+        const int64_t page = u.page[at];
         const int n = min(kKeys, lim - kb * kKeys);
         for (int i = 0; i < n && all != 0xffffffffu; ++i) {
             const uint8_t *v = a.v + ((page * kKeys + i) * a.v_s0 + u.h * a.v_s1) * (F8 ? 1 : 2);
@@ -531,7 +537,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             const int nblk = u.nblk;
             const bool dual = u.dual != 0;
             const int j_tok = tile_tok + (dual ? 0 : tile * t.lay.tt);  // token within the pair
-            const int first = dual ? tile : 0, stride = dual ? 2 : 1;    // this tile's pages
             const bool have = in_tile && j_tok < u.nt;
             const int32_t lim = have ? row_limit(u, u.i0 + j_tok) : 0;
             const uint32_t iq = nq;
@@ -542,7 +547,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             }
             const uint32_t *bits = nullptr;  // the row's own selection, when the unit's rows differ
             bool chosen = true;
-            if (u.mixed && have) {
+            const bool mixed = (u.mixed >> tile) & 1;
+            const int own = u.own[tile];
+            if (mixed && have) {
                 const int64_t row = static_cast<int64_t>(u.qrow0) + (u.i0 + j_tok) / a.bsq;
                 chosen = row >= 0 && row < u.qrow_end;
                 if (chosen)
@@ -550,7 +557,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                            ((t.heads_built > 1 ? static_cast<int64_t>(u.h) : 0) * a.n_rows + row) * t.lay.words;
             }
             float c = t.c;
-            if (F8 && nblk > 0) {
+            if (F8 && own > 0) {
                 if (!warp_wait(sh, &sh.q_ready[iq & 1][tile], (iq >> 1) & 1)) break;
                 c *= sh.row_factor[iq & 1][tile * kRows + r];
             }
@@ -563,10 +570,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             uint32_t word = 0;
             // Half a page, 64 keys, is a step of the online softmax.  Its logits
             // lie in one of two buffers, and its P goes over them.
-            for (int j = first; j < nblk && ok; j += stride, ++n_s) {
-                const int kb = u.kb[j];
+            for (int j = 0, done = 0; done < own && ok; ++j) {
+                const uint32_t entry = u.kb[j];
+                if (!((entry >> (kTakeShift + tile)) & 1u)) continue;  // the other tile's page
+                const int kb = entry & kBlockMask;
                 int left = lim - kb * kKeys;  // keys of the page that the row reads
-                if (u.mixed) {
+                if (mixed) {
                     if (bits != nullptr && (kb >> 5) != word_at) {
                         word_at = kb >> 5;
                         word = bits[word_at];
@@ -574,7 +583,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     if (!chosen || !((word >> (kb & 31)) & 1u)) left = 0;
                 }
                 seen |= left > 0;
-                const bool partial = u.mixed || (kb + 1) * kKeys > u.lim_lo;  // some row does not read it all
+                const bool partial = mixed || (kb + 1) * kKeys > u.lim_lo;  // some row does not read it all
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     ok = warp_wait(sh, &sh.s_full[tile][h], n_s & 1);
@@ -619,7 +628,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                                 threshold = (m_run + kRaise) / c;
                                 m2 = pair(-m_run, -m_run);
                             }
-                            if ((j > first || h == 1) && __any_sync(0xffffffffu, raise)) {
+                            if ((done > 0 || h == 1) && __any_sync(0xffffffffu, raise)) {
                                 // the step before's product may still add to O
                                 ok = warp_wait(sh, &sh.pv_done[tile], h ^ 1);
                                 if (!ok) break;
@@ -656,6 +665,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     unpair(add2(sum[0], sum[1]), l0, l1);
                     l += l0 + l1;
                 }
+                ++done;
+                ++n_s;
             }
             if (!ok) break;
             // a row that reads keys whose logits are all -inf (or NaN) has no
@@ -666,7 +677,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             }
 
             // ------------------------------------------------- epilogue
-            if (nblk > 0) {
+            if (own > 0) {
                 ok = warp_wait(sh, &sh.o_full[tile], n_o & 1);
                 if (!ok) break;
                 ++n_o;
@@ -695,9 +706,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     m_run = m;
                 }
             }
-            if (nblk > 0 && u.marked != 0) take_marked<D, F8>(t, u, have && chosen ? lim : 0, bits, col_o);
+            if (own > 0 && u.marked != 0) take_marked<D, F8>(t, u, tile, have && chosen ? lim : 0, bits, col_o);
             const bool split = u.pieces > 1;
-            const bool none = nblk == 0 || m_run == -INFINITY;  // no key of this piece was read
+            const bool none = own == 0 || m_run == -INFINITY;  // no key of this piece was read
             const int64_t prow = static_cast<int64_t>(u.part) * 256 + tile * kRows + r;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (u.tok0 + j_tok) * a.o_s0 +
                                  static_cast<int64_t>(u.h * t.G + g) * a.o_s1;
@@ -706,7 +717,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 64) {
                 float o[64];
-                if (nblk > 0) {
+                if (own > 0) {
                     tmem_ld32(col_o + c0, o);
                     tmem_ld32(col_o + c0 + 32, o + 32);
                     tc::tmem_wait_ld();
@@ -831,9 +842,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     ++nq;
                 }
                 for (int j = 0; j < nblk; ++j) {
-                    const int kb = u.kb[j];
-                    // V of a block that some row does not read in full
-                    const bool scrub = u.mixed || (kb + 1) * kKeys > u.lim_lo;
+                    const uint32_t entry = u.kb[j];
+                    const int kb = entry & kBlockMask;
+                    // V of a page that some row of a tile that takes it does not read in full
+                    const bool scrub = (u.mixed & (entry >> kTakeShift)) != 0 || (kb + 1) * kKeys > u.lim_lo;
                     const bool unread = kb * kKeys + row >= u.lim_hi;  // by every row
                     bool mark = false;
                     if (M == kModeWide) {
@@ -1048,71 +1060,112 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 ok = warp_wait(sh, &sh.u_full[n & 1], (n >> 1) & 1);
                 if (!ok || u.nblk < 0) break;
                 const int nblk = u.nblk;
-                if (i < u.tiles) {
-                    const int first = u.dual ? i : 0, stride = u.dual ? 2 : 1;
-                    // pages of the other tile only pass by
-                    int k_at = 0, v_at = 0;  // next K and V page in the rings
-                    auto pass_k = [&](int to) {
-                        for (; k_at < to && ok; ++k_at) {
-                            ok = wait_k();
-                            if (ok && lane == 0) tc::mbar_arrive(&sh.k_empty[rk.slot]);
-                            rk.next();
-                        }
-                    };
-                    auto pass_v = [&](int to) {
-                        for (; v_at < to && ok; ++v_at) {
-                            ok = wait_v();
-                            if (ok && lane == 0) tc::mbar_arrive(&sh.v_empty[rv.slot]);
-                            rv.next();
-                        }
-                    };
-                    if (nblk > 0) {
-                        pass_k(first);
-                        ok = ok && wait_q() && wait_k();
-                        if (!ok) break;
-                        qk(0, false);
-                        qk(1, first + stride >= nblk);
-                        ++k_at;
-                    }
-                    for (int j = first; j < nblk && ok; j += stride) {
-                        const bool last = j + stride >= nblk;
-                        pass_v(j);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (h == 0) ok = ok && wait_v() && (j > first || n_o == 0 || warp_wait(sh, &sh.o_free[i], (n_o - 1) & 1));
-                            ok = ok && warp_wait(sh, &sh.p_full[i][h], n_p & 1);
-                            if (!ok) break;
-                            pv(h, j > first || h > 0, h == 1 && last);
-                            if (last) continue;
-                            // the next page's half into the buffer that this half's P leaves
-                            if (h == 0) {
-                                pass_k(j + stride);
-                                ok = ok && wait_k();
-                                if (!ok) break;
-                            }
-                            qk(h, h == 1 && j + 2 * stride >= nblk);
-                        }
-                        ++n_p;
-                        ++v_at;
-                        if (last) ++n_o;
-                        else ++k_at;
-                    }
-                    pass_k(nblk);
-                    pass_v(nblk);
-                } else if (nblk > 0) {
-                    // no second tile: its issuer only lets the pages go
-                    ok = warp_wait(sh, &sh.q_full, nq & 1);
-                    if (ok && lane == 0) tc::mbar_arrive(&sh.q_empty);
-                    for (int j = 0; j < nblk && ok; ++j) {
-                        ok = wait_k() && wait_v();
-                        if (ok && lane == 0) {
-                            tc::mbar_arrive(&sh.k_empty[rk.slot]);
-                            tc::mbar_arrive(&sh.v_empty[rv.slot]);
-                        }
+                const int own = i < u.tiles ? u.own[i] : 0;
+                const bool dual = u.dual != 0;
+                // pages that this tile does not take only pass by
+                int k_at = 0, v_at = 0;  // next K and V page in the rings
+                auto pass_k = [&](int to) {
+                    for (; k_at < to && ok; ++k_at) {
+                        ok = wait_k();
+                        if (ok && lane == 0) tc::mbar_arrive(&sh.k_empty[rk.slot]);
                         rk.next();
+                    }
+                };
+                auto pass_v = [&](int to) {
+                    for (; v_at < to && ok; ++v_at) {
+                        ok = wait_v();
+                        if (ok && lane == 0) tc::mbar_arrive(&sh.v_empty[rv.slot]);
                         rv.next();
                     }
+                };
+                auto next_own = [&](int j) {
+                    while (!((u.kb[j] >> (kTakeShift + i)) & 1u)) ++j;
+                    return j;
+                };
+                // Pages come in the order K, V, K, V, and a ring holds few: where
+                // more than one passes by, both of each have to, in that order,
+                // or the copies would wait for this warp and it for them.
+                auto pass = [&](int to) {
+                    while (ok && (k_at < to || v_at < to)) {
+                        if (k_at <= v_at) pass_k(k_at + 1);
+                        else pass_v(v_at + 1);
+                    }
+                };
+                if (own > 0 && own == nblk) {
+                    // every page, the common case: nothing but the products
+                    // between one wait and the next
+                    ok = wait_q() && wait_k();
+                    if (!ok) break;
+                    qk(0, false);
+                    qk(1, nblk == 1);
+                    for (int j = 0; j < nblk && ok; ++j) {
+                        const bool last = j == nblk - 1;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (h == 0) ok = wait_v() && (j > 0 || n_o == 0 || warp_wait(sh, &sh.o_free[i], (n_o - 1) & 1));
+                            ok = ok && warp_wait(sh, &sh.p_full[i][h], n_p & 1);
+                            if (!ok) break;
+                            pv(h, j > 0 || h > 0, h == 1 && last);
+                            if (last) continue;
+                            // the next page's half into the buffer that this half's P leaves
+                            if (h == 0) ok = wait_k();
+                            if (!ok) break;
+                            qk(h, h == 1 && j == nblk - 2);
+                        }
+                        ++n_p;
+                    }
+                    ++n_o;
+                    k_at = v_at = nblk;
+                } else if (own > 0) {
+                    int j = dual ? i : next_own(0);
+                    if (j > 1) pass(j);
+                    else pass_k(j);
+                    ok = ok && wait_q() && wait_k();
+                    if (!ok) break;
+                    qk(0, false);
+                    qk(1, own == 1);
+                    ++k_at;
+                    for (int done = 0; done < own && ok; ++done) {
+                        const bool last = done == own - 1;
+                        const int next = last ? nblk : (dual ? j + 2 : next_own(j + 1));
+                        const bool near = !last && next - j <= 2;
+                        pass_v(j);
+                        ok = ok && wait_v() && (done > 0 || n_o == 0 || warp_wait(sh, &sh.o_free[i], (n_o - 1) & 1)) &&
+                             warp_wait(sh, &sh.p_full[i][0], n_p & 1);
+                        if (!ok) break;
+                        pv(0, done > 0, false);
+                        if (near) {
+                            // the next page's half into the buffer that this half's P leaves
+                            pass_k(next);
+                            ok = ok && wait_k();
+                            if (!ok) break;
+                            qk(0, false);
+                        }
+                        ok = warp_wait(sh, &sh.p_full[i][1], n_p & 1);
+                        if (!ok) break;
+                        pv(1, true, last);
+                        ++v_at;
+                        ++n_p;
+                        if (last) {
+                            ++n_o;
+                            break;
+                        }
+                        if (!near) {
+                            pass(next);
+                            ok = ok && wait_k();
+                            if (!ok) break;
+                            qk(0, false);
+                        }
+                        qk(1, done == own - 2);
+                        ++k_at;
+                        j = next;
+                    }
+                } else if (nblk > 0) {
+                    // nothing to multiply: the queries, too, only pass by
+                    ok = warp_wait(sh, &sh.q_full, nq & 1);
+                    if (ok && lane == 0) tc::mbar_arrive(&sh.q_empty);
                 }
+                if (ok) pass(nblk);
                 if (!ok) break;
                 if (nblk > 0) ++nq;
                 warp_arrive(&sh.u_empty[n & 1], lane);
@@ -1164,26 +1217,36 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 const int32_t lim_hi = max(min(pre + pr.i0 + pr.nt, cap), 0);
                 const int vis = (lim_hi + kKeys - 1) / kKeys;  // blocks that the last token sees
                 // blocks of the pair: all that it sees, or the union of its query blocks' selections
-                uint32_t word = 0;  // lane l: blocks 32 l ..
-                int32_t qrow0 = 0, qrow_end = 0, q0 = 0, q1 = 0;
-                if (lane * 32 < vis) word = vis - lane * 32 >= 32 ? 0xffffffffu : (1u << (vis - lane * 32)) - 1u;
+                // lane l holds blocks 32 l ..
+                auto below = [&](int blocks) -> uint32_t {
+                    return lane * 32 >= blocks ? 0u : (blocks - lane * 32 >= 32 ? 0xffffffffu : (1u << (blocks - lane * 32)) - 1u);
+                };
+                const int nt0 = min(pr.nt, t.lay.tt);  // tokens of the first tile
+                uint32_t words[2] = {below(vis), pr.nt > nt0 ? below(vis) : 0u};
+                int32_t qrow0 = 0, qrow_end = 0, mixed = 0;
                 if (a.tk != nullptr) {
-                    q0 = pr.i0 / a.bsq;
-                    q1 = (pr.i0 + pr.nt - 1) / a.bsq;
                     qrow0 = a.cub[pr.b * a.cub_s0];
                     qrow_end = min(a.cub[(pr.b + 1) * a.cub_s0], a.n_rows);
-                    uint32_t any = 0;
-                    if (lane < t.lay.words) {
-                        const uint32_t *bm = reinterpret_cast<const uint32_t *>(t.ws + t.lay.bitmaps) +
-                                             (t.heads_built > 1 ? static_cast<int64_t>(h) : 0) * a.n_rows * t.lay.words + lane;
+                    for (int i = 0; i < 2; ++i) {
+                        // the union of the selections of the tile's query blocks
+                        const int from = i == 0 ? 0 : nt0, to = i == 0 ? nt0 : pr.nt;
+                        if (from >= to) continue;
+                        const int q0 = (pr.i0 + from) / a.bsq, q1 = (pr.i0 + to - 1) / a.bsq;
+                        uint32_t any = 0;
+                        if (lane < t.lay.words) {
+                            const uint32_t *bm = reinterpret_cast<const uint32_t *>(t.ws + t.lay.bitmaps) +
+                                                 (t.heads_built > 1 ? static_cast<int64_t>(h) : 0) * a.n_rows * t.lay.words + lane;
 #pragma unroll 4
-                        for (int q = q0; q <= q1; ++q) {
-                            const int64_t row = static_cast<int64_t>(qrow0) + q;
-                            if (row >= 0 && row < qrow_end) any |= bm[row * t.lay.words];
+                            for (int q = q0; q <= q1; ++q) {
+                                const int64_t row = static_cast<int64_t>(qrow0) + q;
+                                if (row >= 0 && row < qrow_end) any |= bm[row * t.lay.words];
+                            }
                         }
+                        words[i] &= any;
+                        if (q1 > q0) mixed |= 1 << i;
                     }
-                    word &= any;
                 }
+                const uint32_t word = words[0] | words[1];
                 // this piece's share of the list, by rank
                 int before = __popc(word);
                 const int mine = before;
@@ -1196,9 +1259,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 before -= mine;
                 const int r0 = static_cast<int>(static_cast<int64_t>(listed) * piece / pr.pieces);
                 const int r1 = static_cast<int>(static_cast<int64_t>(listed) * (piece + 1) / pr.pieces);
-                int count = 0;
+                int count = 0, own0 = 0, own1 = 0;
                 for (int w = 0; w * 32 < vis; ++w) {
                     const uint32_t ww = __shfl_sync(0xffffffffu, word, w);
+                    const uint32_t w0 = __shfl_sync(0xffffffffu, words[0], w), w1 = __shfl_sync(0xffffffffu, words[1], w);
                     const int wb = __shfl_sync(0xffffffffu, before, w);
                     if (wb >= r1 || wb + __popc(ww) <= r0) continue;
                     const int rank = wb + __popc(ww & ((1u << lane) - 1u));
@@ -1210,9 +1274,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     if (take) {
                         const int at = count + __popc(taken & ((1u << lane) - 1u));
                         u.page[at] = page;
-                        u.kb[at] = static_cast<uint16_t>(w * 32 + lane);
+                        const uint32_t tiles = ((w0 >> lane) & 1u) | (((w1 >> lane) & 1u) << 1);
+                        u.kb[at] = static_cast<uint16_t>((w * 32 + lane) | (tiles << kTakeShift));
                     }
                     count += __popc(taken);
+                    own0 += __popc(taken & w0);
+                    own1 += __popc(taken & w1);
+                }
+                const bool dual = pr.nt <= t.lay.tt && count >= 2;
+                if (dual) {
+                    __syncwarp();
+                    for (int at = lane; at < count; at += 32)
+                        u.kb[at] = static_cast<uint16_t>((u.kb[at] & kBlockMask) | ((1u + (at & 1)) << kTakeShift));
+                    own0 = (count + 1) / 2;
+                    own1 = count / 2;
+                    mixed = mixed ? 3 : 0;
                 }
                 u.marks[lane] = 0;
                 if (lane == 0) {
@@ -1221,19 +1297,19 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     u.i0 = pr.i0;
                     u.nt = pr.nt;
                     u.h = h;
-                    u.dual = pr.nt <= t.lay.tt && count >= 2;
-                    u.tiles = u.dual || pr.nt > t.lay.tt ? 2 : 1;
+                    u.dual = dual;
+                    u.tiles = dual || pr.nt > t.lay.tt ? 2 : 1;
+                    u.own[0] = own0;
+                    u.own[1] = own1;
                     u.pre = pre;
                     u.cap = cap;
                     u.lim_lo = lim_lo;
                     u.lim_hi = lim_hi;
-                    // query blocks without a selection of their own also make the rows differ
-                    u.mixed = a.tk != nullptr && (q1 > q0 || static_cast<int64_t>(qrow0) + q1 >= qrow_end || qrow0 < 0);
+                    u.mixed = mixed;
                     u.qrow0 = qrow0;
                     u.qrow_end = qrow_end;
                     u.pieces = pr.pieces;
                     u.part = h * hd->head_parts + pr.part0 + piece;
-                    u.bt_row = table_row;
                     u.marked = 0;
                     id = static_cast<int32_t>(gridDim.x) + atomicAdd(&hd->next_unit, 1);
                 }
