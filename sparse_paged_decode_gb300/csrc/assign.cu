@@ -19,7 +19,7 @@ namespace spd {
 namespace {
 
 constexpr int kAssignThreads = 512;
-constexpr int kTokensPerCta = 2048;
+constexpr int kTokensPerCta = 512;
 
 __device__ __forceinline__ int32_t clip0(int64_t x, int64_t hi) {
     return static_cast<int32_t>(x < 0 ? 0 : (x > hi ? hi : x));
