@@ -10,6 +10,11 @@
 // CTA 0 the per-request outputs.  A token on a grown block takes its page
 // straight from the free list (the same entry that the table cell gets), so
 // no token waits for the table to be written.
+//
+// What bounds it is latency: a launch and three dependent reads (lengths, the
+// page of a token, the write).  Measured: 4.5 us for 466 tokens of 64 requests,
+// 6.1 us for 65536 tokens of 1024 (0.8 MB, 0.1 us of HBM time; four tokens to a
+// thread, on a quarter of the CTAs, took 8.8 us).
 #include "serve.cuh"
 #include "spd_dispatch.h"
 #include "spd_internal.cuh"

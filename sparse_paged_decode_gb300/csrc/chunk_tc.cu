@@ -3,50 +3,71 @@
 //
 // A CTA works through units of the plan (chunk_plan.cuh): two tiles of 128
 // query rows (128 / G tokens with their G heads each) of one kv head, over a
-// piece of their key blocks, one page of 128 keys at a time:
+// piece of their key blocks.  A page of 128 keys is in shared memory once for
+// both tiles; each tile takes it in two steps of 64 keys:
 //
-//   S_i  = Q_i K^T      tcgen05.mma kind::f16, M = 128 rows, N = 128 keys
-//   P_i  = 2^(S_i c - m) one thread per row; its 128 logits sit in registers,
-//                        so the block maximum and the row sum need no exchange
-//   O_i += P_i V        P from tensor memory (written over its own S), V as it
-//                        lies in the page (MN-major)
+//   S_i  = Q_i K^T       tcgen05.mma, M = 128 rows, N = 64 keys, into one of
+//                        the tile's two tensor-memory buffers
+//   P_i  = 2^(S_i c - m) one thread per row; its 64 logits sit in registers and
+//                        their maximum comes with the tensor-memory load, so
+//                        neither needs an exchange
+//   O_i += P_i V         kind::f16, P from tensor memory (written over its own
+//                        S), V as it lies in the page (MN-major)
 //
-// The two tiles share every K and V page in shared memory and alternate on the
-// tensor pipe, each with an issuing warp of its own: one tile's softmax runs
-// while the other tile's products do.  Products of one issuing thread execute
-// in order: S(j+1) of a tile is written after its P V(j) has read P(j) from
-// the same columns, and whoever sees S(j+1) knows that P V(j) is done.
+// Each tile has a warp that issues its products, in the order P V(k), Q K^T(k +
+// 2) into the buffer that P(k) leaves: a step's logits are there when the last
+// step's softmax ends, and one tile's softmax runs while the other's products
+// do.  Products of one issuing thread run in the order they are issued: S(k +
+// 2) is written after P V(k) has read P(k) from the same columns.  A commit
+// covers everything issued before it, so whoever sees S(k + 2) knows that
+// P V(k) is done.
 //
-// A BF16 cache is multiplied as bf16, straight from the pages.  E4M3 pages are
-// widened to f16 (exact) by a warpgroup of their own, and the queries are made
-// f16 by a power of two per row (exact for elements within 2^38 of their row's
-// largest), which the row's logit factor takes back.
-//
-// A pair of one tile of rows (a short chunk, or the end of one) is worked on by
-// both tiles all the same: each holds the rows, takes every other page and
-// keeps sums of its own, and the first tile joins them at the end (the second
-// one's O lies in the same tensor-memory lanes).  A page then takes half as
-// long, which is what a few rows over a long cache wait for.
+// BF16 pages are multiplied as they are.  E4M3 keys are too, against two E4M3
+// terms of each bf16 query (kind::f8f6f4), and E4M3 values are widened to f16
+// (exact) by a warpgroup of their own; f16 queries, and heads of 64 dims, have
+// their keys widened as well.
 //
 // Softmax: c = sm_scale * k_scale * log2(e) > 0.  The exponent offset m of a
-// row is raised only when a block's maximum exceeds it by more than 2^kRaise
+// row is raised only when a step's maximum exceeds it by more than 2^kRaise
 // (then the row's O is rescaled in tensor memory), so p <= 2^kRaise; p is
-// rounded to the 16-bit type of the products, the row sum is kept in fp32.
+// rounded to the 16-bit type of the products (off by at most 2^-8 of itself in
+// bf16, of either sign, so an output of many keys keeps about the bf16 rounding
+// of its own), the row sum takes it unrounded, in fp32.
+//
+// A tile takes the pages that its own query blocks list (every page without a
+// selection), and passes the other tile's by; only rows of different query
+// blocks within a tile test their own bitmaps.  A pair of one tile of rows (a
+// short chunk, or the end of one) is worked on by both tiles all the same: each
+// holds the rows, takes every other page and keeps sums of its own, and the
+// first tile joins them at the end (the second one's O lies in the same
+// tensor-memory lanes).
 //
 // Keys that a row does not read take p = 0 by its limit, a count of keys.  A
-// product with V would still turn 0 * NaN into NaN, so the V tile of a block
-// that some row of the unit does not read in full is scrubbed in shared memory
-// first: keys that no row reads become zeros, and elements that are not finite
-// become zeros and leave a mark; rows that do read such a key look its
-// elements up in the page at the end and take the NaN or infinity from there.
+// product with V would still turn 0 * NaN into NaN, so the V page of a block
+// that some row does not read in full is scrubbed in shared memory first: keys
+// that no row reads become zeros, and elements that are not finite become zeros
+// and leave a mark; rows that do read such a key look its elements up in the
+// page at the end and take the NaN or infinity from there.
+//
+// What bounds it: the tensor pipe needs 64 cycles for 128 x 128 x 16, 2048 a
+// page and two tiles, but shared memory delivers the operands of N = 64 steps
+// in 48 instead of 32 cycles: 2560.  The exponentials of the page take 1024 on
+// the special-function units of an SM, the softmax of one step about 1000 from
+// logits to P.  Measured (eight 512-token chunks at up to 15872 cached tokens,
+// 64 / 8 heads of 128 dims): 498 us over BF16, 1.44 PFLOP/s, 75 % of the
+// measured bf16 rate; the same chunks over 32 selected E4M3 blocks a query
+// block 365 us, 1.23 PFLOP/s.  Steps of 128 keys with one buffer a tile, where
+// the next product waits for the whole softmax, took 553 and 384 us.  A short
+// chunk waits for latencies: of 62 us for 16 tokens of four requests over 14000
+// keys (18 us of HBM time) 6 are the plan, 11 the first unit's records, page
+// list and queries, 6 the join.
 //
 // Roles (16 warps): warps 0-3 and 4-7 the softmax and epilogue of tile 0 and 1
-// (warp w reads TMEM lanes 32 (w % 4) .. +31), warps 8-11 widen (E4M3) and
-// scrub, warp 12 issues the TMA loads, warps 13 and 15 the products of tile 0
-// and 1 (warp 13 owns tensor memory), warp 14 claims units and builds their
-// page lists one unit ahead.
-// Every wait is bounded: one that gives up sets bit 0 of the workspace status
-// word and the CTA winds down.
+// (warp w reads TMEM lanes 32 (w % 4) .. +31), warps 8-11 split queries, widen
+// and scrub, warp 12 issues the TMA loads, warps 13 and 15 the products of tile
+// 0 and 1 (warp 13 owns tensor memory), warp 14 claims units and builds their
+// page lists one unit ahead.  Every wait is bounded: one that gives up sets bit
+// 0 of the workspace status word and the CTA winds down.
 #include <math.h>
 
 #include <cuda_bf16.h>
@@ -64,8 +85,8 @@ namespace spd {
 namespace {
 
 constexpr int kRows = 128;           // query rows of a tile (M)
-constexpr int kKeys = kBlock;        // keys of a block (N of S, K of P V)
-constexpr int kHalf = kKeys / 2;     // keys of a softmax step
+constexpr int kKeys = kBlock;        // keys of a page
+constexpr int kHalf = kKeys / 2;     // keys of a step (N of S, K of P V)
 constexpr int kThreads = 512;
 constexpr int kWarpSide = 8, kWarpTma = 12, kWarpMma = 13, kWarpSched = 14, kWarpMma1 = 15;
 constexpr int kBox = 128 * 128;      // 64 dims of 128 rows of a 16-bit type, bytes
@@ -77,13 +98,13 @@ constexpr uint32_t kRegsSoft = 152, kRegsOther = 104;
 static_assert(256 * kRegsSoft + 256 * kRegsOther <= kThreads * 128, "register split");
 constexpr uint32_t kUnitReleases = 8 + 4 + 1 + 2;  // warps that read a unit record
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;         // S_i at 128 i, O_i at 256 + 128 i
+constexpr uint32_t kColS = 0, kColO = 256;         // S_i at 128 i (two buffers of 64), O_i at 256 + 128 i
 
 // How a cache is multiplied.
 enum Mode {
     kModeBf16,   // BF16 pages as they are, bf16 queries
     kModeTerms,  // E4M3: K as it is against two E4M3 terms of each bf16 query, V widened to f16
-    kModeWide    // E4M3: K and V widened to f16, f16 queries
+    kModeWide    // E4M3: K and V widened to f16, f16 queries (bf16 ones made f16)
 };
 
 template <int D, Mode M>
@@ -991,11 +1012,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             }
         } else if (warp == kWarpMma || warp == kWarpMma1) {
             // ----------------------------------------------- MMA issuers
-            // One warp per tile: a product takes 512 tensor cycles and the
-            // pipe's queue holds few instructions, so what a warp does between
-            // two products (waits, commits: 100 to 300 cycles) would leave the
-            // pipe idle if the other tile's products did not fill it.  The
-            // whole warp waits and counts, one elected lane issues.
+            // One warp per tile: a product takes 256 to 384 tensor cycles and
+            // the pipe's queue holds few instructions, so what a warp does
+            // between two products (waits, commits: 100 to 300 cycles) would
+            // leave the pipe idle if the other tile's products did not fill
+            // it.  The whole warp waits and counts, one elected lane issues.
             const int i = warp == kWarpMma ? 0 : 1;
             const uint32_t idesc_s = M == kModeTerms ? tc::idesc_m128(kHalf, false, false) : tc::idesc_f16_m128(kHalf, kBf16);
             const uint32_t idesc_o = tc::idesc_f16_m128(D, kBf16) | (1u << 16);  // B (V) MN-major

@@ -3,7 +3,9 @@
 //
 // A head row of D elements is read once, normalised and rotated in fp32 and
 // written once, rounded to the type it is kept in: the call moves its inputs
-// and outputs and nothing else, so HBM bandwidth bounds it.
+// and outputs and nothing else, so HBM bandwidth bounds it.  Measured, 64 + 8 +
+// 8 rows of 128 dims a token into E4M3 caches: 62.5 us for 8192 tokens (323 MB,
+// 76 % of the measured copy bandwidth), 6.3 us for 466.
 #include "f32x2.cuh"
 #include "serve.cuh"
 #include "spd_dispatch.h"
@@ -121,8 +123,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32) store_generic_kernel(const S
 // and one K or V row at a time, loaded before the first is used and without
 // waiting for the token's length.  Instructions, then HBM, bound the kernel:
 // with the partner in another lane and the weights applied row by row it took
-// 180 instructions a warp and row pair and 74 us for 8192 tokens of 64 + 16
-// rows of 128 dims (323 MB).
+// 180 instructions a warp and row pair, and 74 us for the 8192 tokens.
 constexpr int kVecThreads = 256;
 constexpr int kVecCtas = 3;  // on an SM
 constexpr int kQRows = 4;
