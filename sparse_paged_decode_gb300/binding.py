@@ -386,6 +386,8 @@ def _scratch(ws, device):
         return None, 0
     if not isinstance(ws, torch.Tensor) or ws.get_device() != device:
         raise TypeError("workspace must be a CUDA tensor on the current device")
+    if not ws.is_contiguous():  # its bytes are used as one run
+        raise ValueError("workspace must be contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 

@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(kThreads) chunk_generic_kernel(const ChunkArgs
         }
         __syncthreads();
         if (tid < n_valid)
-            for (int g = 0; g < G; ++g) ps[g][tid] = expf(ps[g][tid] - m_run[g]);
+            // logits of -inf weigh nothing, also where the row has no others yet
+            for (int g = 0; g < G; ++g) ps[g][tid] = ps[g][tid] == -INFINITY ? 0.f : expf(ps[g][tid] - m_run[g]);
         __syncthreads();
         if (tid < G) {
             float s = 0.f;

@@ -342,6 +342,8 @@ __device__ __forceinline__ bool finite_bits(uint32_t x, bool bf16) {
 
 // The largest magnitude of one bf16 query row of D dims in its swizzled tile,
 // as the power of two that brings it to [2^top, 2^(top + 1)), and the inverse.
+// A row with an infinity or a NaN is multiplied by NaN: its logits are infinite
+// or NaN, so no softmax of it is finite, and E4M3 has no infinity to hold.
 template <int D>
 __device__ __forceinline__ void row_power(const uint8_t *q, int row, int top, float &up, float &down) {
     uint32_t m = 0;
@@ -354,7 +356,7 @@ __device__ __forceinline__ void row_power(const uint8_t *q, int row, int top, fl
         }
     const int e = static_cast<int>(max(m & 0xffffu, m >> 16) >> 7);  // biased exponent
     const int shift = e == 0 ? 0 : min(top - (e - 127), 100);
-    up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+    up = e == 255 ? NAN : __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
     down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
 }
 
@@ -690,11 +692,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 ++n_s;
             }
             if (!ok) break;
-            // a row that reads keys whose logits are all -inf (or NaN) has no
-            // finite softmax: NaN, as the formula gives
-            if (seen && m_run == -INFINITY) {
-                m_run = 0.f;
-                l = NAN;
+            // a row without an offset: it read nothing (l = 0, zeros); NaN
+            // logits (l is NaN, and stays so with any offset); or keys whose
+            // logits are all -inf, which weigh nothing beside other keys but
+            // have no softmax of their own: marked by l = 1
+            if (m_run == -INFINITY && seen) {
+                if (l == 0.f) l = 1.f;
+                else m_run = 0.f;
             }
 
             // ------------------------------------------------- epilogue
@@ -725,6 +729,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     w_other = tc::ex2(other.x - m);
                     l = l * w_own + other.y * w_other;  // a NaN stays one, whatever its weight
                     m_run = m;
+                } else {
+                    l += other.y;
                 }
             }
             if (own > 0 && u.marked != 0) take_marked<D, F8>(t, u, tile, have && chosen ? lim : 0, bits, col_o);
@@ -734,7 +740,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (u.tok0 + j_tok) * a.o_s0 +
                                  static_cast<int64_t>(u.h * t.G + g) * a.o_s1;
             const bool vec = a.o_s2 == 1 && (reinterpret_cast<uintptr_t>(out) & 31) == 0;
-            const float f = none ? 0.f : a.v_scale / l;
+            const float f = none ? (l > 0.f ? NAN : 0.f) : a.v_scale / l;
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 64) {
                 float o[64];
@@ -1389,9 +1395,9 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 #pragma unroll
         for (int d = kJoinLanes / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
         for (int p = lane % kJoinLanes; p < pr.pieces; p += kJoinLanes)
-            if (mine && M != -INFINITY) {
+            if (mine) {
                 const float2 s = stats[p * 256 + own];
-                L += s.y * tc::ex2(s.x - M);  // a NaN stays one, whatever its weight
+                L += M == -INFINITY ? s.y : s.y * tc::ex2(s.x - M);  // a NaN stays one, whatever its weight
             }
 #pragma unroll
         for (int d = kJoinLanes / 2; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
@@ -1413,7 +1419,8 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) o[e] = fmaf(x[e], w, o[e]);
             }
-            const float f = m == -INFINITY ? 0.f : a.v_scale / l;
+            // without an offset: nothing read, or logits that are all -inf
+            const float f = m == -INFINITY ? (l > 0.f ? NAN : 0.f) : a.v_scale / l;
             const int g = ((r0 + i) & 127) % t.G;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + static_cast<int64_t>(pr.tok0 + j) * a.o_s0 +
                                  static_cast<int64_t>(h * t.G + g) * a.o_s1;

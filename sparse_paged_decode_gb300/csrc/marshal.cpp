@@ -111,6 +111,10 @@ struct Args {
             return nullptr;
         }
         const at::Tensor &t = THPVariable_Unpack(o);
+        if (!t.is_contiguous()) {  // its bytes are used as one run
+            fail(PyExc_ValueError, "%s must be contiguous", "workspace");
+            return nullptr;
+        }
         *bytes = t.nbytes();
         return t.data_ptr();
     }

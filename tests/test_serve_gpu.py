@@ -676,3 +676,89 @@ def test_serving_steps(spd, cache):
                                  topk if sparse else None, bq, cub)
             R.check_attention(o, ref, A, "step %d %s" % (step, "sparse" if sparse else "dense"))
         prefix = R.ints(sl).tolist()
+
+
+# ------------------------------------------------ what is read and not finite
+
+
+def held(spd, s, what):
+    """A run whose rows are NaN exactly where the 64-bit definition's are, and
+    within the usual bounds elsewhere."""
+    got = run_chunk(spd, s, check=False).float().cpu().numpy().astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        ref, A = R.attention(s["q"], s["kc"], s["vc"], s["table"], s["rows"], torch.tensor(s["cu"]),
+                             torch.tensor(s["seq_lens"]), torch.tensor(s["prefix"]), s["sm"], s["ks"], s["vs"], s.get("topk"),
+                             s["bq"], None if not s["bq"] else torch.tensor(s["cub"]))
+    nan = np.isnan(ref)
+    assert np.array_equal(np.isnan(got), nan), what + ": NaN pattern"
+    R.check_attention(torch.from_numpy(np.where(nan, 0.0, got)), np.where(nan, 0.0, ref), np.where(nan, 0.0, A), what)
+    return nan
+
+
+@pytest.mark.parametrize("pol", [0, 1])
+@pytest.mark.parametrize("kind", ["e4m3", "e4m3_f16", "e4m3_d64", "bf16"])
+@pytest.mark.parametrize("bq", [0, 8], ids=["dense", "bq8"])
+def test_infinite_queries(spd, bq, kind, pol):
+    """A query row with an infinity has no finite softmax: NaN, and nothing
+    in its neighbours.  One that reads no key stays zero."""
+    D = 64 if kind == "e4m3_d64" else 128
+    s = chunk_inputs([30, 12, 5], [300, 0, 40], 16, 2, D, F16 if kind == "e4m3_f16" else BF16,
+                     BF16 if kind == "bf16" else E4M3, 120, bq=bq, topk=2)
+    s["rows"][2] = -1
+    inf = float("inf")
+    s["q"][3, 5, 7], s["q"][17, 0, 0], s["q"][33, 15, D - 1] = inf, -inf, inf
+    s["q"][20, 9, ::2] = -inf
+    s["q"][44, 3, 1] = inf  # of the request that reads nothing
+    with policy(spd, pol):
+        nan = held(spd, s, "infinite queries")
+    rows = nan.any(-1)
+    assert rows.sum() == 4 and rows[3, 5] and rows[17, 0] and rows[33, 15] and rows[20, 9]
+
+
+@pytest.mark.parametrize("pol", [0, 1])
+@pytest.mark.parametrize("bq", [0, 8], ids=["dense", "bq8"])
+@pytest.mark.parametrize("chunk", [9, 40])
+def test_keys_of_minus_infinity(spd, chunk, bq, pol):
+    """Logits of -inf weigh nothing beside others, wherever the keys are cut
+    into steps, pages, tiles and pieces; a row with no others is NaN."""
+    prefix = 1500
+    s = chunk_inputs([chunk, chunk], [prefix, 260], 16, 2, 128, BF16, BF16, 121, bq=bq, topk=4)
+    s["q"] = s["q"].abs() + 0.125  # times -inf: -inf, never NaN
+    own = [o.tolist() for o in s["owned"][:2]]
+    for b, blocks in ((0, (0, 1, 2, 5, 6, 11)), (1, (0, 1))):
+        for kb in blocks:
+            s["kc"][own[b][kb] * BS:(own[b][kb] + 1) * BS, :, 3] = -float("inf")
+    at = own[1][2] * BS  # the second request's third block up to its fifth new token: rows without another key
+    s["kc"][at:at + 4 + 5, 1, 3] = -float("inf")
+    with policy(spd, pol):
+        nan = held(spd, s, "keys of -inf")
+    if not bq:  # selections may hold nothing but such keys, too
+        assert not nan[:chunk].any() and not nan[:, :8].any()
+        assert nan[chunk:chunk + 5, 8:].all() and not nan[chunk + 5:].any()
+
+
+@pytest.mark.parametrize("bq", [0, 1], ids=["dense", "bq1"])
+@pytest.mark.parametrize("B", [600, 1500, 8192])
+def test_prefill_attention_many_sequences(spd, B, bq):
+    """More sequences than are ranked by length, and than have their pairs in
+    shared memory, up to the most that a call takes."""
+    r = random.Random(B)
+    chunks = [r.choice((0, 1, 1, 1, 2)) for _ in range(B)]
+    prefix = [r.choice((0, 3, 60, 127)) for _ in chunks]
+    s = chunk_inputs(chunks, prefix, 2, 1, 64, BF16, BF16, 122, NB=2, bq=bq, topk=2)
+    run_chunk(spd, s, what="%d sequences" % B)
+
+
+def test_workspace_must_be_one_run(spd, monkeypatch):
+    from sparse_paged_decode_gb300 import binding
+
+    s = chunk_inputs([4], [10], 16, 2, 128, BF16, BF16, 123)
+    args = [s[n].to(DEV) for n in ("q", "kc", "vc", "table", "rows")] + [i32(s[n]) for n in ("cu", "seq_lens", "prefix")]
+    out = nan_like(s["q"].shape, BF16, DEV)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV).expand(1 << 20, 256)
+    for way in {binding._fast, None}:
+        monkeypatch.setattr(binding, "_fast", way)
+        with pytest.raises(ValueError):
+            spd.paged_prefill_attention(*args, out, s["sm"], BS, 1.0, 1.0, ws)
+    torch.cuda.synchronize()
+    assert torch.isnan(out.float()).all(), "a refused call wrote its output"
