@@ -254,13 +254,14 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
             const int at = place(q, r.i0, r.nt);
             r.b = order[at];
             r.tok0 = start[r.b] + r.i0;
-            r.cost = costs[q];
-            r.unit0 = unit0[q];
-            r.pieces = k;
+            r.key.unit0 = unit0[q];
+            r.key.pieces = k;
+            r.key.seq0 = unit0[min(max(poff[at], 0), n_pairs - 1)];
+            r.key.seq_units = (poff[at + 1] < n_pairs ? unit0[max(poff[at + 1], 0)] : ucarry) - r.key.seq0;
             r.part0 = pcarry + kp;
-            r.seq0 = unit0[min(max(poff[at], 0), n_pairs - 1)];
-            r.seq_units = (poff[at + 1] < n_pairs ? unit0[max(poff[at + 1], 0)] : ucarry) - r.seq0;
-            r.reserved[0] = r.reserved[1] = 0;
+            r.row = a.sid[r.b * a.sid_s0];
+            r.pre = pre[r.b];
+            r.cap = cap[r.b];
             pairs[q] = r;
             if (k > 1) splits[scarry + ks] = q;
         }

@@ -35,18 +35,24 @@ struct ChunkHeader {
 };
 static_assert(sizeof(ChunkHeader) == 256, "header is one 256-byte line");
 
+// What a search over the pairs and the unit's place need first, in one load.
+struct ChunkKey {
+    int32_t unit0;   // first unit within a head, over all sequences
+    int32_t seq0;    // unit0 of the sequence's first pair
+    int32_t seq_units;  // units of the sequence within a head
+    int32_t pieces;
+};
+
 struct ChunkPair {
+    ChunkKey key;
     int32_t b;       // sequence
     int32_t i0;      // first token of the pair within its chunk
     int32_t nt;      // tokens
-    int32_t cost;    // key blocks expected
-    int32_t unit0;   // first unit within a head, over all sequences
-    int32_t pieces;
-    int32_t part0;   // first partial slot within a head (split pairs)
     int32_t tok0;    // first query token
-    int32_t seq0;    // unit0 of the sequence's first pair
-    int32_t seq_units;  // units of the sequence within a head
-    int32_t reserved[2];
+    int32_t part0;   // first partial slot within a head (split pairs)
+    int32_t row;     // page-table row of the sequence (any, where cap is 0)
+    int32_t pre;     // cached keys
+    int32_t cap;     // keys in all, at most what the table holds
 };
 static_assert(sizeof(ChunkPair) == 48, "pair record is 48 bytes");
 

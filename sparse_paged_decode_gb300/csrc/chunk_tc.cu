@@ -1204,18 +1204,23 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         } else if (warp == kWarpSched) {
             // ---------------------------------------------- units, page lists
             const ChunkPair *pairs = reinterpret_cast<const ChunkPair *>(t.ws + t.lay.pairs);
-            const int32_t n_units = hd->n_units, n_pairs = hd->n_pairs;
-            // the pair whose units of one head hold v, by 32-way search
-            auto pair_of = [&](int32_t v) {
+            const int32_t n_units = hd->n_units, n_pairs = hd->n_pairs, head_parts = hd->head_parts;
+            // the pair whose units of one head hold v, and its key, by 32-way search
+            auto pair_of = [&](int32_t v, ChunkKey &key) {
                 int lo = 0, span = n_pairs;
-                while (span > 1) {
+                do {
                     const int step = (span + 31) / 32, at = lo + lane * step;
-                    const bool below = lane * step < span && pairs[at].unit0 <= v;
-                    const int last = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // lane 0 is below
-                    const int from = max(last, 0) * step;
-                    lo += from;
-                    span = min(step, span - from);
-                }
+                    int4 k = make_int4(0, 0, 0, 0);
+                    if (lane * step < span) k = *reinterpret_cast<const int4 *>(&pairs[at].key);
+                    const bool below = lane * step < span && k.x <= v;
+                    const int last = max(__popc(__ballot_sync(0xffffffffu, below)) - 1, 0);  // lane 0 is below
+                    key.unit0 = __shfl_sync(0xffffffffu, k.x, last);
+                    key.seq0 = __shfl_sync(0xffffffffu, k.y, last);
+                    key.seq_units = __shfl_sync(0xffffffffu, k.z, last);
+                    key.pieces = __shfl_sync(0xffffffffu, k.w, last);
+                    lo += last * step;
+                    span = min(step, span - last * step);
+                } while (span > 1);
                 return lo;
             };
             int32_t id = blockIdx.x;
@@ -1231,15 +1236,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     break;
                 }
                 // sequence, then head, then the unit among the sequence's
-                const ChunkPair *some = pairs + pair_of(id / a.Hkv);
-                const int32_t rest = id - some->seq0 * a.Hkv;
-                const int h = rest / some->seq_units, v = some->seq0 + rest % some->seq_units;
-                const ChunkPair pr = pairs[pair_of(v)];
-                const int piece = v - pr.unit0;
-                const int32_t table_row = a.sid[pr.b * a.sid_s0];
-                const bool in_table = table_row >= 0 && table_row < a.R;
-                const int32_t pre = min(max(a.pre[pr.b * a.pre_s0], -(1 << 30)), 1 << 30);
-                const int32_t cap = in_table ? min(a.sl[pr.b * a.sl_s0], a.NB * kKeys) : 0;
+                // (each load that waits for another costs the first unit 0.4 us:
+                // a search brings the key along, a pair record all of its sequence)
+                ChunkKey key;
+                pair_of(id / a.Hkv, key);
+                const int32_t rest = id - key.seq0 * a.Hkv;
+                const int h = rest / key.seq_units, v = key.seq0 + rest % key.seq_units;
+                const ChunkPair pr = pairs[pair_of(v, key)];
+                const int piece = v - key.unit0, pieces = key.pieces;
+                const int32_t table_row = pr.row, pre = pr.pre, cap = pr.cap;
                 const int32_t lim_lo = max(min(pre + pr.i0 + 1, cap), 0);
                 const int32_t lim_hi = max(min(pre + pr.i0 + pr.nt, cap), 0);
                 const int vis = (lim_hi + kKeys - 1) / kKeys;  // blocks that the last token sees
@@ -1284,8 +1289,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 }
                 const int listed = __shfl_sync(0xffffffffu, before, 31);
                 before -= mine;
-                const int r0 = static_cast<int>(static_cast<int64_t>(listed) * piece / pr.pieces);
-                const int r1 = static_cast<int>(static_cast<int64_t>(listed) * (piece + 1) / pr.pieces);
+                const int r0 = static_cast<int>(static_cast<int64_t>(listed) * piece / pieces);
+                const int r1 = static_cast<int>(static_cast<int64_t>(listed) * (piece + 1) / pieces);
                 int count = 0, own0 = 0, own1 = 0;
                 for (int w = 0; w * 32 < vis; ++w) {
                     const uint32_t ww = __shfl_sync(0xffffffffu, word, w);
@@ -1335,12 +1340,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     u.mixed = mixed;
                     u.qrow0 = qrow0;
                     u.qrow_end = qrow_end;
-                    u.pieces = pr.pieces;
-                    u.part = h * hd->head_parts + pr.part0 + piece;
+                    u.pieces = pieces;
+                    u.part = h * head_parts + pr.part0 + piece;
                     u.marked = 0;
-                    id = static_cast<int32_t>(gridDim.x) + atomicAdd(&hd->next_unit, 1);
                 }
                 warp_arrive(&sh.u_full[n & 1], lane);
+                if (lane == 0) id = static_cast<int32_t>(gridDim.x) + atomicAdd(&hd->next_unit, 1);
                 id = __shfl_sync(0xffffffffu, id, 0);
             }
         }
@@ -1390,11 +1395,11 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
         const int own = lane / kJoinLanes;
         const bool mine = token(r0 + own) >= 0;
         float M = -INFINITY, L = 0.f;
-        for (int p = lane % kJoinLanes; p < pr.pieces; p += kJoinLanes)
+        for (int p = lane % kJoinLanes; p < pr.key.pieces; p += kJoinLanes)
             if (mine) M = fmaxf(M, stats[p * 256 + own].x);
 #pragma unroll
         for (int d = kJoinLanes / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        for (int p = lane % kJoinLanes; p < pr.pieces; p += kJoinLanes)
+        for (int p = lane % kJoinLanes; p < pr.key.pieces; p += kJoinLanes)
             if (mine) {
                 const float2 s = stats[p * 256 + own];
                 L += M == -INFINITY ? s.y : s.y * tc::ex2(s.x - M);  // a NaN stays one, whatever its weight
@@ -1410,7 +1415,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 #pragma unroll
             for (int e = 0; e < kPer; ++e) o[e] = 0.f;
 #pragma unroll 4
-            for (int p = 0; p < pr.pieces; ++p) {
+            for (int p = 0; p < pr.key.pieces; ++p) {
                 const float w = m == -INFINITY ? 0.f : tc::ex2(stats[p * 256 + i].x - m);
                 const float *src = parts + (static_cast<int64_t>(p) * 256 + i) * D;
                 float x[kPer];
