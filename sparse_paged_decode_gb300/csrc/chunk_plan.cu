@@ -77,7 +77,7 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     ChunkHeader *hd = reinterpret_cast<ChunkHeader *>(p.ws + p.lay.header);
     ChunkPair *pairs = reinterpret_cast<ChunkPair *>(p.ws + p.lay.pairs);
-    int32_t *splits = reinterpret_cast<int32_t *>(p.ws + p.lay.splits);
+    ChunkSplit *splits = reinterpret_cast<ChunkSplit *>(p.ws + p.lay.splits);
     // per sequence: first token, tokens, cached keys, keys in all; order by
     // length, and pair offsets in that order
     int32_t *start = dyn, *n_tok = start + a.B, *pre = n_tok + a.B, *cap = pre + a.B, *order = cap + a.B, *poff = order + a.B;
@@ -263,7 +263,7 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
             r.pre = pre[r.b];
             r.cap = cap[r.b];
             pairs[q] = r;
-            if (k > 1) splits[scarry + ks] = q;
+            if (k > 1) *reinterpret_cast<int4 *>(&splits[scarry + ks]) = make_int4(r.tok0, r.nt, k, r.part0);
         }
         pcarry += ptotal;
         scarry += stotal;

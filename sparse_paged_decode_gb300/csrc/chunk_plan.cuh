@@ -56,6 +56,11 @@ struct ChunkPair {
 };
 static_assert(sizeof(ChunkPair) == 48, "pair record is 48 bytes");
 
+// A pair in more than one piece, for the join.
+struct ChunkSplit {
+    int32_t tok0, nt, pieces, part0;
+};
+
 constexpr int kChunkMaxParts = 608;  // partial slots: four pieces per SM of a 152-SM device
 
 // Byte layout of the workspace for capacities.
@@ -78,7 +83,7 @@ struct ChunkLayout {
         size_t off = 0;
         header = off;   off += align(sizeof(ChunkHeader));
         pairs = off;    off += align(sizeof(ChunkPair) * (size_t)pair_cap);
-        splits = off;   off += align(sizeof(int32_t) * (size_t)pair_cap);
+        splits = off;   off += align(sizeof(ChunkSplit) * (size_t)pair_cap);
         pair_tmp = off; off += align(sizeof(int32_t) * 2 * (size_t)pair_cap);
         bitmaps = off;  off += align(sizeof(uint32_t) * (size_t)Hkv * (size_t)n_rows * (size_t)words);
         stats = off;    off += align(sizeof(float) * 2 * (size_t)part_cap * 256);

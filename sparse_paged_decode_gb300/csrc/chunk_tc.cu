@@ -1372,17 +1372,24 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
     tc::pdl_wait();
     const ChunkArgs &a = t.a;
     const ChunkHeader *hd = reinterpret_cast<const ChunkHeader *>(t.ws + t.lay.header);
-    const ChunkPair *pairs = reinterpret_cast<const ChunkPair *>(t.ws + t.lay.pairs);
-    const int32_t *splits = reinterpret_cast<const int32_t *>(t.ws + t.lay.splits);
+    const int4 *splits = reinterpret_cast<const int4 *>(t.ws + t.lay.splits);  // of ChunkSplit
     const int lane = threadIdx.x & 31;
     constexpr int kGroups = 256 / kJoinRows;  // of a pair and head
-    const int64_t groups = static_cast<int64_t>(hd->n_splits) * a.Hkv * kGroups;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
+    // the first record is on its way with the header, whether there is one or not
+    // (at most kChunkMaxParts / 2 pairs and heads are split)
+    uint32_t k = blockIdx.x * 8 + (threadIdx.x >> 5);
+    auto record = [&](uint32_t at) {
+        const uint32_t i = at / kGroups / a.Hkv;
+        return i < t.lay.pair_cap ? splits[i] : make_int4(0, 0, 0, 0);
+    };
+    int4 next = record(k);
+    const uint32_t groups = hd->n_splits * a.Hkv * kGroups, stride = gridDim.x * 8;
     constexpr int kPer = D / 32;
-    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); k < groups; k += stride) {
+    for (; k < groups; k += stride) {
         const int r0 = static_cast<int>(k % kGroups) * kJoinRows;
         const int h = static_cast<int>((k / kGroups) % a.Hkv);
-        const ChunkPair pr = pairs[splits[k / kGroups / a.Hkv]];
+        const ChunkSplit pr = {next.x, next.y, next.z, next.w};
+        next = record(k + stride);
         auto token = [&](int r) {  // of the pair, or -1 where the row holds none
             const int j = (r >> 7) * t.lay.tt + (r & 127) / t.G;
             return (r & 127) < t.lay.tt * t.G && j < pr.nt ? j : -1;
@@ -1395,11 +1402,11 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
         const int own = lane / kJoinLanes;
         const bool mine = token(r0 + own) >= 0;
         float M = -INFINITY, L = 0.f;
-        for (int p = lane % kJoinLanes; p < pr.key.pieces; p += kJoinLanes)
+        for (int p = lane % kJoinLanes; p < pr.pieces; p += kJoinLanes)
             if (mine) M = fmaxf(M, stats[p * 256 + own].x);
 #pragma unroll
         for (int d = kJoinLanes / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        for (int p = lane % kJoinLanes; p < pr.key.pieces; p += kJoinLanes)
+        for (int p = lane % kJoinLanes; p < pr.pieces; p += kJoinLanes)
             if (mine) {
                 const float2 s = stats[p * 256 + own];
                 L += M == -INFINITY ? s.y : s.y * tc::ex2(s.x - M);  // a NaN stays one, whatever its weight
@@ -1415,7 +1422,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 #pragma unroll
             for (int e = 0; e < kPer; ++e) o[e] = 0.f;
 #pragma unroll 4
-            for (int p = 0; p < pr.key.pieces; ++p) {
+            for (int p = 0; p < pr.pieces; ++p) {
                 const float w = m == -INFINITY ? 0.f : tc::ex2(stats[p * 256 + i].x - m);
                 const float *src = parts + (static_cast<int64_t>(p) * 256 + i) * D;
                 float x[kPer];
