@@ -304,15 +304,32 @@ __device__ __forceinline__ bool elect_one() {
 
 __device__ __forceinline__ bool aborted(Shared &sh) { return *reinterpret_cast<volatile int *>(&sh.abort) != 0; }
 
+// Waits for the phase with the given parity; false once kWaitTries tries have
+// failed, 0.1 s or more (a unit of the longest request takes 2 ms).  Counting
+// the tries instead of reading a clock keeps the waits short in instructions,
+// whose fetching bounds the kernel beside the tensor pipe: with a clock read
+// in each (eight warps' roles, some thirty places) dense bf16 took 489 instead
+// of 466 us, ragged E4M3 108 instead of 98.
+constexpr uint32_t kWaitTries = 1u << 22;
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kWaitTries; ++i) {
+        __nanosleep(30);
+        if (tc::mbar_try_wait(bar, parity)) return true;
+    }
+    return false;
+}
+
 __device__ __forceinline__ bool wait_or_abort(Shared &sh, uint64_t *bar, uint32_t parity) {
-    if (tc::mbar_wait(bar, parity)) return true;
+    if (bar_wait(bar, parity)) return true;
     *reinterpret_cast<volatile int *>(&sh.abort) = 1;
     return false;
 }
 
 // Warp-uniform wait, for the warp-collective accesses that follow it.
 __device__ __forceinline__ bool warp_wait(Shared &sh, uint64_t *bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity));
+    const bool ok = __all_sync(0xffffffffu, bar_wait(bar, parity));
     if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
     return ok;
 }
@@ -593,6 +610,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             uint32_t word = 0;
             // Half a page, 64 keys, is a step of the online softmax.  Its logits
             // lie in one of two buffers, and its P goes over them.
+            // (Two copies of a step cost the fetching of their instructions, one
+            // costs the addresses: dense bf16 465 us with two, 486 with one, over
+            // E4M3, where the queries' terms and the widening want the
+            // instruction cache too, ragged 98 and 95, drawn small batches 2 %.)
+            constexpr int kUnrolled = kBf16 ? 2 : 1;
             for (int j = 0, done = 0; done < own && ok; ++j) {
                 const uint32_t entry = u.kb[j];
                 if (!((entry >> (kTakeShift + tile)) & 1u)) continue;  // the other tile's page
@@ -607,7 +629,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 }
                 seen |= left > 0;
                 const bool partial = mixed || (kb + 1) * kKeys > u.lim_lo;  // some row does not read it all
-#pragma unroll
+#pragma unroll kUnrolled
                 for (int h = 0; h < 2; ++h) {
                     ok = warp_wait(sh, &sh.s_full[tile][h], n_s & 1);
                     if (!ok) break;
@@ -1003,12 +1025,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 // every issued copy lands before the CTA may exit; only after
                 // an abort can one still be in flight
                 if (!ok) {
-                    if (nq > 0) tc::mbar_wait(&sh.q_full, (nq - 1) & 1);
+                    if (nq > 0) bar_wait(&sh.q_full, (nq - 1) & 1);
                     auto landed = [&](const auto &ring, uint64_t *full, int slots) {
                         for (int i = 0; i < slots; ++i) {
                             // the last round of slot i that was begun
                             const uint32_t rounds = ring.round + (static_cast<uint32_t>(i) < ring.slot ? 1 : 0);
-                            if (rounds > 0) tc::mbar_wait(&full[i], (rounds - 1) & 1);
+                            if (rounds > 0) bar_wait(&full[i], (rounds - 1) & 1);
                         }
                     };
                     if (M != kModeWide) landed(rk, sh.k_full, S::kKs);
@@ -1200,7 +1222,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             // every issued product completes before tensor memory is released
             if (elect_one()) tc::mma_commit(&sh.drain[i]);
             __syncwarp();
-            tc::mbar_wait(&sh.drain[i], 0);
+            bar_wait(&sh.drain[i], 0);
         } else if (warp == kWarpSched) {
             // ---------------------------------------------- units, page lists
             const ChunkPair *pairs = reinterpret_cast<const ChunkPair *>(t.ws + t.lay.pairs);
