@@ -279,7 +279,10 @@ __device__ void plan_batch(const ChunkPlanArgs &p) {
 }
 
 __global__ void __launch_bounds__(kPlanT) chunk_plan_kernel(const __grid_constant__ ChunkPlanArgs p) {
-
+    // the attention kernel may take the free SMs and set itself up; it waits
+    // for this kernel's end before it reads global memory (sparse bf16, 1111
+    // tokens, 67.5 -> 62.0 us; sparse E4M3, 4096 tokens, 344 -> 346)
+    tc::pdl_trigger();
     if (blockIdx.x == 0) {
         plan_batch(p);
         return;
