@@ -53,14 +53,19 @@
 // page and two tiles, but shared memory delivers the operands of N = 64 steps
 // in 48 instead of 32 cycles: 2560.  The exponentials of the page take 1024 on
 // the special-function units of an SM, the softmax of one step about 1000 from
-// logits to P.  Measured (eight 512-token chunks at up to 15872 cached tokens,
-// 64 / 8 heads of 128 dims): 498 us over BF16, 1.44 PFLOP/s, 75 % of the
-// measured bf16 rate; the same chunks over 32 selected E4M3 blocks a query
-// block 365 us, 1.23 PFLOP/s.  Steps of 128 keys with one buffer a tile, where
-// the next product waits for the whole softmax, took 553 and 384 us.  A short
-// chunk waits for latencies: of 62 us for 16 tokens of four requests over 14000
-// keys (18 us of HBM time) 6 are the plan, 11 the first unit's records, page
-// list and queries, 6 the join.
+// logits to P.  Beside the pipe it is the fetching of instructions: sixteen
+// warps run a dozen roles' code, so waits, steps and epilogues are kept short
+// (where each measured, it is said there).  Measured (eight 512-token chunks at
+// up to 15872 cached tokens, 64 / 8 heads of 128 dims): 463 us over BF16, 1.55
+// PFLOP/s, 81 % of the measured bf16 rate; the same chunks over 32 selected
+// E4M3 blocks a query block 344 us, 1.30 PFLOP/s.  Steps of 128 keys with one
+// buffer a tile, where the next product waits for the whole softmax, took 7 %
+// more.  A short chunk (16 tokens of four requests over 14000 keys,
+// 56.7 us, 18 of HBM time) is 24 us of products, its 128 rows against two E4M3
+// terms; the others are the plan, the first unit's records, page list and
+// queries (10), and the join (6).  Where neighbouring tiles select different
+// pages (query blocks of 16 tokens over BF16, 60 us) it waits for the L2: 64 KB
+// a page for one tile, 590 MB in all, two pages of each kind in flight.
 //
 // Roles (16 warps): warps 0-3 and 4-7 the softmax and epilogue of tile 0 and 1
 // (warp w reads TMEM lanes 32 (w % 4) .. +31), warps 8-11 split queries, widen
