@@ -310,12 +310,12 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool aborted(Shared &sh) { return *reinterpret_cast<volatile int *>(&sh.abort) != 0; }
 
 // Waits for the phase with the given parity; false once kWaitTries tries have
-// failed, 0.1 s or more (a unit of the longest request takes 2 ms).  Counting
-// the tries instead of reading a clock keeps the waits short in instructions,
-// whose fetching bounds the kernel beside the tensor pipe: with a clock read
-// in each (eight warps' roles, some thirty places) dense bf16 took 489 instead
-// of 466 us, ragged E4M3 108 instead of 98.
-constexpr uint32_t kWaitTries = 1u << 22;
+// failed, about 2 s (a try gives up after 2 us; a unit of the longest request
+// takes 2 ms).  Counting the tries instead of reading a clock keeps the waits
+// short in instructions, whose fetching bounds the kernel beside the tensor
+// pipe: with a clock read in each of some thirty places dense bf16 took 489
+// instead of 466 us, ragged E4M3 108 instead of 98.
+constexpr uint32_t kWaitTries = 1u << 20;
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
     if (tc::mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
