@@ -631,7 +631,9 @@ bool prefill_attention(const spd_tensor *q, const spd_tensor *k, const spd_tenso
     a.sl = static_cast<const int32_t *>(sl->data); a.sl_s0 = sl->stride[0];
     a.pre = static_cast<const int32_t *>(pre->data); a.pre_s0 = pre->stride[0];
     if (sparse) {
-        a.tk = static_cast<const int32_t *>(tk->data);
+        // an address says that there is a selection; of one without rows
+        // nothing is read, and its tensor has none
+        a.tk = static_cast<const int32_t *>(n_rows > 0 ? tk->data : cu->data);
         a.tk_s0 = tk->stride[0]; a.tk_s1 = tk->stride[1]; a.tk_s2 = tk->stride[2];
         a.cub = static_cast<const int32_t *>(cub->data); a.cub_s0 = cub->stride[0];
         a.n_rows = (int32_t)n_rows; a.K = (int32_t)K; a.bsq = bsq;

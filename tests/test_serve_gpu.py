@@ -762,3 +762,31 @@ def test_workspace_must_be_one_run(spd, monkeypatch):
             spd.paged_prefill_attention(*args, out, s["sm"], BS, 1.0, 1.0, ws)
     torch.cuda.synchronize()
     assert torch.isnan(out.float()).all(), "a refused call wrote its output"
+
+
+@pytest.mark.parametrize("pol", [0, 1])
+@pytest.mark.parametrize("cache", [E4M3, BF16], ids=["e4m3", "bf16"])
+def test_tokens_without_a_sequence(spd, cache, pol):
+    """A padded batch with no sequence in it, and one whose selection has no
+    rows: zeros, and nothing beside them."""
+    q = torch.randn((37, 16, 128), device=DEV).to(BF16)
+    kv = torch.full((2 * BS, 2, 128), 0x7F, dtype=torch.uint8, device=DEV).view(E4M3)
+    if cache == BF16:
+        kv = torch.full((2 * BS, 2, 128), float("nan"), device=DEV).to(BF16)
+    none, table = i32([]), i32([[0, 1], [1, 0]])
+    with policy(spd, pol):
+        for rows, cu, lens, cub in ((none, i32([0]), none, i32([0])), (i32([1]), i32([3, 30]), i32([100]), i32([0, 0]))):
+            out = nan_like((39, 16, 128), BF16, DEV)
+            size = spd.prefill_attention_workspace_bytes(37, 16, 2, 128, len(rows), 2, 0)
+            ws = torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)
+            topk = torch.empty((2, 0, 3), dtype=I32, device=DEV)
+            spd.paged_sparse_prefill_attention(q, kv, kv, table, rows, cu, lens, lens, topk, 4, cub, out[1:38], 0.1, BS,
+                                               1.0, 1.0, ws)
+            torch.cuda.synchronize()
+            assert spd.workspace_status(ws) == 0
+            assert not out[1:38].any() and torch.isnan(out[::38].float()).all()
+            if len(rows) == 0:
+                out.fill_(float("nan"))
+                spd.paged_prefill_attention(q, kv, kv, table, rows, cu, lens, lens, out[1:38], 0.1, BS, 1.0, 1.0, ws)
+                torch.cuda.synchronize()
+                assert not out[1:38].any() and torch.isnan(out[::38].float()).all()
