@@ -29,7 +29,8 @@
 //
 // Softmax: c = sm_scale * k_scale * log2(e) > 0.  The exponent offset m of a
 // row is raised only when a step's maximum exceeds it by more than 2^kRaise
-// (then the row's O is rescaled in tensor memory), so p <= 2^kRaise; p is
+// (then the row's O is rescaled in tensor memory), so p <= 2^kRaise, times 2^7
+// where P is f16; p is
 // rounded to the 16-bit type of the products (off by at most 2^-8 of itself in
 // bf16, of either sign, so an output of many keys keeps about the bf16 rounding
 // of its own), the row sum takes it unrounded, in fp32.
@@ -608,6 +609,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             }
             float m_run = -INFINITY, l = 0.f;
             float threshold = -INFINITY;  // logits above it raise the offset
+            // f16 P starts at 2^7, so that small weights stay normal numbers
+            // down to 2^-21 of the largest (and 2^kRaise more fits below 65504)
+            constexpr float kLift = kBf16 ? 0.f : 7.f;
             const uint64_t c2 = pair(c, c);
             uint64_t m2 = 0;              // minus the offset, twice (0 while the row has none)
             bool seen = false, ok = true;
@@ -671,11 +675,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                             const bool raise = mx > threshold;
                             float alpha = 1.f;
                             if (raise) {
-                                const float bm = mx * c;
+                                const float bm = fmaf(mx, c, -kLift);
                                 alpha = tc::ex2(m_run - bm);  // 0 for a row that had none
                                 m_run = bm;
                                 l *= alpha;
-                                threshold = (m_run + kRaise) / c;
+                                threshold = (m_run + (kLift + kRaise)) / c;
                                 m2 = pair(-m_run, -m_run);
                             }
                             if ((done > 0 || h == 1) && __any_sync(0xffffffffu, raise)) {

@@ -790,3 +790,25 @@ def test_tokens_without_a_sequence(spd, cache, pol):
                 spd.paged_prefill_attention(q, kv, kv, table, rows, cu, lens, lens, out[1:38], 0.1, BS, 1.0, 1.0, ws)
                 torch.cuda.synchronize()
                 assert not out[1:38].any() and torch.isnan(out[::38].float()).all()
+
+
+@pytest.mark.parametrize("pol", [0, 1])
+@pytest.mark.parametrize("kind", ["e4m3", "e4m3_f16", "e4m3_d64", "bf16"])
+def test_small_weights_keep_their_bits(spd, kind, pol):
+    """One key takes nearly all of the weight and holds zeros: the output is
+    the others', 20.5 * 2^-24 of weight each, half a step between two f16
+    values if the largest weight is 1."""
+    D = 64 if kind == "e4m3_d64" else 128
+    s = chunk_inputs([20, 3], [300, 700], 8, 1, D, F16 if kind == "e4m3_f16" else BF16, BF16 if kind == "bf16" else E4M3, 124)
+    s["q"].zero_()
+    s["q"][..., 0] = 1.0
+    one = 0x38 if kind != "bf16" else 1.0
+    kc, vc = (s[n].view(torch.uint8) if kind != "bf16" else s[n] for n in ("kc", "vc"))
+    for o in s["owned"][:2]:
+        for page in o.tolist():
+            kc[page * BS:(page + 1) * BS] = 0
+        kc[int(o[0]) * BS, :, 0] = one
+        vc[int(o[0]) * BS] = 0
+    s["ks"], s["sm"] = 1.0, float(24 * np.log(2.0) - np.log(20.5))
+    with policy(spd, pol):
+        run_chunk(spd, s, what="small weights")
