@@ -30,10 +30,9 @@
 // Softmax: c = sm_scale * k_scale * log2(e) > 0.  The exponent offset m of a
 // row is raised only when a step's maximum exceeds it by more than 2^kRaise
 // (then the row's O is rescaled in tensor memory), so p <= 2^kRaise, times 2^7
-// where P is f16; p is
-// rounded to the 16-bit type of the products (off by at most 2^-8 of itself in
-// bf16, of either sign, so an output of many keys keeps about the bf16 rounding
-// of its own), the row sum takes it unrounded, in fp32.
+// where P is f16.  It is rounded to the 16-bit type of the products (off by at
+// most 2^-8 of itself in bf16, of either sign, so an output of many keys keeps
+// about the bf16 rounding of its own); the row sum takes it unrounded, in fp32.
 //
 // A tile takes the pages that its own query blocks list (every page without a
 // selection), and passes the other tile's by; only rows of different query
