@@ -1217,8 +1217,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         j = next;
                     }
                 } else if (nblk > 0) {
-                    // nothing to multiply: the queries, too, only pass by
-                    ok = warp_wait(sh, &sh.q_full, nq & 1);
+                    // nothing to multiply: the queries, too, only pass by, but
+                    // not before their terms are written in place: the next
+                    // unit's queries are copied over them behind this arrival,
+                    // and a unit of one page that the other tile takes has
+                    // nothing else that waits for this tile's
+                    ok = wait_q();
                     if (ok && lane == 0) tc::mbar_arrive(&sh.q_empty);
                 }
                 if (ok) pass(nblk);
