@@ -58,3 +58,41 @@ def test_units_of_one_page_that_one_tile_takes(spd, kind, empty):
     first = run_chunk(spd, s, what="one page, one tile")
     for _ in range(3):
         assert torch.equal(bits(run_chunk(spd, s, check=False)), bits(first)), "two runs differ"
+
+
+# ------------------------------------------- heads that end inside a warp
+
+UNEVEN = [
+    # Hq, Hkv, D, values: row groups of one warp with different numbers of rows
+    (1, 1, 64, True), (1, 1, 128, True), (2, 2, 64, True), (3, 3, 64, True), (3, 3, 128, True), (5, 5, 64, True),
+    (6, 6, 64, True), (10, 5, 64, True), (15, 5, 64, True), (25, 5, 64, True), (17, 17, 128, False), (17, 17, 128, True),
+    (33, 11, 128, True), (70, 35, 64, False), (3, 3, 256, True), (100, 50, 256, True),
+]
+
+
+@pytest.mark.parametrize("cache", [E4M3, BF16, F16], ids=["e4m3", "bf16", "f16"])
+@pytest.mark.parametrize("shape", UNEVEN, ids=lambda u: "%d_%d_%d_%s" % u)
+def test_store_heads_that_end_inside_a_warp(spd, shape, cache):
+    Hq, Hkv, D, values = shape
+    dt = BF16 if cache != F16 else F16
+    for T, Rd, inter in ((1, D, False), (3, D // 2, False), (29, D, True)):
+        s = store_inputs(T, Hq, Hkv, D, Rd, 64, dt, cache, 150 + T, values)
+        if T > 4:
+            s["lens"][2], s["slots"][3] = 0, -1
+        ks, vs = (0.013, 0.02) if cache == E4M3 else (1.0, 1.0)
+        run_store(spd, s, dt, interleaved=inter, ks=ks, vs=vs)
+
+
+@pytest.mark.parametrize("pol", [0, 1])
+@pytest.mark.parametrize("given", ["q", "k"])
+@pytest.mark.parametrize("dt,cache,inter", [(F16, F16, False), (F16, F16, True), (BF16, E4M3, True), (F16, E4M3, True),
+                                            (BF16, BF16, False)])
+def test_store_norm_of_one_of_both(spd, dt, cache, inter, given, pol):
+    """Queries with a norm beside keys without one, and the other way round."""
+    s = store_inputs(41, 8, 2, 128, 64, 90, dt, cache, 160)
+    s["wk" if given == "q" else "wq"] = None
+    old = spd.set_kernel_policy(6, pol)
+    try:
+        run_store(spd, s, dt, interleaved=inter, ks=0.02 if cache == E4M3 else 1.0, vs=0.02 if cache == E4M3 else 1.0)
+    finally:
+        spd.set_kernel_policy(6, old)
