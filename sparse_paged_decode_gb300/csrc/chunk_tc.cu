@@ -452,10 +452,12 @@ __device__ __forceinline__ float split_query_row(uint8_t *q, int row) {
 // Elements of the marked blocks' V rows that this row reads (keys below lim, of
 // its own selection where row_bits is given) and that are not finite, added to
 // the row's O in tensor memory, where the products saw zeros in their place.
-// A warp-collective, and a rare, call.
+// The two sums of a dual unit are joined first, with their weights, and the
+// second one left zero: an infinity of one tile's page is not to meet the other
+// tile's weight, which may be 0.  A warp-collective, and a rare, call.
 template <int D, bool F8>
 __device__ __noinline__ void take_marked(const TcArgs &t, const UnitRec &u, int tile, int32_t lim,
-                                         const uint32_t *row_bits, uint32_t col_o) {
+                                         const uint32_t *row_bits, uint32_t col_o, float w_own, float w_other) {
     const ChunkArgs &a = t.a;
     uint32_t odd[3][D / 32];  // NaN, +inf, -inf dims
     for (int k = 0; k < 3; ++k)
@@ -495,6 +497,17 @@ __device__ __noinline__ void take_marked(const TcArgs &t, const UnitRec &u, int 
         float o[16];
         tc::tmem_ld16(col_o + c0, o);
         tc::tmem_wait_ld();
+        if (u.dual) {
+            float x[16];
+            tc::tmem_ld16(col_o + 128 + c0, x);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                o[i] = fmaf(o[i], w_own, x[i] * w_other);
+                x[i] = 0.f;
+            }
+            tc::tmem_st16(col_o + 128 + c0, x);
+        }
         const uint32_t nan = odd[0][c0 >> 5] >> (c0 & 31), pos = odd[1][c0 >> 5] >> (c0 & 31),
                        neg = odd[2][c0 >> 5] >> (c0 & 31);
 #pragma unroll
@@ -763,7 +776,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     l += other.y;
                 }
             }
-            if (own > 0 && u.marked != 0) take_marked<D, F8>(t, u, tile, have && chosen ? lim : 0, bits, col_o);
+            if (own > 0 && u.marked != 0) {
+                take_marked<D, F8>(t, u, tile, have && chosen ? lim : 0, bits, col_o, w_own, w_other);
+                w_own = 1.f, w_other = 0.f;
+            }
             const bool split = u.pieces > 1;
             const bool none = own == 0 || m_run == -INFINITY;  // no key of this piece was read
             const int64_t prow = static_cast<int64_t>(u.part) * 256 + tile * kRows + r;

@@ -96,3 +96,71 @@ def test_store_norm_of_one_of_both(spd, dt, cache, inter, given, pol):
         run_store(spd, s, dt, interleaved=inter, ks=0.02 if cache == E4M3 else 1.0, vs=0.02 if cache == E4M3 else 1.0)
     finally:
         spd.set_kernel_policy(6, old)
+
+
+# ------------------------------------------- infinite values that a row reads
+
+
+def held_with_infinities(spd, s, what):
+    """A run whose NaN and infinite cells, signs included, are those of the
+    64-bit definition; the finite ones within the usual bounds."""
+    got = run_chunk(spd, s, check=False).float().cpu().numpy().astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        ref, A = R.attention(s["q"], s["kc"], s["vc"], s["table"], s["rows"], torch.tensor(s["cu"]),
+                             torch.tensor(s["seq_lens"]), torch.tensor(s["prefix"]), s["sm"], s["ks"], s["vs"], s.get("topk"),
+                             s["bq"], None if not s["bq"] else torch.tensor(s["cub"]))
+    odd = ~np.isfinite(ref)
+    same = (got == ref) | (np.isnan(got) & np.isnan(ref))
+    assert same[odd].all(), "%s: %d of %d cells that are not finite differ" % (what, (~same[odd]).sum(), odd.sum())
+    R.check_attention(torch.from_numpy(np.where(odd, 0.0, got)), np.where(odd, 0.0, ref), np.where(odd, 0.0, A), what)
+    return odd
+
+
+def requests_like_it(s, n):
+    """The batch of n requests with the pages, lengths and selections of the
+    only one in `s`, and queries of their own: so many that none is cut into
+    pieces."""
+    chunk = s["cu"][1]
+    g = torch.Generator().manual_seed(n)
+    more = dict(q=torch.randn((n * chunk,) + tuple(s["q"].shape[1:]), generator=g).to(s["q"].dtype), rows=s["rows"][:1].repeat(n),
+                cu=[chunk * i for i in range(n + 1)], prefix=s["prefix"] * n, seq_lens=s["seq_lens"] * n)
+    if s["bq"]:
+        rows = s["cub"][1]
+        more.update(topk=s["topk"][:1, :rows].repeat(1, n, 1).expand(s["topk"].shape[0], -1, -1), cub=[rows * i for i in range(n + 1)])
+    return dict(s, **more)
+
+
+@pytest.mark.parametrize("pol", [0, 1])
+@pytest.mark.parametrize("n", [1, 200])  # cut into pieces, and whole
+@pytest.mark.parametrize("D", [64, 128])
+def test_infinite_values_where_the_other_pages_weigh_nothing(spd, D, n, pol):
+    """Three tokens, one tile of rows that two tiles work on page by page:
+    rows that read an infinite value of one tile's page and nothing of the
+    other's."""
+    s = chunk_inputs([3], [900], 64, 8, D, BF16, BF16, 170, bq=1, topk=4)
+    # blocks 1, 2, 4, 5 are listed: two for each tile, in turn
+    s["topk"] = torch.tensor([[[2, 5, -1, -1], [1, 4, -1, -1], [1, 2, 4, 5]]], dtype=I32).expand(8, -1, -1)
+    page = s["owned"][0].tolist()
+    inf = float("inf")
+    s["vc"][page[5] * BS + 9, 0, 3], s["vc"][page[5] * BS + 100, 1, D - 1] = inf, -inf
+    s["vc"][page[4] * BS + 1, 0, 33], s["vc"][page[4] * BS + 2, 1, 0] = -inf, inf
+    s["vc"][page[2] * BS, 0, 17], s["vc"][page[1] * BS + 127, 0, 17] = inf, -inf  # both: NaN
+    with policy(spd, pol):
+        odd = held_with_infinities(spd, requests_like_it(s, n), "infinite values")
+    odd = odd.reshape(n, 3, 64, D)
+    assert odd[:, 0, :8, 3].all() and odd[:, 1, :8, 33].all() and odd[:, 2, :8, 17].all() and not odd[:, 1, :8, 3].any()
+
+
+@pytest.mark.parametrize("n", [1, 200])
+def test_infinite_values_beside_a_weight_of_zero(spd, n):
+    """The same with every key read: the first page's logits lie so far below
+    the second's that its weight is 0 in 32 bits.  The second page ends inside
+    the chunk, so its infinities are looked up."""
+    s = requests_like_it(chunk_inputs([3], [200], 64, 8, 128, BF16, BF16, 171), n)
+    s["q"] = s["q"].abs() + 0.5
+    page = s["owned"][0].tolist()
+    s["kc"][page[0] * BS:(page[0] + 1) * BS] = -32.0  # logits below -32 * 128 * 0.5 / sqrt(128) = -181
+    s["kc"][page[1] * BS:page[1] * BS + 203 - BS] = 0.0
+    s["vc"][page[1] * BS + 3, 0, 5], s["vc"][page[1] * BS + 60, 1, 77] = float("inf"), -float("inf")
+    odd = held_with_infinities(spd, s, "weight of zero")
+    assert odd[:, :8, 5].all() and odd[:, 8:16, 77].all() and odd.sum() == 2 * 3 * n * 8
