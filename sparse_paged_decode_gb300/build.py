@@ -95,6 +95,11 @@ def build_marshal(force: bool = False) -> bool:
         with open(stamp_path) as f:
             if f.read() == h.hexdigest():
                 return True
+    # a module of other sources must not stay behind where this build fails: it
+    # would pass the library arguments of another order
+    for path in (MARSHAL_PATH, stamp_path):
+        if os.path.exists(path):
+            os.remove(path)
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = MARSHAL_PATH + ".tmp%d" % os.getpid()
