@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import serve_ref as R
-from test_serve_gpu import BF16, BS, DEV, E4M3, F16, F32, I32, chunk_inputs, policy, run_chunk, run_store, store_inputs
+from test_serve_gpu import (BF16, BS, DEV, E4M3, F16, I32, check_assign, chunk_inputs, i32, policy, run_assign, run_chunk,
+                            run_store, store_inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +165,51 @@ def test_infinite_values_beside_a_weight_of_zero(spd, n):
     s["vc"][page[1] * BS + 3, 0, 5], s["vc"][page[1] * BS + 60, 1, 77] = float("inf"), -float("inf")
     odd = held_with_infinities(spd, s, "weight of zero")
     assert odd[:, :8, 5].all() and odd[:, 8:16, 77].all() and odd.sum() == 2 * 3 * n * 8
+
+
+# --------------------------------------------------------- long page tables
+
+
+@pytest.mark.parametrize("kind,pol", [(k, 0) for k in KINDS] + [("e4m3", 1)])
+@pytest.mark.parametrize("NB", [129, 1024])
+def test_attention_over_long_page_tables(spd, NB, kind, pol):
+    """Page tables of up to 1024 blocks: page lists and bitmaps to their last
+    word, a request that ends at the table's end and one that ends inside."""
+    D, q_dt, cache = kind_of(kind)
+    whole, half = NB * BS, NB * BS // 2 - 77
+    chunks = [3, 17]
+    with policy(spd, pol):
+        for bq, topk, per_head in ((0, 0, False), (2, 40, True), (16, 600, False)):
+            s = chunk_inputs(chunks, [whole - 3, half], 8, 2, D, q_dt, cache, 180 + bq, NB=NB, bq=bq, topk=topk, per_head=per_head)
+            if bq:
+                pick = s["topk"] if per_head else s["topk"][:1].clone()
+                pick[:, 0, 1:3] = torch.tensor([NB - 1, NB - 2], dtype=I32)
+                pick[:, -1, 1:4] = torch.tensor([NB, NB - 1, 31], dtype=I32)
+                s["topk"] = pick if per_head else pick.expand(2, -1, -1)
+            run_chunk(spd, s, what="NB %d bq %d" % (NB, bq))
+
+
+@pytest.mark.parametrize("NB", [129, 1024])
+def test_whole_chunks_over_long_page_tables(spd, NB):
+    """Chunks of several pairs over every key of a long table, among short
+    ones."""
+    for cache in (E4M3, BF16):
+        s = chunk_inputs([35, 5, 17], [NB * BS - 35, 300, 9000], 8, 1, 128, BF16, cache, 190, NB=NB)
+        run_chunk(spd, s, what="NB %d" % NB)
+
+
+@pytest.mark.parametrize("NB", [25, 1024])
+def test_assign_long_page_tables(spd, NB):
+    g = torch.Generator().manual_seed(NB)
+    B, cap = 70, NB * BS
+    prefix = torch.randint(0, cap + 300, (B,), generator=g).tolist()
+    new = torch.randint(0, 3000, (B,), generator=g).tolist()
+    prefix[:5], new[:5] = [cap - 1, cap, cap - 128, 0, cap - 127], [1, 7, 128, min(cap, 100000), 129]
+    rows = torch.randperm(B + 3, generator=g)[:B].to(I32)
+    table = torch.randperm((B + 3) * NB, generator=g).to(I32).view(B + 3, NB)
+    grown = sum(-(-min(p + n, cap) // BS) - -(-min(p, cap) // BS) for n, p in zip(new, prefix))
+    free = (torch.randperm(grown + 9, generator=g) + (B + 3) * NB).to(I32)
+    T = sum(new) + 11
+    for count in (grown + 9, grown - 20):
+        args = (i32(new), i32(prefix), rows.to(DEV), free.to(DEV), i32([count]), (B + 3) * NB + grown + 9, 64, table.to(DEV), T)
+        check_assign(run_assign(spd, *args), *args, "NB %d" % NB)
