@@ -454,7 +454,8 @@ SPD_API void paged_norm_rope_store(const spd_tensor *q, const spd_tensor *k, con
  *            shared by calls that may run concurrently
  * sm_scale, k_scale, v_scale finite; block_size must be 128
  * Domain: D in [1, 256], Hq / Hkv <= 16, NB in [1, 1024], B <= 8192,
- * total_q * Hq < 2^30.
+ * total_q * Hq < 2^30, logits below 2^26 in magnitude (6.7e7; the fp32 values
+ * of larger ones lie 4 and more apart, and their rows may not be finite).
  */
 SPD_API void paged_prefill_attention(const spd_tensor *q, const spd_tensor *k_cache, const spd_tensor *v_cache,
                                      const spd_tensor *block_table, const spd_tensor *slot_ids,

@@ -691,7 +691,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                                 alpha = tc::ex2(m_run - bm);  // 0 for a row that had none
                                 m_run = bm;
                                 l *= alpha;
-                                threshold = (m_run + (kLift + kRaise)) / c;
+                                // lower by what the rounding of large offsets
+                                // may add, so that p stays below 2^(kLift + kRaise)
+                                threshold = fmaxf(mx, fmaf(fabsf(m_run), -0x1p-22f, m_run + (kLift + kRaise)) / c);
                                 m2 = pair(-m_run, -m_run);
                             }
                             if ((done > 0 || h == 1) && __any_sync(0xffffffffu, raise)) {

@@ -213,3 +213,30 @@ def test_assign_long_page_tables(spd, NB):
     for count in (grown + 9, grown - 20):
         args = (i32(new), i32(prefix), rows.to(DEV), free.to(DEV), i32([count]), (B + 3) * NB + grown + 9, 64, table.to(DEV), T)
         check_assign(run_assign(spd, *args), *args, "NB %d" % NB)
+
+
+# ------------------------------------------------------------- large logits
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_logits_of_tens_of_millions(spd, kind):
+    """Two keys of weight in the halves of a page, the second's logit a little
+    larger, both so large that their 32-bit spacing is 1 to 4: their weights
+    are anything, and their values the same, so the output is that value."""
+    D, q_dt, cache = kind_of(kind)
+    s = chunk_inputs([96], [200], 16, 2, D, q_dt, cache, 200)
+    s["q"].zero_()
+    row = torch.arange(96 * 16).view(96, 16)
+    s["q"][..., 0] = (20000.0 + 26.0 * row).to(q_dt)  # logits of 9 to 26.9 millions
+    s["q"][..., 1] = (3.0 + row % 7).to(q_dt)
+    page = s["owned"][0].tolist()
+    code = (lambda x: torch.tensor(x).to(E4M3).view(torch.uint8).item()) if cache == E4M3 else (lambda x: x)
+    kc = s["kc"].view(torch.uint8) if cache == E4M3 else s["kc"]
+    for p in page:
+        kc[p * BS:(p + 1) * BS] = 0
+    kc[page[0] * BS + 5, :, 0], kc[page[0] * BS + 90, :, 0] = code(448.0), code(448.0)
+    kc[page[0] * BS + 90, :, 1] = code(1.0)
+    vc = s["vc"].view(torch.uint8) if cache == E4M3 else s["vc"]
+    vc[page[0] * BS + 90] = vc[page[0] * BS + 5]
+    s["ks"], s["sm"] = 1.0, 1.0
+    run_chunk(spd, s, what="large logits")
