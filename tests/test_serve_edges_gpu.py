@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import serve_ref as R
+from parity import nan_like
 from test_serve_gpu import (BF16, BS, DEV, E4M3, F16, I32, check_assign, chunk_inputs, i32, policy, run_assign, run_chunk,
                             run_store, store_inputs)
 
@@ -240,3 +241,78 @@ def test_logits_of_tens_of_millions(spd, kind):
     vc[page[0] * BS + 90] = vc[page[0] * BS + 5]
     s["ks"], s["sm"] = 1.0, 1.0
     run_chunk(spd, s, what="large logits")
+
+
+# ------------------------------------------------------ a step as one graph
+
+
+@pytest.mark.parametrize("cache", [E4M3, BF16], ids=["e4m3", "bf16"])
+def test_a_captured_step_goes_on_by_itself(spd, cache):
+    """Slots, stores, selection and attention captured in one graph that also
+    carries the lengths and the free count over: each replay is the next step
+    of the loop, with new lengths, and leaves what the same calls one by one
+    leave."""
+    B, Hq, Hkv, D, NB, bq, K, T = 4, 16, 2, 128, 16, 16, 4, 700
+    pool, rows_cap = 80, 700 // 16 + 4
+    ks = vs = 0.02 if cache == E4M3 else 1.0
+    g = torch.Generator().manual_seed(11)
+    angle = torch.rand((NB * BS, D // 2), generator=g, dtype=torch.float64) * 6.3
+    fixed = dict(rows=i32([2, 0, 4, 1]), free=torch.randperm(pool, generator=g).to(I32).to(DEV),
+                 w=(1 + 0.1 * torch.randn(D, generator=g)).to(BF16).to(DEV),
+                 cos_sin=torch.cat((angle.cos(), angle.sin()), 1).float().to(DEV))
+
+    def state():
+        kv = [torch.full((pool * BS, Hkv, D), 0x7F, dtype=torch.uint8, device=DEV).view(E4M3) if cache == E4M3 else
+              torch.full((pool * BS, Hkv, D), float("nan"), dtype=BF16, device=DEV) for _ in range(2)]
+        s = dict(new=i32([0] * B), prefix=i32([0] * B), count=i32([pool]), x=torch.zeros((T, Hq + 2 * Hkv + 3, D), dtype=BF16, device=DEV),
+                 table=torch.full((5, NB), -1, dtype=I32, device=DEV), kc=kv[0], vc=kv[1],
+                 kic=torch.full((pool * BS, 1, D), float("nan"), dtype=BF16, device=DEV),
+                 q=nan_like((T, Hq, D), BF16, DEV), qi=nan_like((T, 2, D), BF16, DEV), o=nan_like((T, Hq, D), BF16, DEV),
+                 dense=nan_like((T, Hq, D), BF16, DEV), topk=nan_like((2, rows_cap, K), I32, DEV))
+        for n, size in (("cu", B + 1), ("cub", B + 1), ("sl", B), ("req", T), ("lens", T), ("slots", T), ("left", 1)):
+            s[n] = nan_like((size,), I32, DEV)
+        s["was"] = i32([0] * B)
+        s["pws"] = torch.empty(spd.prefill_workspace_bytes(T, 2, NB), dtype=torch.uint8, device=DEV)
+        s["ws"] = torch.empty(spd.prefill_attention_workspace_bytes(T, Hq, Hkv, D, B, NB, rows_cap), dtype=torch.uint8, device=DEV)
+        return s
+
+    def step(s):
+        f, x = fixed, s["x"]
+        s["was"].copy_(s["prefix"])
+        spd.paged_assign_slots(s["new"], s["prefix"], f["rows"], f["free"], s["count"], pool, BS, bq, s["table"], s["cu"], s["cub"],
+                               s["sl"], s["req"], s["lens"], s["slots"], s["left"])
+        spd.paged_norm_rope_store(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:Hq + 2 * Hkv], f["w"], f["w"], f["cos_sin"], s["lens"],
+                                  s["slots"], s["q"], s["kc"], s["vc"], 1e-6, False, BS, ks, vs)
+        spd.paged_norm_rope_store(x[:, -3:-1], x[:, -1:], None, f["w"], f["w"], f["cos_sin"], s["lens"], s["slots"], s["qi"],
+                                  s["kic"], None, 1e-6, False, BS, 1.0, 1.0)
+        spd.msa_prefill_block_score(s["qi"], s["kic"], s["table"], f["rows"], s["cu"], s["sl"], s["prefix"], bq, BS, 1, 1, D ** -0.5,
+                                    s["cub"], s["topk"], s["pws"])
+        head = (s["q"], s["kc"], s["vc"], s["table"], f["rows"], s["cu"], s["sl"], s["prefix"])
+        spd.paged_sparse_prefill_attention(*head, s["topk"], bq, s["cub"], s["o"], D ** -0.5, BS, ks, vs, s["ws"])
+        spd.paged_prefill_attention(*head, s["dense"], D ** -0.5, BS, ks, vs, s["ws"])
+        s["prefix"].copy_(s["sl"])
+        s["count"].copy_(s["left"])
+
+    warm = state()
+    step(warm)  # a step of no tokens; before any capture
+    a, b = state(), state()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(a)
+    torch.cuda.synchronize()
+    for n, new in enumerate(([300, 1, 0, 17], [1, 200, 0, 300], [0, 0, 0, 0], [1, 1, 1, 1], [128, 400, 127, 60])):
+        x = torch.randn(tuple(a["x"].shape), generator=g).to(BF16).to(DEV)
+        for s in (a, b):
+            s["new"].copy_(i32(new))
+            s["x"].copy_(x)
+        graph.replay()
+        step(b)
+        torch.cuda.synchronize()
+        for name in a:
+            if name not in ("ws", "pws"):
+                assert torch.equal(a[name].view(torch.uint8), b[name].view(torch.uint8)), "step %d: %s" % (n, name)
+        for out, topk in ((a["o"], a["topk"]), (a["dense"], None)):
+            ref, A = R.attention(a["q"], a["kc"], a["vc"], a["table"], fixed["rows"], a["cu"], a["sl"], a["was"], D ** -0.5, ks, vs,
+                                 topk, bq, a["cub"])
+            R.check_attention(out, ref, A, "step %d" % n)
+        assert spd.workspace_status(a["ws"]) == 0
