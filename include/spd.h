@@ -397,7 +397,8 @@ SPD_API void paged_assign_slots(const spd_tensor *new_lens, const spd_tensor *pr
  *         y'_a = y_a cos - y_b sin,  y'_b = y_b cos + y_a sin
  *   q_out[t]          = y' of q
  *   k_cache[slots[t]] = y' of k / k_scale;  v_cache[slots[t]] = v[t] / v_scale
- * in fp32 and rounded once (to nearest even; E4M3 saturates at +-448 and
+ * in fp32 (the divisions as products with the scales' fp32 reciprocals) and
+ * rounded once to the kept type (to nearest even; E4M3 saturates at +-448 and
  * keeps NaN).  A token with token_lens outside [1, M] (padding) gets a zero
  * q_out row and stores nothing; a slot outside the pool stores nothing.  The
  * index queries and keys of the score calls go through the same call, with v
@@ -440,8 +441,23 @@ SPD_API void paged_norm_rope_store(const spd_tensor *q, const spd_tensor *k, con
  *   z_tau = sm_scale * k_scale * (q[t][g] . k_cache[slot(tau)][h]),  h = g / (Hq / Hkv)
  * A token that reads no key, and one that no sequence owns, writes zeros.
  * Slots that a token does not read never reach its output, whatever they
- * hold (NaN and infinities included).  Logits, softmax and accumulation are
- * fp32; the output is rounded to bf16 (nearest even).
+ * hold (NaN and infinities included).  Logits, maxima, sums and accumulation
+ * are fp32; the output is rounded to bf16 (nearest even).  Where the shapes
+ * allow the tensor cores (D 64 or 128, 16-bit queries, 16-byte rows, positive
+ * scales) what enters the two products is rounded as follows:
+ *   - probabilities, before the product with V: to bf16 over a BF16 cache (off
+ *     by at most 2^-8 of themselves), to f16 over an E4M3 one (2^-11, for
+ *     probabilities down to 2^-21 of the row's largest)
+ *   - bf16 queries over an E4M3 cache: of 128 dims to two E4M3 terms (an
+ *     element is exact within 2^9 of the largest of its head row, else off by
+ *     at most 2^-17 of that one), of 64 dims to f16 (exact within 2^31, else
+ *     off by at most 2^-39); bf16 queries over a BF16 cache and f16 ones over
+ *     an E4M3 cache enter as they are
+ * so |out - exact| <= 2^-8 |exact| + (2^-8 + 2^-10) sum_tau softmax(z)_tau
+ * |v_scale * v| as long as a query row has no element that decides its logits
+ * beside one 2^9 times larger that does not.  Stage 5 of
+ * spd_set_kernel_policy selects the kernel that rounds neither.  An infinite
+ * value whose probability underflows in fp32 may give NaN (0 times infinity).
  *
  * q          [total_q, Hq, D] f32 | bf16 | f16
  * k_cache, v_cache [P*128, Hkv, D] e4m3 | bf16, innermost stride 1

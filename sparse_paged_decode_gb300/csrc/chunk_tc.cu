@@ -28,9 +28,9 @@
 // their keys widened as well.
 //
 // Softmax: c = sm_scale * k_scale * log2(e) > 0.  The exponent offset m of a
-// row is raised only when a step's maximum exceeds it by more than 2^kRaise
-// (then the row's O is rescaled in tensor memory), so p <= 2^kRaise, times 2^7
-// where P is f16.  It is rounded to the 16-bit type of the products (off by at
+// row is raised only when a step's maximum, as a power of two, exceeds it by
+// more than kRaise (then the row's O is rescaled in tensor memory), so p <=
+// 2^kRaise, times 2^7 where P is f16.  It is rounded to the 16-bit type of the products (off by at
 // most 2^-8 of itself in bf16, of either sign, so an output of many keys keeps
 // about the bf16 rounding of its own); the row sum takes it unrounded, in fp32.
 //
@@ -382,8 +382,10 @@ __device__ __forceinline__ void row_power(const uint8_t *q, int row, int top, fl
     down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
 }
 
-// A bf16 query row to f16, in place, scaled by a power of two (exact for
-// elements within 2^38 of the row's largest); returns the inverse scale.
+// A bf16 query row to f16, in place, scaled by a power of two into [2^14,
+// 2^15): exact for elements within 2^31 of the row's largest (eight bits above
+// f16's smallest step of 2^-24), and off by at most 2^-39 of that beyond.
+// Returns the inverse scale.
 template <int D>
 __device__ __forceinline__ float halve_query_row(uint8_t *q, int row) {
     float up, down;

@@ -141,7 +141,6 @@ __device__ __forceinline__ uint64_t swapped(uint64_t x) {
     return pair(hi, lo);
 }
 
-// Four neighbouring values, rounded and stored at p.
 template <bool kBf16>
 __device__ __forceinline__ uint32_t round2(uint64_t x) {
     float lo, hi;
@@ -154,6 +153,7 @@ __device__ __forceinline__ uint32_t round2(uint64_t x) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Four neighbouring values, rounded and stored at p.
 template <bool kBf16, bool kF8>
 __device__ __forceinline__ void store4(void *p, uint64_t x0, uint64_t x1) {
     if (kF8) {
