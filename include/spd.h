@@ -454,8 +454,8 @@ SPD_API void paged_norm_rope_store(const spd_tensor *q, const spd_tensor *k, con
  *     off by at most 2^-39); bf16 queries over a BF16 cache and f16 ones over
  *     an E4M3 cache enter as they are
  * so |out - exact| <= 2^-8 |exact| + (2^-8 + 2^-10) sum_tau softmax(z)_tau
- * |v_scale * v| as long as a query row has no element that decides its logits
- * beside one 2^9 times larger that does not.  Stage 5 of
+ * |v_scale * v| while the queries' rounding moves no logit by 2^-10, as where
+ * 2^-17 sm_scale * k_scale * max_d |q_d| * sum_d |k_d| <= 2^-10. Stage 5 of
  * spd_set_kernel_policy selects the kernel that rounds neither.  An infinite
  * value whose probability underflows in fp32 may give NaN (0 times infinity).
  *

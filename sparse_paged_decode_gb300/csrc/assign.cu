@@ -12,9 +12,10 @@
 // no token waits for the table to be written.
 //
 // What bounds it is latency: a launch and three dependent reads (lengths, the
-// page of a token, the write).  Measured: 4.5 us for 466 tokens of 64 requests,
-// 6.1 us for 65536 tokens of 1024 (0.8 MB, 0.1 us of HBM time; four tokens to a
-// thread, on a quarter of the CTAs, took 8.8 us).
+// page of a token, the write).  Measured in a graph: 4.6 us for 466 tokens of
+// 64 requests, 6.2 us for 65536 tokens of 1024 (0.8 MB, 0.1 us of HBM time; four
+// tokens to a thread, on a quarter of the CTAs, took 8.8 us); 6.2 and 8.2 us
+// called one by one.
 #include "serve.cuh"
 #include "spd_dispatch.h"
 #include "spd_internal.cuh"

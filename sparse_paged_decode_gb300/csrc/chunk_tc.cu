@@ -56,16 +56,18 @@
 // logits to P.  Beside the pipe it is the fetching of instructions: sixteen
 // warps run a dozen roles' code, so waits, steps and epilogues are kept short
 // (where each measured, it is said there).  Measured (eight 512-token chunks at
-// up to 15872 cached tokens, 64 / 8 heads of 128 dims): 463 us over BF16, 1.55
-// PFLOP/s, 81 % of the measured bf16 rate; the same chunks over 32 selected
-// E4M3 blocks a query block 344 us, 1.30 PFLOP/s.  Steps of 128 keys with one
-// buffer a tile, where the next product waits for the whole softmax, took 7 %
-// more.  A short chunk (16 tokens of four requests over 14000 keys,
-// 56.7 us, 18 of HBM time) is 24 us of products, its 128 rows against two E4M3
-// terms; the others are the plan, the first unit's records, page list and
-// queries (10), and the join (6).  Where neighbouring tiles select different
-// pages (query blocks of 16 tokens over BF16, 60 us) it waits for the L2: 64 KB
-// a page for one tile, 590 MB in all, two pages of each kind in flight.
+// up to 15872 cached tokens, 64 / 8 heads of 128 dims, a graph of calls on one
+// set of inputs; called one by one on changing ones in brackets): 466 (500) us
+// over BF16, 1.54 (1.43) PFLOP/s, 80 (75) % of the measured bf16 rate; the same
+// chunks over 32 selected E4M3 blocks a query block 346 (355) us, 1.30 (1.26)
+// PFLOP/s.  Steps of 128 keys with one buffer a tile, where the next product
+// waits for the whole softmax, took 7 % more.  A short chunk (16 tokens of four
+// requests over 14000 keys, 57 (61) us, 18 of HBM time) is 24 us of products,
+// its 128 rows against two E4M3 terms; the others are the plan, the first unit's
+// records, page list and queries (10), and the join (6).  Where neighbouring
+// tiles select different pages (query blocks of 16 tokens over BF16, 60 to 64
+// (69) us) it waits for the L2: 64 KB a page for one tile, 590 MB in all, two
+// pages of each kind in flight.
 //
 // Roles (16 warps): warps 0-3 and 4-7 the softmax and epilogue of tile 0 and 1
 // (warp w reads TMEM lanes 32 (w % 4) .. +31), warps 8-11 split queries, widen

@@ -4,8 +4,10 @@
 // A head row of D elements is read once, normalised and rotated in fp32 and
 // written once, rounded to the type it is kept in: the call moves its inputs
 // and outputs and nothing else, so HBM bandwidth bounds it.  Measured, 64 + 8 +
-// 8 rows of 128 dims a token into E4M3 caches: 63.6 us for 8192 tokens (323 MB,
-// 75 % of the measured copy bandwidth), 6.4 us for 466.
+// 8 rows of 128 dims a token into E4M3 caches: 61.7 us for 8192 tokens in a
+// graph and 63.4 us called one by one (323 MB, 77 and 75 % of the measured copy
+// bandwidth); 6.5 us for 466 tokens that the L2 holds, 8.9 us over buffers that
+// it does not.
 #include "f32x2.cuh"
 #include "serve.cuh"
 #include "spd_dispatch.h"
