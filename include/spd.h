@@ -455,9 +455,10 @@ SPD_API void paged_norm_rope_store(const spd_tensor *q, const spd_tensor *k, con
  *     an E4M3 cache enter as they are
  * so |out - exact| <= 2^-8 |exact| + (2^-8 + 2^-10) sum_tau softmax(z)_tau
  * |v_scale * v| while the queries' rounding moves no logit by 2^-10, as where
- * 2^-17 sm_scale * k_scale * max_d |q_d| * sum_d |k_d| <= 2^-10. Stage 5 of
- * spd_set_kernel_policy selects the kernel that rounds neither.  An infinite
- * value whose probability underflows in fp32 may give NaN (0 times infinity).
+ * 2^-17 sm_scale * k_scale * max_d |q_d| * sum_d |k_d| <= 2^-10.
+ * Stage 5 of spd_set_kernel_policy selects the kernel that rounds neither.  An
+ * infinite value whose probability is 0 in fp32 (underflow, or a logit of
+ * -inf) gives that infinity or NaN.
  *
  * q          [total_q, Hq, D] f32 | bf16 | f16
  * k_cache, v_cache [P*128, Hkv, D] e4m3 | bf16, innermost stride 1
