@@ -17,6 +17,8 @@
  *   paged_prefill_attention          a ragged batch of chunks of new tokens
  *   paged_sparse_prefill_attention   over the caches: every key, or the blocks
  *                                    msa_prefill_block_score selected
+ * and the store and the paged attention calls once more, with the suffix
+ * _block_scaled, for E4M3 caches with one scale for each page and kv head.
  *
  * Contract shared by every entry point ("Kernel ABI" -- Core rules; "Slot
  * contract" -- 1. The validator owns the boundary):
@@ -503,6 +505,96 @@ SPD_API void paged_sparse_prefill_attention(const spd_tensor *q, const spd_tenso
                                             const spd_tensor *cu_seqblocks_q, const spd_tensor *out,
                                             float sm_scale, int32_t block_size, float k_scale, float v_scale,
                                             void *workspace, size_t workspace_bytes, spd_stream_t stream);
+
+/*
+ * Block-scaled caches: E4M3 codes with one fp32 scale for each page and kv
+ * head, k_scales and v_scales [P, Hkv].  A slot's value is its code times its
+ * page's scale, so pages and heads may differ in magnitude by any power of two
+ * where the calls above have one scale for all.
+ *
+ * paged_norm_rope_store_block_scaled appends: queries, norms, rotations, padding
+ * and slots as in paged_norm_rope_store; v and v_cache are needed.  The stored
+ * rows of a page must be one run, neighbouring rows of the batch whose slots
+ * rise by one (what paged_assign_slots gives); of two runs in one page, the
+ * page's codes and scales are unspecified.  A run that begins at offset f of its page
+ * appends to the f tokens that the page holds; with f = 0 it begins the page
+ * anew.  For each kv head, with y the run's rows (fp32),
+ *   need  = the smallest 2^e, e in [-64, 64], with max |y| <= 448 * 2^e, over
+ *           the finite elements (2^-64 where there is none but zeros)
+ *   old   = the page's scale (none where f = 0, or where it is not finite and > 0)
+ *   scale = old where old >= need, else need
+ * the codes at offsets below f become round(code * (old / scale)) where there is
+ * an old scale, those of the run round(y / scale) (as a product with the scale's
+ * fp32 reciprocal; to nearest even, saturating at +-448, keeping NaN), and the page's
+ * scale becomes scale.  Codes at later offsets stay as they are; they count as
+ * empty.  With scales of this call's making old / scale is a power of two, so
+ * only codes that become subnormal are rounded a second time, and a second call on the
+ * same inputs changes nothing.
+ *
+ * k_cache, v_cache IN/OUT [P*block_size, Hkv, D] e4m3
+ * k_scales, v_scales IN/OUT [P, Hkv] f32: only the named pages' entries are written
+ * the other arguments as in paged_norm_rope_store
+ */
+SPD_API void paged_norm_rope_store_block_scaled(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v,
+                                                const spd_tensor *q_weight, const spd_tensor *k_weight,
+                                                const spd_tensor *cos_sin, const spd_tensor *token_lens,
+                                                const spd_tensor *slots, const spd_tensor *q_out,
+                                                const spd_tensor *k_cache, const spd_tensor *v_cache,
+                                                const spd_tensor *k_scales, const spd_tensor *v_scales, float eps,
+                                                int32_t interleaved, int32_t block_size, spd_stream_t stream);
+
+/*
+ * The paged attention calls over block-scaled caches: the calls of the same
+ * name without the suffix, with
+ *   z_tau = sm_scale * ks * (q[t][g] . k_cache[slot(tau)][h])
+ *   out[t][g] = sum_tau softmax(z)_tau * vs * v_cache[slot(tau)][h]
+ * where ks and vs are the scales of tau's page and of kv head h, each taken as
+ * the nearest value of [2^-64, 2^64] (the smallest for a NaN): any positive
+ * scales will do, not only powers of two.  Scales of pages that a row does not
+ * read never reach its output.
+ *
+ * k_cache, v_cache [P*128, Hkv, D] e4m3; k_scales, v_scales [P, Hkv] f32, any
+ * strides; workspaces, the other arguments and the domain as for the calls without
+ * the suffix.  The rounding is theirs too, but that the weights which the tensor
+ * cores round to f16 are those times vs: they keep their 11 bits down to 2^-21
+ * (prefill) or 2^-14 (decode) of the row's largest product of the two, and the
+ * bound becomes
+ *   |out - exact| <= 2^-8 |exact| + (2^-8 + 2^-10) A + 2^-22 M
+ * with A = sum_tau softmax(z)_tau |vs * v| and M = 448 times the row's largest
+ * softmax(z)_tau * vs, per key that is read.
+ */
+SPD_API void paged_decode_attention_block_scaled(const spd_tensor *q, const spd_tensor *k_cache,
+                                                 const spd_tensor *v_cache, const spd_tensor *k_scales,
+                                                 const spd_tensor *v_scales, const spd_tensor *block_table,
+                                                 const spd_tensor *seq_lens, const spd_tensor *req_idx,
+                                                 const spd_tensor *out, float sm_scale, int32_t block_size,
+                                                 void *workspace, size_t workspace_bytes, spd_stream_t stream);
+
+SPD_API void paged_sparse_decode_attention_block_scaled(const spd_tensor *q, const spd_tensor *k_cache,
+                                                        const spd_tensor *v_cache, const spd_tensor *k_scales,
+                                                        const spd_tensor *v_scales, const spd_tensor *block_table,
+                                                        const spd_tensor *seq_lens, const spd_tensor *req_idx,
+                                                        const spd_tensor *topk_idx, const spd_tensor *out,
+                                                        float sm_scale, int32_t block_size, void *workspace,
+                                                        size_t workspace_bytes, spd_stream_t stream);
+
+SPD_API void paged_prefill_attention_block_scaled(const spd_tensor *q, const spd_tensor *k_cache,
+                                                  const spd_tensor *v_cache, const spd_tensor *k_scales,
+                                                  const spd_tensor *v_scales, const spd_tensor *block_table,
+                                                  const spd_tensor *slot_ids, const spd_tensor *cu_seqlens,
+                                                  const spd_tensor *seq_lens, const spd_tensor *prefix_lens,
+                                                  const spd_tensor *out, float sm_scale, int32_t block_size,
+                                                  void *workspace, size_t workspace_bytes, spd_stream_t stream);
+
+SPD_API void paged_sparse_prefill_attention_block_scaled(const spd_tensor *q, const spd_tensor *k_cache,
+                                                         const spd_tensor *v_cache, const spd_tensor *k_scales,
+                                                         const spd_tensor *v_scales, const spd_tensor *block_table,
+                                                         const spd_tensor *slot_ids, const spd_tensor *cu_seqlens,
+                                                         const spd_tensor *seq_lens, const spd_tensor *prefix_lens,
+                                                         const spd_tensor *topk_idx, int32_t block_size_q,
+                                                         const spd_tensor *cu_seqblocks_q, const spd_tensor *out,
+                                                         float sm_scale, int32_t block_size, void *workspace,
+                                                         size_t workspace_bytes, spd_stream_t stream);
 
 /*
  * Workspace bytes the two prefill attention calls need for these capacities;

@@ -14,6 +14,9 @@ CUDA kernel:
   paged_prefill_attention         chunks of new tokens over the caches, every key
   paged_sparse_prefill_attention  the same over the selected blocks
 
+The store and the paged attention calls have a form for E4M3 caches with one
+scale for each page and kv head: the same names with ``_block_scaled``.
+
 The Python functions of the same names (in :mod:`.binding`) only marshal
 torch tensors into the C ABI; every step runs in the CUDA library.  They
 raise if the library has not been built: there is no CPU fallback.
@@ -34,6 +37,11 @@ __all__ = [
     "paged_norm_rope_store",
     "paged_prefill_attention",
     "paged_sparse_prefill_attention",
+    "paged_norm_rope_store_block_scaled",
+    "paged_decode_attention_block_scaled",
+    "paged_sparse_decode_attention_block_scaled",
+    "paged_prefill_attention_block_scaled",
+    "paged_sparse_prefill_attention_block_scaled",
     "prefill_attention_workspace_bytes",
     "decode_workspace_bytes",
     "launch_count",

@@ -32,6 +32,11 @@ __all__ = [
     "paged_norm_rope_store",
     "paged_prefill_attention",
     "paged_sparse_prefill_attention",
+    "paged_norm_rope_store_block_scaled",
+    "paged_decode_attention_block_scaled",
+    "paged_sparse_decode_attention_block_scaled",
+    "paged_prefill_attention_block_scaled",
+    "paged_sparse_prefill_attention_block_scaled",
     "prefill_attention_workspace_bytes",
     "decode_workspace_bytes",
     "launch_count",
@@ -106,6 +111,16 @@ def _load():
     L.paged_prefill_attention.restype = None
     L.paged_sparse_prefill_attention.argtypes = [B] * 9 + [i32, B, B, f32, i32, f32, f32, vp, sz, vp]
     L.paged_sparse_prefill_attention.restype = None
+    L.paged_norm_rope_store_block_scaled.argtypes = [B] * 13 + [f32, i32, i32, vp]
+    L.paged_norm_rope_store_block_scaled.restype = None
+    L.paged_decode_attention_block_scaled.argtypes = [B] * 9 + [f32, i32, vp, sz, vp]
+    L.paged_decode_attention_block_scaled.restype = None
+    L.paged_sparse_decode_attention_block_scaled.argtypes = [B] * 10 + [f32, i32, vp, sz, vp]
+    L.paged_sparse_decode_attention_block_scaled.restype = None
+    L.paged_prefill_attention_block_scaled.argtypes = [B] * 11 + [f32, i32, vp, sz, vp]
+    L.paged_prefill_attention_block_scaled.restype = None
+    L.paged_sparse_prefill_attention_block_scaled.argtypes = [B] * 11 + [i32, B, B, f32, i32, vp, sz, vp]
+    L.paged_sparse_prefill_attention_block_scaled.restype = None
     L.spd_prefill_attention_workspace_bytes.argtypes = [ctypes.c_int64] * 7
     L.spd_prefill_attention_workspace_bytes.restype = sz
     L.attention_sdpa.argtypes = [P, P, P, P, f32, i32, vp]
@@ -378,6 +393,97 @@ def paged_sparse_prefill_attention(q, k_cache, v_cache, block_table, slot_ids, c
         _pack(seq_lens, "seq_lens", d), _pack(prefix_lens, "prefix_lens", d), _pack(topk_idx, "topk_idx", d),
         block_size_q, _pack(cu_seqblocks_q, "cu_seqblocks_q", d), _pack(out, "out", d), sm_scale, block_size, k_scale,
         v_scale, *_scratch(workspace, d), raw)
+    _check_fast()
+
+
+def paged_norm_rope_store_block_scaled(q, k, v, q_weight, k_weight, cos_sin, token_lens, slots, q_out, k_cache, v_cache,
+                                       k_scales, v_scales, eps, interleaved, block_size, stream=None) -> None:
+    """paged_norm_rope_store into E4M3 caches with one scale for each page and
+    kv head: ``k_scales`` and ``v_scales`` [P, Hkv] f32 grow in place, as
+    powers of two, with what is stored, and the codes that a page holds
+    already follow."""
+    if _fast is not None:
+        _fast.paged_norm_rope_store_block_scaled(q, k, v, q_weight, k_weight, cos_sin, token_lens, slots, q_out, k_cache,
+            v_cache, k_scales, v_scales, eps, 1 if interleaved else 0, block_size, _raw(stream))
+        return
+    d, raw = _place(stream)
+    lib.paged_norm_rope_store_block_scaled(
+        _pack(q, "q", d), _pack(k, "k", d), _pack(v, "v", d), _pack(q_weight, "q_weight", d),
+        _pack(k_weight, "k_weight", d), _pack(cos_sin, "cos_sin", d), _pack(token_lens, "token_lens", d),
+        _pack(slots, "slots", d), _pack(q_out, "q_out", d), _pack(k_cache, "k_cache", d), _pack(v_cache, "v_cache", d),
+        _pack(k_scales, "k_scales", d), _pack(v_scales, "v_scales", d), eps, 1 if interleaved else 0, block_size, raw)
+    _check_fast()
+
+
+def paged_decode_attention_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, req_idx, out,
+                                        sm_scale, block_size, workspace, stream=None) -> None:
+    """paged_decode_attention over E4M3 caches with one scale for each page and
+    kv head (``k_scales``, ``v_scales`` [P, Hkv] f32)."""
+    if _fast is not None:
+        _fast.paged_decode_attention_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, req_idx,
+            out, sm_scale, block_size, workspace, _raw(stream))
+        return
+    d, raw = _place(stream)
+    lib.paged_decode_attention_block_scaled(
+        _pack(q, "q", d), _pack(k_cache, "k_cache", d), _pack(v_cache, "v_cache", d), _pack(k_scales, "k_scales", d),
+        _pack(v_scales, "v_scales", d), _pack(block_table, "block_table", d), _pack(seq_lens, "seq_lens", d),
+        _pack(req_idx, "req_idx", d), _pack(out, "out", d), sm_scale, block_size, *_scratch(workspace, d), raw)
+    _check_fast()
+
+
+def paged_sparse_decode_attention_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, req_idx,
+                                               topk_idx, out, sm_scale, block_size, workspace, stream=None) -> None:
+    """paged_sparse_decode_attention over E4M3 caches with one scale for each
+    page and kv head."""
+    if _fast is not None:
+        _fast.paged_sparse_decode_attention_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens,
+            req_idx, topk_idx, out, sm_scale, block_size, workspace, _raw(stream))
+        return
+    d, raw = _place(stream)
+    lib.paged_sparse_decode_attention_block_scaled(
+        _pack(q, "q", d), _pack(k_cache, "k_cache", d), _pack(v_cache, "v_cache", d), _pack(k_scales, "k_scales", d),
+        _pack(v_scales, "v_scales", d), _pack(block_table, "block_table", d), _pack(seq_lens, "seq_lens", d),
+        _pack(req_idx, "req_idx", d), _pack(topk_idx, "topk_idx", d), _pack(out, "out", d), sm_scale, block_size,
+        *_scratch(workspace, d), raw)
+    _check_fast()
+
+
+def paged_prefill_attention_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, slot_ids, cu_seqlens,
+                                         seq_lens, prefix_lens, out, sm_scale, block_size, workspace,
+                                         stream=None) -> None:
+    """paged_prefill_attention over E4M3 caches with one scale for each page
+    and kv head."""
+    if _fast is not None:
+        _fast.paged_prefill_attention_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, slot_ids,
+            cu_seqlens, seq_lens, prefix_lens, out, sm_scale, block_size, workspace, _raw(stream))
+        return
+    d, raw = _place(stream)
+    lib.paged_prefill_attention_block_scaled(
+        _pack(q, "q", d), _pack(k_cache, "k_cache", d), _pack(v_cache, "v_cache", d), _pack(k_scales, "k_scales", d),
+        _pack(v_scales, "v_scales", d), _pack(block_table, "block_table", d), _pack(slot_ids, "slot_ids", d),
+        _pack(cu_seqlens, "cu_seqlens", d), _pack(seq_lens, "seq_lens", d), _pack(prefix_lens, "prefix_lens", d),
+        _pack(out, "out", d), sm_scale, block_size, *_scratch(workspace, d), raw)
+    _check_fast()
+
+
+def paged_sparse_prefill_attention_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, slot_ids,
+                                                cu_seqlens, seq_lens, prefix_lens, topk_idx, block_size_q,
+                                                cu_seqblocks_q, out, sm_scale, block_size, workspace,
+                                                stream=None) -> None:
+    """paged_sparse_prefill_attention over E4M3 caches with one scale for each
+    page and kv head."""
+    if _fast is not None:
+        _fast.paged_sparse_prefill_attention_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, slot_ids,
+            cu_seqlens, seq_lens, prefix_lens, topk_idx, block_size_q, cu_seqblocks_q, out, sm_scale, block_size,
+            workspace, _raw(stream))
+        return
+    d, raw = _place(stream)
+    lib.paged_sparse_prefill_attention_block_scaled(
+        _pack(q, "q", d), _pack(k_cache, "k_cache", d), _pack(v_cache, "v_cache", d), _pack(k_scales, "k_scales", d),
+        _pack(v_scales, "v_scales", d), _pack(block_table, "block_table", d), _pack(slot_ids, "slot_ids", d),
+        _pack(cu_seqlens, "cu_seqlens", d), _pack(seq_lens, "seq_lens", d), _pack(prefix_lens, "prefix_lens", d),
+        _pack(topk_idx, "topk_idx", d), block_size_q, _pack(cu_seqblocks_q, "cu_seqblocks_q", d), _pack(out, "out", d),
+        sm_scale, block_size, *_scratch(workspace, d), raw)
     _check_fast()
 
 

@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kThreads) chunk_generic_kernel(const ChunkArgs
         if (page < 0 || page >= a.P) continue;
         any = true;
         const int64_t base = page * kBlock;
+        const float zs = zscale * page_k_scale(a.sc, page, h), vs = page_v_scale(a.sc, page, h);
         const int n_valid = min(kBlock, L - kb * kBlock);
         if (tid < n_valid) {
             const int64_t krow = (base + tid) * a.k_s0 + h * a.k_s1;
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) chunk_generic_kernel(const ChunkArgs
             }
 #pragma unroll
             for (int g = 0; g < kMaxGroup; ++g)
-                if (g < G) ps[g][tid] = z[g] * zscale;
+                if (g < G) ps[g][tid] = z[g] * zs;
         }
         __syncthreads();
         if (tid < G) {
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) chunk_generic_kernel(const ChunkArgs
             }
 #pragma unroll
             for (int g = 0; g < kMaxGroup; ++g)
-                if (g < G) acc[c][g] = acc[c][g] * alpha_s[g] + part[g];
+                if (g < G) acc[c][g] = fmaf(acc[c][g], alpha_s[g], part[g] * vs);
         }
         __syncthreads();
     }

@@ -286,6 +286,8 @@ attention_generic_kernel(AttnArgs a) {
         if (page < 0 || page >= a.P) continue;
         const int64_t base = page * kBlock;
 
+        const float zs = zscale * page_k_scale(a.sc, page, h), vs = page_v_scale(a.sc, page, h);
+
         // logits of token tid for every q head
         const bool valid = static_cast<int64_t>(b) * kBlock + tid < L;
         if (valid) {
@@ -301,7 +303,7 @@ attention_generic_kernel(AttnArgs a) {
             }
 #pragma unroll
             for (int g = 0; g < kMaxGroup; ++g)
-                if (g < G) ps[g][tid] = z[g] * zscale;
+                if (g < G) ps[g][tid] = z[g] * zs;
         } else {
             for (int g = 0; g < G; ++g) ps[g][tid] = -INFINITY;
         }
@@ -344,7 +346,7 @@ attention_generic_kernel(AttnArgs a) {
             }
 #pragma unroll
             for (int g = 0; g < kMaxGroup; ++g)
-                if (g < G) acc[c][g] = acc[c][g] * alpha_s[g] + part[g];
+                if (g < G) acc[c][g] = fmaf(acc[c][g], alpha_s[g], part[g] * vs);
         }
         __syncthreads();
     }

@@ -27,6 +27,11 @@ decltype(&paged_assign_slots) p_assign = nullptr;
 decltype(&paged_norm_rope_store) p_store = nullptr;
 decltype(&paged_prefill_attention) p_dense = nullptr;
 decltype(&paged_sparse_prefill_attention) p_sparse = nullptr;
+decltype(&paged_norm_rope_store_block_scaled) p_store_bs = nullptr;
+decltype(&paged_decode_attention_block_scaled) p_decode_bs = nullptr;
+decltype(&paged_sparse_decode_attention_block_scaled) p_sparse_decode_bs = nullptr;
+decltype(&paged_prefill_attention_block_scaled) p_dense_bs = nullptr;
+decltype(&paged_sparse_prefill_attention_block_scaled) p_sparse_bs = nullptr;
 decltype(&spd_last_error) p_error = nullptr;
 PyObject *raise_last = nullptr;  // Python callable that raises the library's last error
 
@@ -217,6 +222,73 @@ PyObject *attention(PyObject *const *a, Py_ssize_t n, bool sparse) {
 PyObject *dense_attention(PyObject *, PyObject *const *a, Py_ssize_t n) { return attention(a, n, false); }
 PyObject *sparse_attention(PyObject *, PyObject *const *a, Py_ssize_t n) { return attention(a, n, true); }
 
+PyObject *store_block(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Args x(a, n, 17);
+        const auto *q = x.tensor("q"), *k = x.tensor("k"), *v = x.tensor("v"), *wq = x.tensor("q_weight"),
+                   *wk = x.tensor("k_weight"), *cs = x.tensor("cos_sin"), *tl = x.tensor("token_lens"),
+                   *slots = x.tensor("slots"), *qo = x.tensor("q_out"), *kc = x.tensor("k_cache"),
+                   *vc = x.tensor("v_cache"), *ks = x.tensor("k_scales"), *vs = x.tensor("v_scales");
+        const float eps = x.real();
+        const int32_t inter = x.integer(), bs = x.integer();
+        const spd_stream_t s = x.stream();
+        if (!x.ok) return nullptr;
+        p_store_bs(q, k, v, wq, wk, cs, tl, slots, qo, kc, vc, ks, vs, eps, inter, bs, s);
+        return done();
+    });
+}
+
+PyObject *decode_block(PyObject *const *a, Py_ssize_t n, bool sparse) {
+    return guarded([&]() -> PyObject * {
+        Args x(a, n, sparse ? 14 : 13);
+        const auto *q = x.tensor("q"), *k = x.tensor("k_cache"), *v = x.tensor("v_cache"), *ks = x.tensor("k_scales"),
+                   *vs = x.tensor("v_scales"), *bt = x.tensor("block_table"), *sl = x.tensor("seq_lens"),
+                   *ri = x.tensor("req_idx");
+        const spd_tensor *tk = sparse ? x.tensor("topk_idx") : nullptr;
+        const auto *out = x.tensor("out");
+        const float sm = x.real();
+        const int32_t bs = x.integer();
+        size_t bytes = 0;
+        void *ws = x.workspace(&bytes);
+        const spd_stream_t s = x.stream();
+        if (!x.ok) return nullptr;
+        if (sparse) p_sparse_decode_bs(q, k, v, ks, vs, bt, sl, ri, tk, out, sm, bs, ws, bytes, s);
+        else p_decode_bs(q, k, v, ks, vs, bt, sl, ri, out, sm, bs, ws, bytes, s);
+        return done();
+    });
+}
+
+PyObject *attention_block(PyObject *const *a, Py_ssize_t n, bool sparse) {
+    return guarded([&]() -> PyObject * {
+        Args x(a, n, sparse ? 18 : 15);
+        const auto *q = x.tensor("q"), *k = x.tensor("k_cache"), *v = x.tensor("v_cache"), *ks = x.tensor("k_scales"),
+                   *vs = x.tensor("v_scales"), *bt = x.tensor("block_table"), *sid = x.tensor("slot_ids"),
+                   *cu = x.tensor("cu_seqlens"), *sl = x.tensor("seq_lens"), *pre = x.tensor("prefix_lens");
+        const spd_tensor *tk = nullptr, *cub = nullptr;
+        int32_t bq = 0;
+        if (sparse) {
+            tk = x.tensor("topk_idx");
+            bq = x.integer();
+            cub = x.tensor("cu_seqblocks_q");
+        }
+        const auto *out = x.tensor("out");
+        const float sm = x.real();
+        const int32_t bs = x.integer();
+        size_t bytes = 0;
+        void *ws = x.workspace(&bytes);
+        const spd_stream_t s = x.stream();
+        if (!x.ok) return nullptr;
+        if (sparse) p_sparse_bs(q, k, v, ks, vs, bt, sid, cu, sl, pre, tk, bq, cub, out, sm, bs, ws, bytes, s);
+        else p_dense_bs(q, k, v, ks, vs, bt, sid, cu, sl, pre, out, sm, bs, ws, bytes, s);
+        return done();
+    });
+}
+
+PyObject *decode_block_dense(PyObject *, PyObject *const *a, Py_ssize_t n) { return decode_block(a, n, false); }
+PyObject *decode_block_sparse(PyObject *, PyObject *const *a, Py_ssize_t n) { return decode_block(a, n, true); }
+PyObject *attention_block_dense(PyObject *, PyObject *const *a, Py_ssize_t n) { return attention_block(a, n, false); }
+PyObject *attention_block_sparse(PyObject *, PyObject *const *a, Py_ssize_t n) { return attention_block(a, n, true); }
+
 // bind(path of libspd.so, callable that raises its last error)
 PyObject *bind(PyObject *, PyObject *args) {
     const char *path = nullptr;
@@ -232,8 +304,15 @@ PyObject *bind(PyObject *, PyObject *args) {
     p_store = reinterpret_cast<decltype(p_store)>(get("paged_norm_rope_store"));
     p_dense = reinterpret_cast<decltype(p_dense)>(get("paged_prefill_attention"));
     p_sparse = reinterpret_cast<decltype(p_sparse)>(get("paged_sparse_prefill_attention"));
+    p_store_bs = reinterpret_cast<decltype(p_store_bs)>(get("paged_norm_rope_store_block_scaled"));
+    p_decode_bs = reinterpret_cast<decltype(p_decode_bs)>(get("paged_decode_attention_block_scaled"));
+    p_sparse_decode_bs =
+        reinterpret_cast<decltype(p_sparse_decode_bs)>(get("paged_sparse_decode_attention_block_scaled"));
+    p_dense_bs = reinterpret_cast<decltype(p_dense_bs)>(get("paged_prefill_attention_block_scaled"));
+    p_sparse_bs = reinterpret_cast<decltype(p_sparse_bs)>(get("paged_sparse_prefill_attention_block_scaled"));
     auto error = reinterpret_cast<decltype(p_error)>(get("spd_last_error"));
-    if (!p_assign || !p_store || !p_dense || !p_sparse || !error) {
+    if (!p_assign || !p_store || !p_dense || !p_sparse || !p_store_bs || !p_decode_bs || !p_sparse_decode_bs ||
+        !p_dense_bs || !p_sparse_bs || !error) {
         PyErr_SetString(PyExc_RuntimeError, "libspd.so lacks a serving-step call");
         return nullptr;
     }
@@ -250,6 +329,11 @@ PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, nullptr},
                          FAST("paged_norm_rope_store", store),
                          FAST("paged_prefill_attention", dense_attention),
                          FAST("paged_sparse_prefill_attention", sparse_attention),
+                         FAST("paged_norm_rope_store_block_scaled", store_block),
+                         FAST("paged_decode_attention_block_scaled", decode_block_dense),
+                         FAST("paged_sparse_decode_attention_block_scaled", decode_block_sparse),
+                         FAST("paged_prefill_attention_block_scaled", attention_block_dense),
+                         FAST("paged_sparse_prefill_attention_block_scaled", attention_block_sparse),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "spd_internal.cuh"
+
 namespace spd {
 
 constexpr int kMaxSeqs = 8192;  // requests of one call
@@ -47,11 +49,16 @@ struct StoreArgs {
     int32_t T, Hq, Hkv, D, Rd, M;
     int32_t interleaved;
     float eps, k_inv, v_inv;        // reciprocal scales
+    float *ks, *vs;                 // [P, Hkv] scales of block-scaled caches, or null
+    int64_t ks_s0, ks_s1, vs_s0, vs_s1;
 };
 
 cudaError_t launch_store_generic(const StoreArgs &a, cudaStream_t stream);
 cudaError_t launch_store_vec(const StoreArgs &a, cudaStream_t stream, bool *used);
 cudaError_t dispatch_store(const StoreArgs &a, cudaStream_t stream);
+
+cudaError_t launch_store_block_generic(const StoreArgs &a, cudaStream_t stream);
+cudaError_t dispatch_store_block(const StoreArgs &a, cudaStream_t stream);
 
 struct ChunkArgs {
     const void *q;                  // [total_q, Hq, D]
@@ -71,7 +78,8 @@ struct ChunkArgs {
     int32_t q_dt, kv_dt;
     int32_t total_q, Hq, Hkv, D, B, R, NB, n_rows, K, bsq;
     int64_t P;
-    float sm_scale, k_scale, v_scale;
+    float sm_scale, k_scale, v_scale;  // the last two 1 for block-scaled caches
+    PageScales sc;
 };
 
 cudaError_t launch_chunk_generic(const ChunkArgs &a, cudaStream_t stream);

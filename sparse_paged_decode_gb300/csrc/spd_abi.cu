@@ -158,6 +158,23 @@ bool check_paging(const spd_tensor *bt, const spd_tensor *sl, const spd_tensor *
     return true;
 }
 
+// Scales [P, Hkv] of a block-scaled cache of P pages.
+bool check_scales(const spd_tensor *t, const char *name, int64_t P, int64_t Hkv) {
+    if (!check_desc(t, name, 2, {SPD_F32})) return false;
+    if (t->shape[0] != P || t->shape[1] != Hkv)
+        return fail(SPD_ERR_INVALID_ARGUMENT, "%s must be [pages=%lld, Hkv=%lld]", name, (long long)P, (long long)Hkv);
+    return true;
+}
+
+PageScales page_scales(const spd_tensor *ks, const spd_tensor *vs) {
+    PageScales s{};
+    if (ks == nullptr) return s;
+    // a cache without pages has no scales either: nothing reads them
+    s.k = static_cast<const float *>(ks->data); s.k_s0 = ks->stride[0]; s.k_s1 = ks->stride[1];
+    s.v = static_cast<const float *>(vs->data); s.v_s0 = vs->stride[0]; s.v_s1 = vs->stride[1];
+    return s;
+}
+
 bool check_cuda(cudaError_t e, const char *what) {
     if (e != cudaSuccess)
         return fail(SPD_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -229,13 +246,24 @@ bool select_topk(const spd_tensor *s, const spd_tensor *o, cudaStream_t stream) 
 
 // ----------------------------------------------------------------- stage 3
 
+// What the attention calls know of their caches' scales: one static scale each,
+// or one a page and kv head (block-scaled calls, E4M3 caches only).
+struct Scales {
+    float k = 1.f, v = 1.f;
+    bool block = false;
+    const spd_tensor *ks = nullptr, *vs = nullptr;
+};
+
 bool attention(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v, const spd_tensor *bt,
                const spd_tensor *sl, const spd_tensor *ri, const spd_tensor *tk, const spd_tensor *out,
-               float sm_scale, int32_t block_size, float k_scale, float v_scale, void *ws, size_t ws_bytes,
+               float sm_scale, int32_t block_size, const Scales &sc, void *ws, size_t ws_bytes,
                cudaStream_t stream, const char *entry) {
+    const spd_tensor *ks = sc.ks, *vs = sc.vs;
     if (!check_desc(q, "q", 3, {SPD_F32, SPD_BF16, SPD_F16})) return false;
     if (!check_desc(k, "k_cache", 3, {SPD_E4M3, SPD_BF16})) return false;
     if (!check_desc(v, "v_cache", 3, {SPD_E4M3, SPD_BF16})) return false;
+    if (sc.block && (k->dtype != SPD_E4M3 || v->dtype != SPD_E4M3))
+        return fail(SPD_ERR_UNSUPPORTED, "%s: block-scaled caches hold e4m3", entry);
     if (k->dtype != v->dtype) return fail(SPD_ERR_INVALID_ARGUMENT, "k_cache and v_cache dtypes differ");
     if (!check_desc(out, "out", 3, {SPD_BF16})) return false;
     const int64_t T = q->shape[0], Hq = q->shape[1], D = q->shape[2];
@@ -261,10 +289,13 @@ bool attention(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v, co
         K = tk->shape[2];
         if (K < 1 || K > INT32_MAX / 2) return fail(SPD_ERR_INVALID_ARGUMENT, "topk_idx needs K >= 1");
     }
-    if (!check_scalar(sm_scale, "sm_scale") || !check_scalar(k_scale, "k_scale") || !check_scalar(v_scale, "v_scale"))
+    if (!check_scalar(sm_scale, "sm_scale") || !check_scalar(sc.k, "k_scale") || !check_scalar(sc.v, "v_scale"))
+        return false;
+    if (sc.block && (!check_scales(ks, "k_scales", k->shape[0] / kBlock, Hkv) ||
+                     !check_scales(vs, "v_scales", k->shape[0] / kBlock, Hkv)))
         return false;
     if (!check_output_layout(out, "out")) return false;
-    if (!check_no_overlap(out, "out", {q, k, v, bt, sl, ri, tk})) return false;
+    if (!check_no_overlap(out, "out", {q, k, v, bt, sl, ri, tk, ks, vs})) return false;
     const size_t need = spd_decode_workspace_bytes(T, Hq, Hkv, D, NB, block_size);
     if (need > 0) {
         if (ws == nullptr || ws_bytes < need)
@@ -295,7 +326,8 @@ bool attention(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v, co
     a.T = (int32_t)T; a.Hq = (int32_t)Hq; a.Hkv = (int32_t)Hkv; a.D = (int32_t)D;
     a.R = (int32_t)bt->shape[0]; a.NB = (int32_t)NB; a.K = (int32_t)K;
     a.P = k->shape[0] / kBlock;
-    a.sm_scale = sm_scale; a.k_scale = k_scale; a.v_scale = v_scale;
+    a.sm_scale = sm_scale; a.k_scale = sc.k; a.v_scale = sc.v;
+    a.sc = page_scales(ks, vs);
     return check_cuda(dispatch_attention(a, ws, ws_bytes, stream), entry);
 }
 
@@ -477,7 +509,8 @@ bool caches_interleave(const spd_tensor *k, const spd_tensor *v) {
 bool norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v, const spd_tensor *wq,
                      const spd_tensor *wk, const spd_tensor *cs, const spd_tensor *tl, const spd_tensor *slots,
                      const spd_tensor *qo, const spd_tensor *kc, const spd_tensor *vc, float eps,
-                     int32_t interleaved, int32_t block_size, float k_scale, float v_scale, cudaStream_t stream) {
+                     int32_t interleaved, int32_t block_size, const Scales &sc, cudaStream_t stream) {
+    const spd_tensor *ks = sc.ks, *vs = sc.vs;
     if (!check_desc(q, "q", 3, {SPD_F32, SPD_BF16, SPD_F16}) || !check_desc(k, "k", 3, {SPD_F32, SPD_BF16, SPD_F16}) ||
         !check_desc(cs, "cos_sin", 2, {SPD_F32}) || !check_desc(tl, "token_lens", 1, {SPD_I32}) ||
         !check_desc(slots, "slots", 1, {SPD_I32}) || !check_desc(qo, "q_out", 3, {SPD_F32, SPD_BF16, SPD_F16}) ||
@@ -485,6 +518,7 @@ bool norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_tensor 
         return false;
     if ((v == nullptr) != (vc == nullptr))
         return fail(SPD_ERR_INVALID_ARGUMENT, "v and v_cache must be given together");
+    if (sc.block && v == nullptr) return fail(SPD_ERR_INVALID_ARGUMENT, "v and v_cache are needed");
     if (v != nullptr && (!check_desc(v, "v", 3, {SPD_F32, SPD_BF16, SPD_F16}) ||
                          !check_desc(vc, "v_cache", 3, {SPD_F32, SPD_BF16, SPD_F16, SPD_E4M3})))
         return false;
@@ -498,6 +532,7 @@ bool norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_tensor 
     if (k->dtype != q->dtype || (v != nullptr && v->dtype != q->dtype))
         return fail(SPD_ERR_UNSUPPORTED, "k and v must have the dtype of q");
     if (vc != nullptr && vc->dtype != kc->dtype) return fail(SPD_ERR_INVALID_ARGUMENT, "k_cache and v_cache dtypes differ");
+    if (sc.block && kc->dtype != SPD_E4M3) return fail(SPD_ERR_UNSUPPORTED, "block-scaled caches hold e4m3");
     if (k->shape[0] != T || k->shape[2] != D) return fail(SPD_ERR_INVALID_ARGUMENT, "k must be [T, Hkv, D] with q's T and D");
     if (tl->shape[0] != T || slots->shape[0] != T)
         return fail(SPD_ERR_INVALID_ARGUMENT, "token_lens and slots must have T=%lld entries", (long long)T);
@@ -520,10 +555,12 @@ bool norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_tensor 
         return fail(SPD_ERR_UNSUPPORTED, "too many tokens, positions or slots");
     if (!check_scalar(eps, "eps")) return false;
     if (eps < 0.f) return fail(SPD_ERR_INVALID_ARGUMENT, "eps must be >= 0");
-    const float k_inv = 1.f / k_scale, v_inv = 1.f / v_scale;
-    if (!(k_scale > 0.f) || !(v_scale > 0.f) || k_scale == INFINITY || v_scale == INFINITY || k_inv == INFINITY ||
-        v_inv == INFINITY)
+    const float k_inv = 1.f / sc.k, v_inv = 1.f / sc.v;
+    if (!(sc.k > 0.f) || !(sc.v > 0.f) || sc.k == INFINITY || sc.v == INFINITY || k_inv == INFINITY || v_inv == INFINITY)
         return fail(SPD_ERR_INVALID_ARGUMENT, "k_scale and v_scale must be finite and > 0 with finite reciprocals");
+    if (sc.block && (!check_scales(ks, "k_scales", kc->shape[0] / kBlock, Hkv) ||
+                     !check_scales(vs, "v_scales", kc->shape[0] / kBlock, Hkv)))
+        return false;
     if (!check_outputs({{qo, "q_out"}, {kc, "k_cache"}}, {q, k, v, wq, wk, cs, tl, slots})) return false;
     if (vc != nullptr && numel(vc) > 0) {
         if (!check_output_layout(vc, "v_cache") || !check_no_overlap(vc, "v_cache", {q, k, v, wq, wk, cs, tl, slots, qo}))
@@ -534,6 +571,8 @@ bool norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_tensor 
         if (alo < bhi && blo < ahi && !caches_interleave(kc, vc))
             return fail(SPD_ERR_ALIASING, "k_cache overlaps v_cache");
     }
+    if (sc.block && !check_outputs({{ks, "k_scales"}, {vs, "v_scales"}}, {q, k, v, wq, wk, cs, tl, slots, qo, kc, vc}))
+        return false;
     if (T == 0) return true;
 
     StoreArgs a{};
@@ -553,6 +592,11 @@ bool norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_tensor 
     a.T = (int32_t)T; a.Hq = (int32_t)Hq; a.Hkv = (int32_t)Hkv; a.D = (int32_t)D; a.Rd = (int32_t)Rd; a.M = (int32_t)M;
     a.interleaved = interleaved != 0;
     a.eps = eps; a.k_inv = k_inv; a.v_inv = v_inv;
+    if (sc.block) {
+        a.ks = static_cast<float *>(ks->data); a.ks_s0 = ks->stride[0]; a.ks_s1 = ks->stride[1];
+        a.vs = static_cast<float *>(vs->data); a.vs_s0 = vs->stride[0]; a.vs_s1 = vs->stride[1];
+        return check_cuda(dispatch_store_block(a, stream), "paged_norm_rope_store_block_scaled launch");
+    }
     return check_cuda(dispatch_store(a, stream), "paged_norm_rope_store launch");
 }
 
@@ -561,8 +605,9 @@ bool norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_tensor 
 bool prefill_attention(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v, const spd_tensor *bt,
                        const spd_tensor *sid, const spd_tensor *cu, const spd_tensor *sl, const spd_tensor *pre,
                        const spd_tensor *tk, int32_t bsq, const spd_tensor *cub, const spd_tensor *out,
-                       float sm_scale, int32_t block_size, float k_scale, float v_scale, bool sparse, void *ws,
+                       float sm_scale, int32_t block_size, const Scales &sc, bool sparse, void *ws,
                        size_t ws_bytes, cudaStream_t stream, const char *entry) {
+    const spd_tensor *ks = sc.ks, *vs = sc.vs;
     if (!check_desc(q, "q", 3, {SPD_F32, SPD_BF16, SPD_F16}) || !check_desc(k, "k_cache", 3, {SPD_E4M3, SPD_BF16}) ||
         !check_desc(v, "v_cache", 3, {SPD_E4M3, SPD_BF16}) || !check_desc(bt, "block_table", 2, {SPD_I32}) ||
         !check_desc(sid, "slot_ids", 1, {SPD_I32}) || !check_desc(cu, "cu_seqlens", 1, {SPD_I32}) ||
@@ -571,6 +616,8 @@ bool prefill_attention(const spd_tensor *q, const spd_tensor *k, const spd_tenso
         return false;
     if (sparse && (!check_desc(tk, "topk_idx", 3, {SPD_I32}) || !check_desc(cub, "cu_seqblocks_q", 1, {SPD_I32})))
         return false;
+    if (sc.block && (k->dtype != SPD_E4M3 || v->dtype != SPD_E4M3))
+        return fail(SPD_ERR_UNSUPPORTED, "%s: block-scaled caches hold e4m3", entry);
     if (k->dtype != v->dtype) return fail(SPD_ERR_INVALID_ARGUMENT, "k_cache and v_cache dtypes differ");
     const int64_t total_q = q->shape[0], Hq = q->shape[1], D = q->shape[2], Hkv = k->shape[1];
     const int64_t B = sid->shape[0], NB = bt->shape[1];
@@ -604,16 +651,19 @@ bool prefill_attention(const spd_tensor *q, const spd_tensor *k, const spd_tenso
     }
     if (out->shape[0] != total_q || out->shape[1] != Hq || out->shape[2] != D)
         return fail(SPD_ERR_INVALID_ARGUMENT, "out must be [total_q, Hq, D] like q");
-    if (!check_scalar(sm_scale, "sm_scale") || !check_scalar(k_scale, "k_scale") || !check_scalar(v_scale, "v_scale"))
+    if (!check_scalar(sm_scale, "sm_scale") || !check_scalar(sc.k, "k_scale") || !check_scalar(sc.v, "v_scale"))
         return false;
-    if (!check_outputs({{out, "out"}}, {q, k, v, bt, sid, cu, sl, pre, tk, cub})) return false;
+    if (sc.block && (!check_scales(ks, "k_scales", k->shape[0] / kBlock, Hkv) ||
+                     !check_scales(vs, "v_scales", k->shape[0] / kBlock, Hkv)))
+        return false;
+    if (!check_outputs({{out, "out"}}, {q, k, v, bt, sid, cu, sl, pre, tk, cub, ks, vs})) return false;
     const size_t need = spd_prefill_attention_workspace_bytes(total_q, Hq, Hkv, D, B, NB, n_rows);
     if (ws == nullptr || ws_bytes < need)
         return fail(SPD_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", entry, need, ws_bytes);
     if (reinterpret_cast<uintptr_t>(ws) % 256 != 0)
         return fail(SPD_ERR_WORKSPACE, "%s: workspace must be 256-byte aligned", entry);
     const uintptr_t wlo = reinterpret_cast<uintptr_t>(ws), whi = wlo + ws_bytes;
-    for (const spd_tensor *t : {out, q, k, v, bt, sid, cu, sl, pre, tk, cub}) {
+    for (const spd_tensor *t : {out, q, k, v, bt, sid, cu, sl, pre, tk, cub, ks, vs}) {
         if (t == nullptr || numel(t) == 0) continue;
         uintptr_t lo, hi;
         byte_span(t, &lo, &hi);
@@ -643,7 +693,8 @@ bool prefill_attention(const spd_tensor *q, const spd_tensor *k, const spd_tenso
     a.total_q = (int32_t)total_q; a.Hq = (int32_t)Hq; a.Hkv = (int32_t)Hkv; a.D = (int32_t)D;
     a.B = (int32_t)B; a.R = (int32_t)bt->shape[0]; a.NB = (int32_t)NB;
     a.P = k->shape[0] / kBlock;
-    a.sm_scale = sm_scale; a.k_scale = k_scale; a.v_scale = v_scale;
+    a.sm_scale = sm_scale; a.k_scale = sc.k; a.v_scale = sc.v;
+    a.sc = page_scales(ks, vs);
     return check_cuda(dispatch_chunk(a, ws, ws_bytes, stream), entry);
 }
 
@@ -757,7 +808,7 @@ void paged_sparse_decode_attention(const spd_tensor *q, const spd_tensor *k_cach
         return;
     }
     spd::attention(q, k_cache, v_cache, block_table, seq_lens, req_idx, topk_idx, out, sm_scale, block_size,
-                   k_scale, v_scale, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream),
+                   {k_scale, v_scale}, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream),
                    "paged_sparse_decode_attention");
 }
 
@@ -788,7 +839,7 @@ void paged_sparse_decode_attention_noalloc(const spd_tensor *q, const spd_tensor
     // everything the kernels need to start from zero (the per-pair merge
     // counters, the status word) is written by this call's planner kernel
     spd::attention(q, k_cache, v_cache, block_table, seq_lens, req_idx, topk_idx, out, sm_scale, block_size,
-                   k_scale, v_scale, ws, kNoAllocScratchBytes, reinterpret_cast<cudaStream_t>(stream),
+                   {k_scale, v_scale}, ws, kNoAllocScratchBytes, reinterpret_cast<cudaStream_t>(stream),
                    "paged_sparse_decode_attention_noalloc");
 }
 
@@ -798,7 +849,7 @@ void paged_decode_attention(const spd_tensor *q, const spd_tensor *k_cache, cons
                             float v_scale, void *workspace, size_t workspace_bytes, spd_stream_t stream) {
     spd::set_ok();
     spd::attention(q, k_cache, v_cache, block_table, seq_lens, req_idx, nullptr, out, sm_scale, block_size,
-                   k_scale, v_scale, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream),
+                   {k_scale, v_scale}, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream),
                    "paged_decode_attention");
 }
 
@@ -844,7 +895,7 @@ void paged_norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_t
                            float k_scale, float v_scale, spd_stream_t stream) {
     spd::set_ok();
     spd::norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, token_lens, slots, q_out, k_cache, v_cache, eps,
-                         interleaved, block_size, k_scale, v_scale, reinterpret_cast<cudaStream_t>(stream));
+                         interleaved, block_size, {k_scale, v_scale}, reinterpret_cast<cudaStream_t>(stream));
 }
 
 void paged_prefill_attention(const spd_tensor *q, const spd_tensor *k_cache, const spd_tensor *v_cache,
@@ -854,7 +905,7 @@ void paged_prefill_attention(const spd_tensor *q, const spd_tensor *k_cache, con
                              size_t workspace_bytes, spd_stream_t stream) {
     spd::set_ok();
     spd::prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqlens, seq_lens, prefix_lens, nullptr, 1,
-                           nullptr, out, sm_scale, block_size, k_scale, v_scale, false, workspace, workspace_bytes,
+                           nullptr, out, sm_scale, block_size, {k_scale, v_scale}, false, workspace, workspace_bytes,
                            reinterpret_cast<cudaStream_t>(stream), "paged_prefill_attention");
 }
 
@@ -867,8 +918,81 @@ void paged_sparse_prefill_attention(const spd_tensor *q, const spd_tensor *k_cac
                                     size_t workspace_bytes, spd_stream_t stream) {
     spd::set_ok();
     spd::prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqlens, seq_lens, prefix_lens, topk_idx,
-                           block_size_q, cu_seqblocks_q, out, sm_scale, block_size, k_scale, v_scale, true, workspace,
+                           block_size_q, cu_seqblocks_q, out, sm_scale, block_size, {k_scale, v_scale}, true, workspace,
                            workspace_bytes, reinterpret_cast<cudaStream_t>(stream), "paged_sparse_prefill_attention");
+}
+
+void paged_norm_rope_store_block_scaled(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v,
+                                        const spd_tensor *q_weight, const spd_tensor *k_weight,
+                                        const spd_tensor *cos_sin, const spd_tensor *token_lens,
+                                        const spd_tensor *slots, const spd_tensor *q_out, const spd_tensor *k_cache,
+                                        const spd_tensor *v_cache, const spd_tensor *k_scales,
+                                        const spd_tensor *v_scales, float eps, int32_t interleaved,
+                                        int32_t block_size, spd_stream_t stream) {
+    spd::set_ok();
+    spd::norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, token_lens, slots, q_out, k_cache, v_cache, eps,
+                         interleaved, block_size, {1.f, 1.f, true, k_scales, v_scales},
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+void paged_decode_attention_block_scaled(const spd_tensor *q, const spd_tensor *k_cache, const spd_tensor *v_cache,
+                                         const spd_tensor *k_scales, const spd_tensor *v_scales,
+                                         const spd_tensor *block_table, const spd_tensor *seq_lens,
+                                         const spd_tensor *req_idx, const spd_tensor *out, float sm_scale,
+                                         int32_t block_size, void *workspace, size_t workspace_bytes,
+                                         spd_stream_t stream) {
+    spd::set_ok();
+    spd::attention(q, k_cache, v_cache, block_table, seq_lens, req_idx, nullptr, out, sm_scale, block_size,
+                   {1.f, 1.f, true, k_scales, v_scales}, workspace, workspace_bytes,
+                   reinterpret_cast<cudaStream_t>(stream), "paged_decode_attention_block_scaled");
+}
+
+void paged_sparse_decode_attention_block_scaled(const spd_tensor *q, const spd_tensor *k_cache,
+                                                const spd_tensor *v_cache, const spd_tensor *k_scales,
+                                                const spd_tensor *v_scales, const spd_tensor *block_table,
+                                                const spd_tensor *seq_lens, const spd_tensor *req_idx,
+                                                const spd_tensor *topk_idx, const spd_tensor *out, float sm_scale,
+                                                int32_t block_size, void *workspace, size_t workspace_bytes,
+                                                spd_stream_t stream) {
+    spd::set_ok();
+    if (topk_idx == nullptr) {
+        spd::fail(SPD_ERR_INVALID_ARGUMENT,
+                  "topk_idx is NULL (use paged_decode_attention_block_scaled for dense decode)");
+        return;
+    }
+    spd::attention(q, k_cache, v_cache, block_table, seq_lens, req_idx, topk_idx, out, sm_scale, block_size,
+                   {1.f, 1.f, true, k_scales, v_scales}, workspace, workspace_bytes,
+                   reinterpret_cast<cudaStream_t>(stream), "paged_sparse_decode_attention_block_scaled");
+}
+
+void paged_prefill_attention_block_scaled(const spd_tensor *q, const spd_tensor *k_cache, const spd_tensor *v_cache,
+                                          const spd_tensor *k_scales, const spd_tensor *v_scales,
+                                          const spd_tensor *block_table, const spd_tensor *slot_ids,
+                                          const spd_tensor *cu_seqlens, const spd_tensor *seq_lens,
+                                          const spd_tensor *prefix_lens, const spd_tensor *out, float sm_scale,
+                                          int32_t block_size, void *workspace, size_t workspace_bytes,
+                                          spd_stream_t stream) {
+    spd::set_ok();
+    spd::prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqlens, seq_lens, prefix_lens, nullptr, 1,
+                           nullptr, out, sm_scale, block_size, {1.f, 1.f, true, k_scales, v_scales}, false, workspace,
+                           workspace_bytes, reinterpret_cast<cudaStream_t>(stream),
+                           "paged_prefill_attention_block_scaled");
+}
+
+void paged_sparse_prefill_attention_block_scaled(const spd_tensor *q, const spd_tensor *k_cache,
+                                                 const spd_tensor *v_cache, const spd_tensor *k_scales,
+                                                 const spd_tensor *v_scales, const spd_tensor *block_table,
+                                                 const spd_tensor *slot_ids, const spd_tensor *cu_seqlens,
+                                                 const spd_tensor *seq_lens, const spd_tensor *prefix_lens,
+                                                 const spd_tensor *topk_idx, int32_t block_size_q,
+                                                 const spd_tensor *cu_seqblocks_q, const spd_tensor *out,
+                                                 float sm_scale, int32_t block_size, void *workspace,
+                                                 size_t workspace_bytes, spd_stream_t stream) {
+    spd::set_ok();
+    spd::prefill_attention(q, k_cache, v_cache, block_table, slot_ids, cu_seqlens, seq_lens, prefix_lens, topk_idx,
+                           block_size_q, cu_seqblocks_q, out, sm_scale, block_size,
+                           {1.f, 1.f, true, k_scales, v_scales}, true, workspace, workspace_bytes,
+                           reinterpret_cast<cudaStream_t>(stream), "paged_sparse_prefill_attention_block_scaled");
 }
 
 size_t spd_prefill_attention_workspace_bytes(int64_t total_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t B,

@@ -49,6 +49,13 @@ struct SelectArgs {
     int32_t Hi, T, NB, K;
 };
 
+// Scales of block-scaled E4M3 caches: one per page and kv head.  k is null for
+// the calls whose caches have one static scale each.
+struct PageScales {
+    const float *k, *v;     // [P, Hkv]
+    int64_t k_s0, k_s1, v_s0, v_s1;
+};
+
 // Stage 3: paged decode attention (sparse when tk != nullptr).
 struct AttnArgs {
     const void *q;          // [T, Hq, D]
@@ -69,7 +76,8 @@ struct AttnArgs {
     int32_t q_dt, kv_dt;    // kv_dt: SPD_E4M3 or SPD_BF16 (both caches)
     int32_t T, Hq, Hkv, D, R, NB, K;
     int64_t P;
-    float sm_scale, k_scale, v_scale;
+    float sm_scale, k_scale, v_scale;  // the last two 1 for block-scaled caches
+    PageScales sc;
 };
 
 // ------------------------------------------------------------------ launchers
@@ -111,6 +119,16 @@ __device__ __forceinline__ float load_float(const void *base, int dt, int64_t of
 __device__ __forceinline__ float kv_value(const uint8_t *base, int kv_dt, int64_t off) {
     if (kv_dt == SPD_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(base)[off]);
     return e4m3_to_float(base[off]);
+}
+
+// A block's scale as attention takes it: the nearest value of [2^-64, 2^64], so
+// that products and reciprocals of scales stay finite (the smallest for a NaN).
+__device__ __forceinline__ float clip_scale(float s) { return fminf(fmaxf(s, 0x1p-64f), 0x1p64f); }
+__device__ __forceinline__ float page_k_scale(const PageScales &sc, int64_t page, int h) {
+    return sc.k == nullptr ? 1.f : clip_scale(sc.k[page * sc.k_s0 + h * sc.k_s1]);
+}
+__device__ __forceinline__ float page_v_scale(const PageScales &sc, int64_t page, int h) {
+    return sc.k == nullptr ? 1.f : clip_scale(sc.v[page * sc.v_s0 + h * sc.v_s1]);
 }
 
 // seq_len of query token t clipped to [0, NB*128]; 0 when its request row is
