@@ -44,7 +44,9 @@
 #include <cmath>
 #include <mutex>
 #include <set>
+#include <utility>
 
+#include "block_scale.cuh"
 #include "plan.cuh"
 #include "spd_internal.cuh"
 #include "tc_ptx.cuh"
@@ -66,6 +68,7 @@ constexpr int kSoftThreads = 128;
 constexpr int kConvThreads = 64;
 constexpr int kWarpTma = 4, kWarpMma = 5, kWarpConv = 6;
 constexpr int kStages = 3;         // K and V half-page stages of E4M3
+constexpr int kScaleRing = 4;      // pages of scales (block-scaled caches)
 constexpr int kTerms = 2;               // E4M3 terms of a bf16 query
 constexpr int kQTile = kM * 128;        // one query term: 128 rows x 128 bytes
 constexpr int kKVHalf = kHalf * 128;    // E4M3 half page of one kv head: 64 slots x 128 bytes
@@ -97,6 +100,10 @@ struct Shared {
     uint32_t tmem_base;
     int abort;
     int last;     // the unit that took the last ticket of its pair merges
+    // scales of a page, by page ordinal (block-scaled caches).  Three K stages of
+    // half pages let the loader be at most the fourth half page ahead of the one
+    // whose softmax runs: two pages on, of four.
+    float2 scale[kScaleRing];
 };
 
 // The barriers sit in the padding below the aligned tiles when it is large
@@ -125,6 +132,7 @@ struct RowsArgs {
     int64_t o_s0, o_s1, o_s2;
     int32_t T, Hq, Hkv, G, R, NB, gmax;
     float v_scale;
+    PageScales sc;
     char *ws;
     PlanLayout lay;
 };
@@ -280,6 +288,8 @@ __device__ void merge_pair(const RowsArgs &a, const PlanUnit &un, const float *p
     }
 }
 
+// kBs: block-scaled caches (block_scale.cuh).
+template <bool kBs>
 __global__ void __launch_bounds__(kThreads, 2)
 attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                            const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ RowsArgs a) {
@@ -302,7 +312,7 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
         tc::mbar_init(&sh.q_full, 1);
         tc::mbar_init(&sh.q_empty, 1);
         for (int i = 0; i < kStages; ++i) {
-            tc::mbar_init(&sh.k_full[i], 1);
+            tc::mbar_init(&sh.k_full[i], kBs ? 2 : 1);  // the copy, and the scales'
             tc::mbar_init(&sh.k_empty[i], 1);
             tc::mbar_init(&sh.v_full[i], 1);
             tc::mbar_init(&sh.v_empty[i], kConvThreads);
@@ -376,6 +386,12 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
                         if (gb >= kStages && !(ok = wait_or_abort(sh, &sh.k_empty[st], ph, status))) break;
                         tc::mbar_arrive_expect_tx(&sh.k_full[st], kKVHalf);
                         tc::tma_load_3d(smem + kOffK + st * kKVHalf, &tmap_k, &sh.k_full[st], 0, un.h, key0, policy);
+                        if (kBs) {
+                            if ((i & 1) == 0)
+                                load_block_scale(&sh.scale[(gb >> 1) % kScaleRing], a.sc, e.page, un.h, &sh.k_full[st]);
+                            else
+                                tc::mbar_arrive(&sh.k_full[st]);
+                        }
                         ++nk;
                         if (gb >= kStages && !(ok = wait_or_abort(sh, &sh.v_empty[st], ph, status))) break;
                         tc::mbar_arrive_expect_tx(&sh.v_full[st], kKVHalf);
@@ -595,6 +611,8 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
             // the row's logit factor: s c is the logit in log2 units
             const float c = active ? cfac[static_cast<int64_t>(un.t0 + j) * a.Hq + un.h * a.G + g] : 0.f;
             float m_run = -INFINITY, l = 0.f;
+            float cb = c;              // logit factor of the page
+            BlockScale bs = {1.f, 0.f, 1.f};
             PlanEntry e_next{}, e{};
             if (un.count > 0) e_next = lists[un.entry];
             const int nblk = 2 * un.count;  // half pages
@@ -611,6 +629,10 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
                 ok = warp_wait(sh, &sh.s_full[sb], (b >> 1) & 1, status);
                 if (!ok) break;
                 tc::tc_fence_after();
+                if (kBs && (i & 1) == 0) {
+                    bs = block_scale(sh.scale[(b >> 1) % kScaleRing]);
+                    cb = c * bs.k;
+                }
                 float s[kHalf];
                 if (warp_active) {
 #pragma unroll
@@ -628,7 +650,7 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
                     }
                     // block maximum of s c (c may be negative: then the minimum of s)
                     float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-                    if (c >= 0.f) {
+                    if (cb >= 0.f) {
 #pragma unroll
                         for (int k = 0; k < kHalf; k += 4) {
                             mx0 = fmaxf(mx0, s[k]);
@@ -646,7 +668,7 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
                         }
                     }
                     const float mraw = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-                    const float bm = (mraw == -INFINITY) ? -INFINITY : mraw * fabsf(c);
+                    const float bm = (mraw == -INFINITY) ? -INFINITY : (kBs ? fmaf(mraw, fabsf(cb), bs.lg_v) : mraw * fabsf(cb));
                     // raise the offset if the block's maximum runs more than
                     // 2^kRaise above it (or the row had none yet)
                     if (bm != -INFINITY && (m_run == -INFINITY || bm > m_run + kRaise)) {
@@ -654,26 +676,28 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
                         m_run = bm;
                         l *= alpha;
                     }
-                    const float m_eff = (m_run == -INFINITY) ? 0.f : m_run;
+                    const float m_eff = ((m_run == -INFINITY) ? 0.f : m_run) - (kBs ? bs.lg_v : 0.f);
+                    float sum = kBs ? 0.f : l;
                     // p = 2^(s c - m) in [0, 2^kRaise], f16; masked keys take
                     // p = 0 whatever the sign of c
                     if (lim >= kHalf) {
 #pragma unroll
                         for (int k = 0; k < kHalf; k += 2) {
-                            const float p0 = tc::ex2(fmaf(s[k], c, -m_eff));
-                            const float p1 = tc::ex2(fmaf(s[k + 1], c, -m_eff));
-                            l += p0 + p1;
+                            const float p0 = tc::ex2(fmaf(s[k], cb, -m_eff));
+                            const float p1 = tc::ex2(fmaf(s[k + 1], cb, -m_eff));
+                            sum += p0 + p1;
                             pk[k / 2] = tc::f32x2_to_f16x2(p0, p1);
                         }
                     } else {
 #pragma unroll
                         for (int k = 0; k < kHalf; k += 2) {
-                            const float p0 = (k < lim) ? tc::ex2(fmaf(s[k], c, -m_eff)) : 0.f;
-                            const float p1 = (k + 1 < lim) ? tc::ex2(fmaf(s[k + 1], c, -m_eff)) : 0.f;
-                            l += p0 + p1;
+                            const float p0 = (k < lim) ? tc::ex2(fmaf(s[k], cb, -m_eff)) : 0.f;
+                            const float p1 = (k + 1 < lim) ? tc::ex2(fmaf(s[k + 1], cb, -m_eff)) : 0.f;
+                            sum += p0 + p1;
                             pk[k / 2] = tc::f32x2_to_f16x2(p0, p1);
                         }
                     }
+                    l = kBs ? fmaf(sum, bs.inv_v, l) : sum;
                 }
                 // On the unit's last half page L the previous product must be
                 // done before P(L) is handed off: the epilogue then waits for
@@ -826,18 +850,18 @@ bool make_tmap_terms(CUtensorMap *m, const uint8_t *base, int64_t T, int64_t hq,
 }
 
 // The largest shared-memory carveout for the kernel on the current device
-// (two CTAs of 113 KB per SM), once per device.
+// (two CTAs of 113 KB per SM), once per device and kernel.
 cudaError_t prefer_shared_carveout(const void *func) {
     static std::mutex mu;
-    static std::set<int> done;
+    static std::set<std::pair<int, const void *>> done;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
-    if (done.count(dev)) return cudaSuccess;
+    if (done.count({dev, func})) return cudaSuccess;
     e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout,
                              static_cast<int>(cudaSharedmemCarveoutMaxShared));
-    if (e == cudaSuccess) done.insert(dev);
+    if (e == cudaSuccess) done.insert({dev, func});
     return e;
 }
 
@@ -871,8 +895,9 @@ cudaError_t launch_attention_e4m3_rows(const AttnArgs &a, void *ws, size_t ws_by
     // two persistent CTAs per SM
     const int sms = device_sm_count();
     const int ctas = 2 * sms;
-    cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(attention_e4m3_rows_kernel), kSmemBytes);
-    if (e == cudaSuccess) e = prefer_shared_carveout(reinterpret_cast<const void *>(attention_e4m3_rows_kernel));
+    const auto kernel = a.sc.k != nullptr ? attention_e4m3_rows_kernel<true> : attention_e4m3_rows_kernel<false>;
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), kSmemBytes);
+    if (e == cudaSuccess) e = prefer_shared_carveout(reinterpret_cast<const void *>(kernel));
     if (e != cudaSuccess) return e;
 
     PlanArgs p{};
@@ -903,6 +928,7 @@ cudaError_t launch_attention_e4m3_rows(const AttnArgs &a, void *ws, size_t ws_by
     t.out = a.out; t.o_s0 = a.o_s0; t.o_s1 = a.o_s1; t.o_s2 = a.o_s2;
     t.T = a.T; t.Hq = a.Hq; t.Hkv = a.Hkv; t.G = G; t.R = a.R; t.NB = a.NB; t.gmax = gmax;
     t.v_scale = a.v_scale;
+    t.sc = a.sc;
     t.ws = static_cast<char *>(ws);
     t.lay = lay;
     cudaLaunchConfig_t cfg = {};
@@ -915,7 +941,7 @@ cudaError_t launch_attention_e4m3_rows(const AttnArgs &a, void *ws, size_t ws_by
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attention_e4m3_rows_kernel, tq, tk, tv, t);
+    e = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, t);
     if (e == cudaSuccess) *used = true;
     return e;
 }

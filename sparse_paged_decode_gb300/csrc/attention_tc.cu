@@ -53,6 +53,8 @@
 #include <algorithm>
 #include <cmath>
 
+#include "block_scale.cuh"
+#include "f32x2.cuh"
 #include "plan.cuh"
 #include "spd_internal.cuh"
 #include "tc_ptx.cuh"
@@ -70,6 +72,7 @@ constexpr int kSoftThreads = 128;     // one softmax group
 constexpr int kConvThreads = 128;     // warps 12-15
 constexpr int kWarpConv = 12;         // first V-widening warp
 constexpr int kStages = 3;
+constexpr int kScaleRing = 8;         // pages of scales (block-scaled caches)
 constexpr int kTile = 128 * 128;      // bytes of one K or V tile
 constexpr int kNMax = 64;             // query rows per group (padded)
 constexpr int kMaxEntries = kPlanMaxNB;
@@ -101,6 +104,7 @@ struct TcArgs {
     int32_t terms;      // E4M3 query terms: 2 for bf16 queries (exact), 3 otherwise
     int32_t per_token;  // query terms loaded token by token (G >= 8), else one box per group
     float v_scale;
+    PageScales sc;
     char *ws;
     PlanLayout lay;
 };
@@ -141,6 +145,10 @@ struct __align__(16) Shared {
     int Lj[2][16];                  // key limit of each group row (double-buffered by unit)
     BlockRows ent[2][kMaxEntries];  // the unit's block list (double-buffered by unit)
     uint8_t nvalid[4][kMaxEntries];  // per V-widening warp: tokens of each block valid for some row
+    // scales of a page, by block ordinal (block-scaled caches).  V of block b + 2 is
+    // widened, and its stage given back, once block b's product is done: the
+    // loader is at most the fourth block ahead of one whose softmax runs.
+    float2 scale[kScaleRing];
 };
 
 // dynamic shared memory: E4M3 K and V stages, query terms, f16 V and P tiles
@@ -278,8 +286,9 @@ __device__ __forceinline__ void chunk16(const float (&x)[kNMax], int ch, float (
 // raise keeps both forms of each offset in shared memory (m or 0, and the
 // threshold: 2^kRaise, or -inf without an offset), so a column costs one
 // FMA, the mask and one compare.
+template <bool kBs>
 __device__ __forceinline__ bool load_u(const Shared &sh, int wg, int mb, int nch, bool stacked, uint32_t tS,
-                                       uint64_t colmask, float (&u)[kNMax]) {
+                                       uint64_t colmask, const BlockScale &bs, float (&u)[kNMax]) {
     // stacked: the second term's logits follow in chunks nch..2nch-1
     const int nld = stacked ? 2 * nch : nch;
 #pragma unroll
@@ -304,10 +313,19 @@ __device__ __forceinline__ bool load_u(const Shared &sh, int wg, int mb, int nch
             const float4 th = *reinterpret_cast<const float4 *>(&sh.thr[wg][c4]);
             const float cfs[4] = {cf.x, cf.y, cf.z, cf.w}, mes[4] = {me.x, me.y, me.z, me.w};
             const float ths[4] = {th.x, th.y, th.z, th.w};
+            float vs[4];
+            if (kBs) {  // u = (s ks) cfac + (log2 vs - m), two columns to an instruction
+                const uint64_t k2 = pair(bs.k, bs.k), lg2 = pair(bs.lg_v, bs.lg_v);
+#pragma unroll
+                for (int q = 0; q < 4; q += 2)
+                    unpair(fma2(mul2(pair(u[c4 + q], u[c4 + q + 1]), k2), pair(cfs[q], cfs[q + 1]),
+                                add2(lg2, pair(-mes[q], -mes[q + 1]))),
+                           vs[q], vs[q + 1]);
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int col = c4 + q;
-                const float v = fmaf(u[col], cfs[q], -mes[q]);
+                const float v = kBs ? vs[q] : fmaf(u[col], cfs[q], -mes[q]);
                 u[col] = ((colmask >> col) & 1) ? v : -INFINITY;
                 need[q] |= u[col] > ths[q];
             }
@@ -319,6 +337,7 @@ __device__ __forceinline__ bool load_u(const Shared &sh, int wg, int mb, int nch
 // The blocks of one unit that fall to this softmax group (global block index
 // b with b % 2 == group), N = 16 * nch query columns.  Returns false when the
 // CTA must stop (an abort, decided uniformly within the group).
+template <bool kBs>
 __device__ __forceinline__ bool unit_blocks(const Soft &c, const TcArgs &a, const PlanUnit &un, uint32_t gb) {
     Shared &sh = *c.sh;
     const int wg = c.wg, mb = c.mb;
@@ -352,9 +371,11 @@ __device__ __forceinline__ bool unit_blocks(const Soft &c, const TcArgs &a, cons
         const int sb = k & 1;  // S buffer of this block
         const uint32_t tS = c.tmem + kColS + (2 * wg + sb) * kSCols + c.lane_base;
         const bool have = warp_wait(sh, &sh.s_full[wg][sb], (k >> 1) & 1, c.status);
+        BlockScale bs = {1.f, 0.f, 1.f};
         if (have) {
             tc::tc_fence_after();
-            need = load_u(sh, wg, mb, nch, stacked, tS, colmask, u);
+            if (kBs) bs = block_scale(sh.scale[b % kScaleRing]);
+            need = load_u<kBs>(sh, wg, mb, nch, stacked, tS, colmask, bs, u);
         }
         // votes alternate between two slots by block parity: a warp can be at
         // most one block ahead of the slowest reader of its group
@@ -448,7 +469,7 @@ __device__ __forceinline__ bool unit_blocks(const Soft &c, const TcArgs &a, cons
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     p[q] = have ? tc::ex2(u[c8 + q]) : 0.f;
-                    lsum[c8 + q] += p[q];
+                    lsum[c8 + q] = kBs ? fmaf(p[q], bs.inv_v, lsum[c8 + q]) : lsum[c8 + q] + p[q];
                 }
                 uint4 w;
                 w.x = tc::f32x2_to_f16x2(p[0], p[1]);
@@ -668,6 +689,8 @@ __device__ __forceinline__ void resolve_ticket(const Soft &c, const TcArgs &a, P
     pm.un.pair = -1;
 }
 
+// kBs: block-scaled caches (block_scale.cuh).
+template <bool kBs>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                     const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ TcArgs a) {
@@ -684,7 +707,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     // planner; global memory is touched only after pdl_wait
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            tc::mbar_init(&sh.kv_full[i], 1);
+            tc::mbar_init(&sh.kv_full[i], kBs ? 2 : 1);  // the copies, and the scales'
             tc::mbar_init(&sh.kv_empty[i], kConvThreads + 1);  // V widened + Q K^T done
         }
         for (int i = 0; i < 2; ++i) {
@@ -788,6 +811,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                     tc::mbar_arrive_expect_tx(&sh.kv_full[st], 2 * kTile);
                     tc::tma_load_3d(smem + kOffK + st * kTile, &tmap_k, &sh.kv_full[st], 0, un.h, e.page * 128, policy);
                     tc::tma_load_3d(smem + kOffV + st * kTile, &tmap_v, &sh.kv_full[st], 0, un.h, e.page * 128, policy);
+                    if (kBs) load_block_scale(&sh.scale[lb % kScaleRing], a.sc, e.page, un.h, &sh.kv_full[st]);
                 }
                 if (!ok) break;
                 un = claim();
@@ -1053,7 +1077,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                 sh.thr[g][col] = -INFINITY;
             }
             soft_sync();
-            const bool ok = unit_blocks(c, a, un, gb);
+            const bool ok = unit_blocks<kBs>(c, a, un, gb);
             unit_finish(c, a, un, gb, ok);
             tc::mbar_arrive(&sh.meta_empty[c.mb]);
             gb += un.count;
@@ -1148,8 +1172,9 @@ cudaError_t launch_attention_tc(const AttnArgs &a, void *ws, size_t ws_bytes, cu
     if (!make_tmap(&tv, a.v, a.P * 128, a.Hkv, a.v_s0, a.v_s1)) return cudaSuccess;
 
     const int sms = device_sm_count();
+    const auto kernel = a.sc.k != nullptr ? attention_tc_kernel<true> : attention_tc_kernel<false>;
     {
-        cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(attention_tc_kernel), kSmemBytes);
+        cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), kSmemBytes);
         if (e != cudaSuccess) return e;
     }
 
@@ -1192,6 +1217,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, void *ws, size_t ws_bytes, cu
     t.terms = (a.q_dt == SPD_BF16) ? 2 : kTerms;  // bf16 queries are exact in two E4M3 terms
     t.per_token = per_token ? 1 : 0;
     t.v_scale = a.v_scale;
+    t.sc = a.sc;
     t.ws = static_cast<char *>(ws);
     t.lay = lay;
     cudaLaunchConfig_t cfg = {};
@@ -1204,7 +1230,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, void *ws, size_t ws_bytes, cu
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attention_tc_kernel, tk, tv, tq, t);
+    e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, tq, t);
     if (e == cudaSuccess) *used = true;
     return e;
 }

@@ -1,0 +1,47 @@
+// block_scale.cuh -- how the tensor-core attention kernels take the scales of
+// block-scaled E4M3 caches (one K and one V scale a page and kv head).
+//
+// With ks and vs the scales of a key's page, z its logit in log2 units and m
+// the row's running offset,
+//   z  = ks (q . k) c,   w = 2^(z + log2 vs - m),   O += w v,   l += w / vs
+// so O / l = sum 2^z vs v / sum 2^z: the V scale enters through the exponent.
+// The offset is a maximum of z + log2 vs, so the weights that are rounded to
+// 16 bits are relative to the largest product of weight and scale, whatever the
+// scales' range; no scaled copy of V is made, and partial sums of a row join as
+// without scales.  (A scale in the widened f16 values instead would leave the
+// range of f16 for scales 2^8 apart.)
+//
+// The loading thread copies a page's two scales beside its keys, with cp.async
+// and an arrival on the same barrier: a ring of kScaleRing pages, which no
+// loader runs ahead of (each kernel says why).
+#pragma once
+
+#include "spd_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace spd {
+
+struct BlockScale {
+    float k, lg_v, inv_v;  // the K scale, log2 of the V scale, its reciprocal
+};
+
+__device__ __forceinline__ BlockScale block_scale(float2 kv) {
+    BlockScale s;
+    const float v = clip_scale(kv.y);
+    const uint32_t bits = __float_as_uint(v);
+    s.k = clip_scale(kv.x);
+    // exponent and significand apart: exact for powers of two, 2^-22 off at most
+    s.lg_v = static_cast<float>(static_cast<int>(bits >> 23) - 127) +
+             __log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+    s.inv_v = 1.f / v;
+    return s;
+}
+
+// The two scales of a page and head on their way to `dst`, arriving on `bar`.
+__device__ __forceinline__ void load_block_scale(float2 *dst, const PageScales &sc, int64_t page, int h, uint64_t *bar) {
+    tc::cp_async4(&dst->x, sc.k + page * sc.k_s0 + h * sc.k_s1);
+    tc::cp_async4(&dst->y, sc.v + page * sc.v_s0 + h * sc.v_s1);
+    tc::cp_async_arrive(bar);
+}
+
+}  // namespace spd

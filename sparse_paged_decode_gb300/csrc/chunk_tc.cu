@@ -80,6 +80,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "block_scale.cuh"
 #include "chunk_plan.cuh"
 #include "f32x2.cuh"
 #include "spd_dispatch.h"
@@ -146,6 +147,11 @@ struct Ring {
     __device__ __forceinline__ uint32_t parity() const { return round & 1; }
 };
 
+// Pages of scales (block-scaled caches).  While a tile's softmax is on a page,
+// its products have taken or passed at most the next one, and three K pages at
+// most wait behind that: the loader is four pages ahead at most.
+constexpr int kScaleRing = 8;
+
 constexpr int kTakeShift = 14;
 constexpr uint32_t kBlockMask = (1u << kTakeShift) - 1;
 
@@ -181,6 +187,7 @@ struct Shared {
     int abort;
     uint64_t dual_ready;              // the second tile's sums of a dual unit
     float2 dual_stats[kRows];         // its rows' exponent offsets and sums
+    float2 scale[kScaleRing];         // scales of a page, by page ordinal
     float row_factor[2][2 * kRows];  // by parity of the units with products: what the queries' scaling takes from the logits
     UnitRec unit[2];
 };
@@ -525,7 +532,8 @@ __device__ __noinline__ void take_marked(const TcArgs &t, const UnitRec &u, int 
     }
 }
 
-template <int D, Mode M>
+// kBs: block-scaled caches (block_scale.cuh); E4M3 modes only.
+template <int D, Mode M, bool kBs>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TcArgs t) {
@@ -555,9 +563,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             tc::mbar_init(&sh.v_empty[i], 2);
         }
         for (int i = 0; i < 3; ++i) {
-            tc::mbar_init(&sh.k_full[i], M == kModeWide ? 4 : 1);  // its widening warps, or the copy
+            // its widening warps, or the copy (and the scales')
+            tc::mbar_init(&sh.k_full[i], M == kModeWide ? 4 : (kBs ? 2 : 1));
             tc::mbar_init(&sh.k_empty[i], 2);
-            tc::mbar_init(&sh.r_full[i], 1);
+            tc::mbar_init(&sh.r_full[i], M == kModeWide && kBs ? 2 : 1);
             tc::mbar_init(&sh.r_empty[i], 4);
         }
         tc::mbar_init(&sh.dual_ready, 4);
@@ -593,6 +602,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         const bool in_tile = r < t.lay.tt * t.G;
         uint32_t n_s = 0, n_o = 0;  // S buffers seen, O tiles seen
         uint32_t nq = 0, n_dual = 0;  // units with products, dual units
+        uint32_t n_pages = 0;         // pages of the units so far
         for (uint32_t n = 0;; ++n) {
             UnitRec &u = sh.unit[n & 1];
             if (!warp_wait(sh, &sh.u_full[n & 1], (n >> 1) & 1) || u.nblk < 0) break;
@@ -601,8 +611,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             const int j_tok = tile_tok + (dual ? 0 : tile * t.lay.tt);  // token within the pair
             const bool have = in_tile && j_tok < u.nt;
             const int32_t lim = have ? row_limit(u, u.i0 + j_tok) : 0;
-            const uint32_t iq = nq;
+            const uint32_t iq = nq, page0 = n_pages;
             if (nblk > 0) ++nq;
+            n_pages += nblk;
             if (tile >= u.tiles) {
                 warp_arrive(&sh.u_empty[n & 1], lane);
                 continue;
@@ -628,8 +639,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             // f16 P starts at 2^7, so that small weights stay normal numbers
             // down to 2^-21 of the largest (and 2^kRaise more fits below 65504)
             constexpr float kLift = kBf16 ? 0.f : 7.f;
-            const uint64_t c2 = pair(c, c);
+            uint64_t c2 = pair(c, c);
             uint64_t m2 = 0;              // minus the offset, twice (0 while the row has none)
+            // block-scaled: the page's logit factor and its V scale; the threshold
+            // is in log2 units then, m2 without the V scale
+            float cb = c;
+            BlockScale bs = {1.f, 0.f, 1.f};
             bool seen = false, ok = true;
             int word_at = -1;
             uint32_t word = 0;
@@ -659,6 +674,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     ok = warp_wait(sh, &sh.s_full[tile][h], n_s & 1);
                     if (!ok) break;
                     tc::tc_fence_after();
+                    if (kBs && h == 0) {
+                        bs = block_scale(sh.scale[(page0 + j) % kScaleRing]);
+                        cb = fmaxf(c * bs.k, 1e-37f);  // above 0: masked logits are -inf
+                        c2 = pair(cb, cb);
+                    }
                     float x[kHalf], top[2];
                     top[0] = tmem_ld32_max(col_s + h * kHalf, x);
                     top[1] = tmem_ld32_max(col_s + h * kHalf + 32, x + 32);
@@ -677,6 +697,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         for (int ch = 0; ch < 2; ++ch) tmem_st16u(col_s + h * kHalf + ch * 16, zero);
                     } else {
                         float mx = fmaxf(top[0], top[1]);
+                        if (kBs) mx = fmaf(mx, cb, bs.lg_v);
                         if (__any_sync(0xffffffffu, left < kHalf || mx > threshold)) {
                             if (left < kHalf) {
                                 mx = -INFINITY;
@@ -685,19 +706,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                                     x[i] = i < left ? x[i] : -INFINITY;
                                     mx = fmaxf(mx, x[i]);
                                 }
+                                if (kBs) mx = fmaf(mx, cb, bs.lg_v);
                             }
                             // raise the offset if the step's maximum runs more
                             // than 2^kRaise above it (or the row had none yet)
                             const bool raise = mx > threshold;
                             float alpha = 1.f;
                             if (raise) {
-                                const float bm = fmaf(mx, c, -kLift);
+                                const float bm = kBs ? mx - kLift : fmaf(mx, c, -kLift);
                                 alpha = tc::ex2(m_run - bm);  // 0 for a row that had none
                                 m_run = bm;
                                 l *= alpha;
                                 // lower by what the rounding of large offsets
                                 // may add, so that p stays below 2^(kLift + kRaise)
-                                threshold = fmaxf(mx, fmaf(fabsf(m_run), -0x1p-22f, m_run + (kLift + kRaise)) / c);
+                                const float most = fmaf(fabsf(m_run), -0x1p-22f, m_run + (kLift + kRaise));
+                                threshold = fmaxf(mx, kBs ? most : most / c);
                                 m2 = pair(-m_run, -m_run);
                             }
                             if ((done > 0 || h == 1) && __any_sync(0xffffffffu, raise)) {
@@ -716,13 +739,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                                 }
                             }
                         }
+                        const uint64_t off2 = kBs ? add2(m2, pair(bs.lg_v, bs.lg_v)) : m2;
 #pragma unroll
                         for (int ch = 0; ch < 2; ++ch) {
                             uint32_t pk[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 float x0, x1;
-                                unpair(fma2(pair(x[ch * 32 + 2 * i], x[ch * 32 + 2 * i + 1]), c2, m2), x0, x1);
+                                unpair(fma2(pair(x[ch * 32 + 2 * i], x[ch * 32 + 2 * i + 1]), c2, off2), x0, x1);
                                 const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
                                 sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
                                 pk[i] = pack2(p0, p1, kBf16);
@@ -735,7 +759,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     warp_arrive(&sh.p_full[tile][h], lane);
                     float l0, l1;
                     unpair(add2(sum[0], sum[1]), l0, l1);
-                    l += l0 + l1;
+                    l = kBs ? fmaf(l0 + l1, bs.inv_v, l) : l + (l0 + l1);
                 }
                 ++done;
                 ++n_s;
@@ -991,7 +1015,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 Ring<S::kKs> rk;
                 Ring<S::kVs> rv;
                 Ring<F8 ? S::kRs : 1> rr;
-                uint32_t nq = 0;
+                uint32_t nq = 0, n_pages = 0;
                 bool ok = true;
                 // the next page of a ring, once its slot's last round has been read
                 auto room = [&](const auto &ring, uint64_t *empty) {
@@ -1016,6 +1040,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                             ok = room(rr, sh.r_empty);
                             if (!ok) break;
                             copy8(&tmap_k, smem + S::kOffRaw + rr.slot * S::kPage8, &sh.r_full[rr.slot], u.h, slot0);
+                            if (kBs) load_block_scale(&sh.scale[n_pages++ % kScaleRing], a.sc, u.page[j], u.h, &sh.r_full[rr.slot]);
                             rr.next();
                         } else {
                             ok = room(rk, sh.k_empty);
@@ -1023,6 +1048,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                             uint8_t *dst = smem + S::kOffK + rk.slot * S::kPageK;
                             if (M == kModeTerms) copy8(&tmap_k, dst, &sh.k_full[rk.slot], u.h, slot0);
                             else copy16(&tmap_k, dst, &sh.k_full[rk.slot], u.h, slot0);
+                            if (kBs) load_block_scale(&sh.scale[n_pages++ % kScaleRing], a.sc, u.page[j], u.h, &sh.k_full[rk.slot]);
                             rk.next();
                         }
                         if (j == 0) {
@@ -1041,6 +1067,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                             ok = room(rr, sh.r_empty);
                             if (!ok) break;
                             copy8(&tmap_v, smem + S::kOffRaw + rr.slot * S::kPage8, &sh.r_full[rr.slot], u.h, slot0);
+                            if (M == kModeWide && kBs) tc::mbar_arrive(&sh.r_full[rr.slot]);  // no scales beside V
                             rr.next();
                         } else {
                             ok = room(rv, sh.v_empty);
@@ -1528,7 +1555,7 @@ bool map_ok(const void *base, int es, int64_t s0, int64_t s1, int64_t n0, int64_
     return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (n1 <= 1 || legal(s1)) && (n0 <= 1 || legal(s0));
 }
 
-template <int D, Mode M>
+template <int D, Mode M, bool kBs = false>
 cudaError_t launch(const ChunkArgs &a, void *ws, cudaStream_t stream, bool *used) {
     using S = Shape<D, M>;
     constexpr bool F8 = S::kF8;
@@ -1547,7 +1574,7 @@ cudaError_t launch(const ChunkArgs &a, void *ws, cudaStream_t stream, bool *used
         !make_map(&mk, kv_type, es, a.k, D, a.Hkv, slots, ks1, a.k_s0, F8 ? D : 64, 1, kKeys) ||
         !make_map(&mv, kv_type, es, a.v, D, a.Hkv, slots, vs1, a.v_s0, F8 ? D : 64, 1, kKeys))
         return cudaSuccess;
-    const void *func = reinterpret_cast<const void *>(chunk_tc_kernel<D, M>);
+    const void *func = reinterpret_cast<const void *>(chunk_tc_kernel<D, M, kBs>);
     cudaError_t e = opt_in_smem(func, kSmem);
     if (e != cudaSuccess) return e;
 
@@ -1580,7 +1607,7 @@ cudaError_t launch(const ChunkArgs &a, void *ws, cudaStream_t stream, bool *used
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, M>, mq, mk, mv, t);
+    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, M, kBs>, mq, mk, mv, t);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(8 * p.ctas);
     cfg.blockDim = dim3(256);
@@ -1601,12 +1628,17 @@ cudaError_t launch_chunk_tc(const ChunkArgs &a, void *ws, cudaStream_t stream, b
     if (a.q_dt != SPD_BF16 && !(f8 && a.q_dt == SPD_F16)) return cudaSuccess;
     // the exponents need one sign, and the queries' scaling some headroom
     const float c = a.sm_scale * a.k_scale * kLog2e;
-    if (!(c > 1e-30f) || !(c < 1e30f)) return cudaSuccess;
+    const bool block = a.sc.k != nullptr;  // whose scales go down to 2^-64 and up to 2^64
+    if (!(c > (block ? 1e-10f : 1e-30f)) || !(c < (block ? 1e10f : 1e30f))) return cudaSuccess;
     const int es = f8 ? 1 : 2;
     if (a.P < 1 || a.q_s2 != 1 || !map_ok(a.q, 2, a.q_s0, a.q_s1, a.total_q, a.Hq) ||
         !map_ok(a.k, es, a.k_s0, a.k_s1, a.P * kKeys, a.Hkv) || !map_ok(a.v, es, a.v_s0, a.v_s1, a.P * kKeys, a.Hkv))
         return cudaSuccess;
     if (!f8) return a.D == 128 ? launch<128, kModeBf16>(a, ws, stream, used) : launch<64, kModeBf16>(a, ws, stream, used);
+    if (block) {
+        if (a.D == 128 && a.q_dt == SPD_BF16) return launch<128, kModeTerms, true>(a, ws, stream, used);
+        return a.D == 128 ? launch<128, kModeWide, true>(a, ws, stream, used) : launch<64, kModeWide, true>(a, ws, stream, used);
+    }
     // 64-dim terms would need rows of 64 bytes, f16 queries a third term: those are multiplied as f16
     if (a.D == 128 && a.q_dt == SPD_BF16) return launch<128, kModeTerms>(a, ws, stream, used);
     return a.D == 128 ? launch<128, kModeWide>(a, ws, stream, used) : launch<64, kModeWide>(a, ws, stream, used);

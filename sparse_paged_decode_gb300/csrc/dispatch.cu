@@ -97,7 +97,7 @@ cudaError_t dispatch_attention(const AttnArgs &a, void *workspace, size_t worksp
     // keys-on-lanes kernel otherwise: the first one's time per page does not
     // grow with the group's width up to 128 rows, the second one's does, and
     // it is the faster of the two for narrow groups.
-    const int pol = a.sc.k == nullptr ? g_policy[3] : 1;
+    const int pol = g_policy[3];
     if (pol == 0 && a.kv_dt == SPD_BF16) {
         e = launch_attention_bf16_tc(a, workspace, workspace_bytes, stream, &used);
     } else if (a.kv_dt == SPD_E4M3 && (pol == 0 || pol == 2 || pol == 3)) {

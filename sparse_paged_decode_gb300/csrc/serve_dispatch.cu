@@ -34,7 +34,7 @@ cudaError_t dispatch_store_block(const StoreArgs &a, cudaStream_t stream) {
 
 cudaError_t dispatch_chunk(const ChunkArgs &a, void *ws, size_t ws_bytes, cudaStream_t stream) {
     (void)ws_bytes;
-    if (g_serve_policy[0] == 0 && a.sc.k == nullptr) {
+    if (g_serve_policy[0] == 0) {
         bool used = false;
         const cudaError_t e = launch_chunk_tc(a, ws, stream, &used);
         if (e != cudaSuccess || used) return e;
