@@ -55,9 +55,12 @@ struct StoreArgs {
 
 cudaError_t launch_store_generic(const StoreArgs &a, cudaStream_t stream);
 cudaError_t launch_store_vec(const StoreArgs &a, cudaStream_t stream, bool *used);
+bool store_vec_covers(const StoreArgs &a);       // shapes and layouts of the vector kernels
+int store_row_groups(const StoreArgs &a, int n_kv);
 cudaError_t dispatch_store(const StoreArgs &a, cudaStream_t stream);
 
 cudaError_t launch_store_block_generic(const StoreArgs &a, cudaStream_t stream);
+cudaError_t launch_store_block_vec(const StoreArgs &a, cudaStream_t stream, bool *used);
 cudaError_t dispatch_store_block(const StoreArgs &a, cudaStream_t stream);
 
 struct ChunkArgs {

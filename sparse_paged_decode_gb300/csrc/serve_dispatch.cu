@@ -29,6 +29,11 @@ cudaError_t dispatch_store(const StoreArgs &a, cudaStream_t stream) {
 }
 
 cudaError_t dispatch_store_block(const StoreArgs &a, cudaStream_t stream) {
+    if (g_serve_policy[1] == 0) {
+        bool used = false;
+        const cudaError_t e = launch_store_block_vec(a, stream, &used);
+        if (e != cudaSuccess || used) return e;
+    }
     return launch_store_block_generic(a, stream);
 }
 
