@@ -94,16 +94,21 @@ __device__ __forceinline__ uint32_t round2(uint64_t x) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Four values as E4M3 codes, saturating.
+__device__ __forceinline__ uint32_t e4m3x4(uint64_t x0, uint64_t x1) {
+    float v[4];
+    unpair(x0, v[0], v[1]);
+    unpair(x1, v[2], v[3]);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
 // Four neighbouring values, rounded and stored at p.
 template <bool kBf16, bool kF8>
 __device__ __forceinline__ void store4(void *p, uint64_t x0, uint64_t x1) {
     if (kF8) {
-        float v[4];
-        unpair(x0, v[0], v[1]);
-        unpair(x1, v[2], v[3]);
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
-        *static_cast<uint32_t *>(p) = lo | (hi << 16);
+        *static_cast<uint32_t *>(p) = e4m3x4(x0, x1);
     } else {
         *static_cast<uint2 *>(p) = make_uint2(round2<kBf16>(x0), round2<kBf16>(x1));
     }

@@ -150,211 +150,258 @@ __global__ void __launch_bounds__(kWarps * 32) store_block_generic_kernel(const 
     }
 }
 
-// The layouts of the vector store (store.cuh), one launch: the first kv_blocks
-// CTAs append K and V, the others write the queries as store_vec_kernel does.
+// The layouts of the vector store (store.cuh), one launch: some CTAs append K
+// and V, the others write the queries as store_vec_kernel does.
 //
 // An appending CTA takes one K or V head of `tile` batch rows: the runs that
 // begin in them, with the rows behind the tile that end the last one.  Runs are
-// found by ballots over "row i does not continue row i - 1".  A run of more than
-// kShort rows is the whole CTA's work, a shorter one a warp's, and held codes
-// that grow are multiplied by the whole CTA behind all runs (16 KB at most: one
-// round trip).  Rows are read twice, for their maximum and to be stored: the
-// second time they come from L1 or L2, and nothing is kept between.
-constexpr int kShort = 16;
+// found by ballots over "row i does not continue row i - 1".  Then it goes from
+// run to run, as many at a time as have kKept rows together: its warps take the
+// rows in turn, whatever run they belong to, leave them in shared memory (K in
+// fp32, V as it came) and bring each run's largest magnitude together by an atomic
+// maximum (of the bits of numbers that are not negative: no order matters); one
+// thread a run fixes its scale; the rows are rounded and stored from shared
+// memory.  Held codes that grow are multiplied by the whole CTA behind that (16 KB
+// a run at most: one round trip).
 constexpr int kMaxTile = 128;
+constexpr int kKept = kBlock;  // rows kept in shared memory: a whole page's run
 
 struct Append {
     int32_t slot[kVecThreads];              // of row tile0 - 1 + i; -1 where it stores nothing
+    int32_t len[kVecThreads];
     uint32_t begins[kVecThreads / 32];      // bit per row: it does not continue the row before
     uint32_t leads[kVecThreads / 32];       // it begins a run of this tile
-    float top[kVecThreads / 32];
+    uint32_t top[kMaxTile + 1];             // by the row that begins the run: its largest magnitude's bits,
+    float inv[kMaxTile + 1];                // its scale's reciprocal
     int n_grown;
-    int32_t grown[kMaxTile];                // rows of short runs whose pages grow,
+    int32_t grown[kMaxTile];                // runs whose pages hold codes that grow,
     float ratio[kMaxTile];                  // and by what
 };
 
-// What the appending of one head works on.
-template <bool kBf16, int kLanes, int kMode>
-struct Head {
-    const StoreArgs &a;
-    const float *weights;                   // of K
-    const RowLane<kLanes, kMode> me;
-    const bool is_k, norm;
-    const int h, lane;                      // kv head, lane within a row's lanes
-    const uint16_t *src;
-    int64_t src_s0;
-    uint8_t *dst;                           // head h of slot 0
-    int64_t dst_s0;
-
-    __device__ __forceinline__ Head(const StoreArgs &a_, const float *w, bool k, int h_)
-        : a(a_), weights(w), me(a_, threadIdx.x % kLanes), is_k(k), norm(k && a_.wk != nullptr), h(h_),
-          lane(threadIdx.x % kLanes) {
-        src = static_cast<const uint16_t *>(is_k ? a.k : a.v) + h * (is_k ? a.k_s1 : a.v_s1);
-        src_s0 = is_k ? a.k_s0 : a.v_s0;
-        dst = static_cast<uint8_t *>(is_k ? a.kc : a.vc) + h * (is_k ? a.kc_s1 : a.vc_s1);
-        dst_s0 = is_k ? a.kc_s0 : a.vc_s0;
+// The larger of two pairs' magnitudes, each half for itself.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+    if (kBf16) {
+        const __nv_bfloat162 m = __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162 *>(&a)),
+                                         __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&b)));
+        return *reinterpret_cast<const uint32_t *>(&m);
     }
+    const __half2 m = __hmax2(__habs2(*reinterpret_cast<const __half2 *>(&a)), __habs2(*reinterpret_cast<const __half2 *>(&b)));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
 
-    // Rows t + j0, t + j0 + step, ... of a run of n rows, kBatch of them at a time
-    // (all loads, then the mathematics): f(j, y) for the row's values y.  Lanes
-    // whose row lies behind the run work on zeros, and get no call.
-    template <typename F>
-    __device__ __forceinline__ void rows(int64_t t, int n, int warp_row, int step, F &&f) const {
-        constexpr int kBatch = 2;
-        const int sub = threadIdx.x % 32 / kLanes;
-        for (int j0 = warp_row; j0 < n; j0 += kBatch * step) {  // the same for a warp's lanes
+// The largest finite magnitude of eight values.  A maximum passes NaN over; only
+// where an infinity comes out are the values looked at one by one.
+__device__ __forceinline__ float largest(const uint64_t (&y)[4]) {
+    float v[8], top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) unpair(y[e], v[2 * e], v[2 * e + 1]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+    if (top == INFINITY) {
+        top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs(v[e]));
+    }
+    return top;
+}
+
+template <bool kBf16, int kLanes, int kMode, bool kIsK>
+__device__ __forceinline__ void append_tile(const StoreArgs &a, const float *weights, Append &sh, uint4 *kept, int64_t tile0,
+                                            int tile, int h) {
+    constexpr int kWarps = kVecThreads / 32, kRows = 32 / kLanes;  // rows of a warp at a time
+    constexpr int kStep = kWarps * kRows;                          // of the CTA
+    constexpr int kBatch = kIsK ? 2 : 4;                           // such steps in flight (K has angles too)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = threadIdx.x % kLanes;
+    const uint16_t *src = static_cast<const uint16_t *>(kIsK ? a.k : a.v) + h * (kIsK ? a.k_s1 : a.v_s1);
+    const int64_t src_s0 = kIsK ? a.k_s0 : a.v_s0;
+    uint8_t *dst = static_cast<uint8_t *>(kIsK ? a.kc : a.vc) + h * (kIsK ? a.kc_s1 : a.vc_s1);  // slot 0
+    const int64_t dst_s0 = kIsK ? a.kc_s0 : a.vc_s0;
+    float *scale_at = nullptr;  // of the run that this thread's row begins
+    float old = 0.f;
+    {
+        const int i = threadIdx.x;
+        const int64_t t = tile0 - 1 + i;
+        Row r{0, -1, false, false};
+        if (t >= 0 && t < a.T) r = row_of(a, t);
+        const int32_t slot = r.stored ? r.slot : -1;
+        sh.slot[i] = slot;
+        sh.len[i] = r.len;
+        if (i <= kMaxTile) sh.top[i] = 0;
+        if (i == 0) sh.n_grown = 0;
+        __syncthreads();
+        const bool begins = !(i > 0 && slot >= 0 && slot % kBlock != 0 && sh.slot[i - 1] == slot - 1);
+        const bool leads = begins && slot >= 0 && i >= 1 && i <= tile;
+        if (leads) {
+            scale_at = (kIsK ? a.ks + h * a.ks_s1 : a.vs + h * a.vs_s1) + slot / kBlock * (kIsK ? a.ks_s0 : a.vs_s0);
+            if (slot % kBlock != 0) old = *scale_at;
+        }
+        const uint32_t b = __ballot_sync(0xffffffffu, begins), l = __ballot_sync(0xffffffffu, leads);
+        if (lane == 0) {
+            sh.begins[warp] = b;
+            sh.leads[warp] = l;
+        }
+        __syncthreads();
+    }
+    // the rows from the first run's beginning to the last one's end
+    int first = kVecThreads, end = 0;
+#pragma unroll
+    for (int w = 0; w <= kMaxTile / 32; ++w) {
+        const uint32_t l = sh.leads[w];
+        if (l == 0) continue;
+        first = min(first, w * 32 + __ffs(l) - 1);
+        end = w * 32 + 31 - __clz(l);
+    }
+    if (end == 0) {
+        __syncthreads();  // before another tile's rows
+        return;
+    }
+    {
+        int w = end >> 5;
+        uint32_t behind = sh.begins[w] & ~((2u << (end & 31)) - 1u);
+        while (behind == 0 && ++w < kWarps) behind = sh.begins[w];
+        end = behind != 0 ? w * 32 + __ffs(behind) - 1 : kVecThreads;
+    }
+    // the last row up to i that begins something (row 0 does)
+    auto begin_of = [&](int i) {
+        int w = i >> 5;
+        uint32_t before = sh.begins[w] & ((2u << (i & 31)) - 1u);
+        while (before == 0) before = sh.begins[--w];
+        return w * 32 + 31 - __clz(before);
+    };
+
+    const RowLane<kLanes, kMode> me(a, col);
+    const int da = kIsK ? me.da : 8 * col, db = kIsK ? me.db : da + 4;
+    const int sub = warp * kRows + lane / kLanes;
+    const bool wide = ((reinterpret_cast<uintptr_t>(dst) | static_cast<uintptr_t>(dst_s0)) & 7) == 0;
+    for (int lo = first, hi; lo < end; lo = hi) {
+        // whole runs: a run has at most kKept rows, so one fits
+        hi = end - lo <= kKept ? end : begin_of(lo + kKept);
+        const bool one = begin_of(hi - 1) == lo;  // a long run's rows by themselves, the common case of a chunk
+        float acc = 0.f;
+        for (int i0 = lo; i0 < hi; i0 += kStep * kBatch) {
+            // all loads of the turn, then the mathematics; a row that is not there is
+            // made of zeros
             uint2 wa[kBatch], wb[kBatch];
             float4 c[kBatch], s[kBatch];
+            bool there[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int j = j0 + i * step + sub;
-                wa[i] = wb[i] = make_uint2(0, 0);
-                c[i] = make_float4(1.f, 1.f, 1.f, 1.f);
-                s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (j < n) {
-                    const uint16_t *row = src + (t + j) * src_s0 + me.da;
-                    wa[i] = *reinterpret_cast<const uint2 *>(row);
-                    wb[i] = *reinterpret_cast<const uint2 *>(row + (me.db - me.da));
-                    if (is_k && me.turns) {
-                        const float *cs = a.cs + static_cast<int64_t>(a.tl[(t + j) * a.tl_s0] - 1) * a.cs_s0 + 4 * lane;
-                        c[i] = *reinterpret_cast<const float4 *>(cs);
-                        s[i] = *reinterpret_cast<const float4 *>(cs + a.Rd / 2);
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + sub + k * kStep;
+                there[k] = i < hi && (one || sh.slot[i] >= 0);
+                wa[k] = wb[k] = make_uint2(0, 0);
+                c[k] = make_float4(1.f, 1.f, 1.f, 1.f);
+                s[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (there[k]) {
+                    const uint16_t *row = src + (tile0 - 1 + i) * src_s0 + da;
+                    wa[k] = *reinterpret_cast<const uint2 *>(row);
+                    wb[k] = *reinterpret_cast<const uint2 *>(row + (db - da));
+                    if (kIsK && me.turns) {
+                        const float *cs = a.cs + static_cast<int64_t>(sh.len[i] - 1) * a.cs_s0 + 4 * col;
+                        c[k] = *reinterpret_cast<const float4 *>(cs);
+                        s[k] = *reinterpret_cast<const float4 *>(cs + a.Rd / 2);
                     }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int j = j0 + i * step + sub;
-                const uint64_t x[4] = {widen2<kBf16>(wa[i].x), widen2<kBf16>(wa[i].y), widen2<kBf16>(wb[i].x),
-                                       widen2<kBf16>(wb[i].y)};
-                uint64_t y[4] = {x[0], x[1], x[2], x[3]};
-                if (is_k) {  // the same for the whole CTA
-                    uint64_t own[4], cross[4];
-                    me.factors(weights, c[i], s[i], own, cross);
-                    me.turn(x, own, cross, norm, a.eps, y);
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + sub + k * kStep;
+                float top;
+                if (kIsK) {
+                    const uint64_t x[4] = {widen2<kBf16>(wa[k].x), widen2<kBf16>(wa[k].y), widen2<kBf16>(wb[k].x),
+                                           widen2<kBf16>(wb[k].y)};
+                    uint64_t own[4], cross[4], y[4];
+                    me.factors(weights, c[k], s[k], own, cross);
+                    me.turn(x, own, cross, a.wk != nullptr, a.eps, y);
+                    top = largest(y);
+                    if (there[k]) {
+                        ulonglong2 *row = reinterpret_cast<ulonglong2 *>(kept) + (i - lo) * (2 * kLanes);
+                        row[da / 4] = make_ulonglong2(y[0], y[1]);
+                        row[db / 4] = make_ulonglong2(y[2], y[3]);
+                    }
+                } else {
+                    const uint32_t m = max_abs2<kBf16>(max_abs2<kBf16>(wa[k].x, wa[k].y), max_abs2<kBf16>(wb[k].x, wb[k].y));
+                    float t0, t1;
+                    unpair(widen2<kBf16>(m), t0, t1);
+                    top = fmaxf(t0, t1);
+                    if (!(top < INFINITY)) {
+                        const uint64_t x[4] = {widen2<kBf16>(wa[k].x), widen2<kBf16>(wa[k].y), widen2<kBf16>(wb[k].x),
+                                               widen2<kBf16>(wb[k].y)};
+                        top = largest(x);
+                    }
+                    if (there[k]) kept[(i - lo) * kLanes + col] = make_uint4(wa[k].x, wa[k].y, wb[k].x, wb[k].y);
                 }
-                if (j < n) f(j, y);
+                if (one) {
+                    acc = fmaxf(acc, top);
+                } else {
+#pragma unroll
+                    for (int m = kLanes / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+                    if (there[k] && col == 0) atomicMax(&sh.top[begin_of(i)], __float_as_uint(top));
+                }
             }
         }
-    }
-
-    __device__ __forceinline__ float largest(int64_t t, int n, int warp_row, int step) const {
-        float top = 0.f;
-        rows(t, n, warp_row, step, [&](int, const uint64_t *y) {
+        if (one) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float lo, hi;
-                unpair(y[e], lo, hi);
-                top = fmaxf(top, fmaxf(finite_abs(lo), finite_abs(hi)));
-            }
-        });
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        return top;
-    }
-
-    __device__ __forceinline__ void keep(int64_t t, int n, int32_t slot, float scale, int warp_row, int step) const {
-        const float inv = 1.f / scale;
-        const uint64_t inv2 = pair(inv, inv);
-        rows(t, n, warp_row, step, [&](int j, const uint64_t *y) {
-            uint8_t *at = dst + (static_cast<int64_t>(slot) + j) * dst_s0 + me.da;
-            store4<kBf16, true>(at, mul2(y[0], inv2), mul2(y[1], inv2));
-            store4<kBf16, true>(at + (me.db - me.da), mul2(y[2], inv2), mul2(y[3], inv2));
-        });
-    }
-
-    // the f codes rows that a page holds, times ratio; the whole CTA
-    __device__ __forceinline__ void grow(int64_t page, int f, float ratio) const {
-        constexpr int kWords = 2 * kLanes, kBatch = 8;  // words of a row; of a thread at a time
-        for (int i0 = threadIdx.x; i0 < f * kWords; i0 += kBatch * kVecThreads) {
-            uint32_t w[kBatch];
-            auto at = [&](int i) {
-                return reinterpret_cast<uint32_t *>(dst + (page * kBlock + i / kWords) * dst_s0) + i % kWords;
-            };
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (i0 + k * kVecThreads < f * kWords) w[k] = *at(i0 + k * kVecThreads);
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (i0 + k * kVecThreads < f * kWords) {
-                    uint32_t out = 0;
-#pragma unroll
-                    for (int b = 0; b < 32; b += 8) out |= static_cast<uint32_t>(rescaled((w[k] >> b) & 0xffu, ratio)) << b;
-                    *at(i0 + k * kVecThreads) = out;
-                }
-        }
-    }
-};
-
-template <bool kBf16, int kLanes, int kMode>
-__device__ __forceinline__ void append_tile(const StoreArgs &a, const float *weights, Append &sh, int64_t tile0, int tile,
-                                            bool is_k, int h) {
-    constexpr int kWarps = kVecThreads / 32, kRows = 32 / kLanes;  // rows of a warp at a time
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = threadIdx.x;
-    {
-        const int64_t t = tile0 - 1 + i;
-        int32_t slot = -1;
-        if (t >= 0 && t < a.T) {
-            const Row r = row_of(a, t);
-            if (r.stored) slot = r.slot;
-        }
-        sh.slot[i] = slot;
-        if (i == 0) sh.n_grown = 0;
-        __syncthreads();
-        const bool continues = i > 0 && slot >= 0 && slot % kBlock != 0 && sh.slot[i - 1] == slot - 1;
-        const uint32_t begins = __ballot_sync(0xffffffffu, !continues);
-        const uint32_t leads = __ballot_sync(0xffffffffu, !continues && slot >= 0 && i >= 1 && i <= tile);
-        if (lane == 0) {
-            sh.begins[warp] = begins;
-            sh.leads[warp] = leads;
+            for (int m = 16; m > 0; m >>= 1) acc = fmaxf(acc, __shfl_xor_sync(0xffffffffu, acc, m));
+            if (lane == 0) atomicMax(&sh.top[lo], __float_as_uint(acc));
         }
         __syncthreads();
-    }
-    const Head<kBf16, kLanes, kMode> head(a, weights, is_k, h);
-    float *scales = is_k ? a.ks + h * a.ks_s1 : a.vs + h * a.vs_s1;
-    const int64_t scales_s0 = is_k ? a.ks_s0 : a.vs_s0;
-    int n_short = 0;
-    for (int w = 0; w * 32 <= tile; ++w) {
-        for (uint32_t bits = sh.leads[w]; bits != 0; bits &= bits - 1) {
-            const int at = w * 32 + __ffs(bits) - 1;
-            // the run ends where the next row begins something
-            int word = at >> 5;
-            uint32_t behind = sh.begins[word] & ~((2u << (at & 31)) - 1u);
-            while (behind == 0 && ++word < kWarps) behind = sh.begins[word];
-            const int n = (behind != 0 ? word * 32 + __ffs(behind) - 1 : kVecThreads) - at;
-            const bool whole = n > kShort;
-            if (!whole && n_short++ % kWarps != warp) continue;
-            const int32_t slot = sh.slot[at];
-            const int64_t t = tile0 - 1 + at, page = slot / kBlock;
-            const int f = slot % kBlock;
-            float *scale_at = scales + page * scales_s0;
-            const float old = f > 0 ? *scale_at : 0.f;
-            const int row0 = whole ? warp * kRows : 0, step = whole ? kWarps * kRows : kRows;
-            float top = head.largest(t, n, row0, step);
-            if (whole) {
-                if (lane == 0) sh.top[warp] = top;
-                __syncthreads();
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sh.top[k]);
-            }
+        if (scale_at != nullptr && threadIdx.x >= lo && threadIdx.x < hi) {
             float ratio;
-            const float scale = page_scale(top, old, ratio);
-            if (lane == 0 && (!whole || warp == 0)) {
-                *scale_at = scale;
-                if (ratio != 1.f) {
-                    const int k = atomicAdd(&sh.n_grown, 1);
-                    sh.grown[k] = at;
-                    sh.ratio[k] = ratio;
-                }
+            const float scale = page_scale(__uint_as_float(sh.top[threadIdx.x]), old, ratio);
+            *scale_at = scale;
+            sh.inv[threadIdx.x] = 1.f / scale;
+            if (ratio != 1.f) {
+                const int k = atomicAdd(&sh.n_grown, 1);
+                sh.grown[k] = threadIdx.x;
+                sh.ratio[k] = ratio;
             }
-            head.keep(t, n, slot, scale, row0, step);
-            if (whole) __syncthreads();  // before the next long run's maxima
         }
+        __syncthreads();
+        // a lane rounds and stores eight neighbouring dims
+        for (int i = lo + sub; i < hi; i += kStep) {
+            const int32_t slot = sh.slot[i];
+            if (slot < 0) continue;
+            const float inv = sh.inv[one ? lo : begin_of(i)];
+            const uint64_t inv2 = pair(inv, inv);
+            uint64_t y[4];
+            if (kIsK) {
+                const ulonglong2 *row = reinterpret_cast<const ulonglong2 *>(kept) + (i - lo) * (2 * kLanes) + 2 * col;
+                y[0] = row[0].x, y[1] = row[0].y, y[2] = row[1].x, y[3] = row[1].y;
+            } else {
+                const uint4 w = kept[(i - lo) * kLanes + col];
+                y[0] = widen2<kBf16>(w.x), y[1] = widen2<kBf16>(w.y), y[2] = widen2<kBf16>(w.z), y[3] = widen2<kBf16>(w.w);
+            }
+            const uint32_t c0 = e4m3x4(mul2(y[0], inv2), mul2(y[1], inv2)), c1 = e4m3x4(mul2(y[2], inv2), mul2(y[3], inv2));
+            uint8_t *at = dst + slot * dst_s0 + 8 * col;
+            if (wide) {
+                *reinterpret_cast<uint2 *>(at) = make_uint2(c0, c1);
+            } else {
+                reinterpret_cast<uint32_t *>(at)[0] = c0;
+                reinterpret_cast<uint32_t *>(at)[1] = c1;
+            }
+        }
+        __syncthreads();  // before other rows take their place
     }
-    __syncthreads();
-    for (int k = 0; k < sh.n_grown; ++k) {
-        const int32_t slot = sh.slot[sh.grown[k]];
-        head.grow(slot / kBlock, slot % kBlock, sh.ratio[k]);
+    for (int g = 0; g < sh.n_grown; ++g) {
+        constexpr int kWords = 2 * kLanes, kFlight = 8;  // words of a row; of a thread in flight
+        const int32_t slot = sh.slot[sh.grown[g]];
+        const int words = slot % kBlock * kWords;
+        const float ratio = sh.ratio[g];
+        uint8_t *page = dst + static_cast<int64_t>(slot / kBlock * kBlock) * dst_s0;
+        auto at = [&](int i) { return reinterpret_cast<uint32_t *>(page + i / kWords * dst_s0) + i % kWords; };
+        for (int i0 = threadIdx.x; i0 < words; i0 += kFlight * kVecThreads) {
+            uint32_t w[kFlight];
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) w[k] = i0 + k * kVecThreads < words ? *at(i0 + k * kVecThreads) : 0u;
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+                uint32_t out = 0;
+#pragma unroll
+                for (int b = 0; b < 32; b += 8) out |= static_cast<uint32_t>(rescaled((w[k] >> b) & 0xffu, ratio)) << b;
+                if (i0 + k * kVecThreads < words) *at(i0 + k * kVecThreads) = out;
+            }
+        }
     }
     __syncthreads();  // before another tile's rows
 }
@@ -364,26 +411,37 @@ __global__ void __launch_bounds__(kVecThreads, kVecCtas)
 store_block_vec_kernel(const StoreArgs a, int groups, int tile, int64_t items, unsigned kv_blocks) {
     __shared__ __align__(16) float weights[2][8 * kLanes];
     __shared__ Append sh;
+    extern __shared__ uint4 kept[];  // kKept rows of 8 * kLanes floats
     load_weights<kLanes>(a, weights);
-    if (blockIdx.x >= kv_blocks) {
-        store_rows<kBf16, true, kLanes, kMode, false>(a, weights, groups, blockIdx.x - kv_blocks, gridDim.x - kv_blocks);
+    // the two kinds of CTA in turn, as long as there are both: the queries' loads
+    // fill the time that the appending ones wait
+    const unsigned q_blocks = gridDim.x - kv_blocks, both = 2 * min(kv_blocks, q_blocks);
+    const bool of_q = blockIdx.x < both ? blockIdx.x & 1 : q_blocks > kv_blocks;
+    const unsigned block = blockIdx.x < both ? blockIdx.x / 2 : blockIdx.x - both / 2;
+    if (of_q) {
+        store_rows<kBf16, true, kLanes, kMode, false>(a, weights, groups, block, q_blocks);
         return;
     }
     const int n_heads = 2 * a.Hkv;
-    for (int64_t item = blockIdx.x; item < items; item += kv_blocks) {
+    for (int64_t item = block; item < items; item += kv_blocks) {
         const int u = static_cast<int>(item % n_heads);
-        append_tile<kBf16, kLanes, kMode>(a, weights[1], sh, item / n_heads * tile, tile, u < a.Hkv,
-                                          u < a.Hkv ? u : u - a.Hkv);
+        const int64_t tile0 = item / n_heads * tile;
+        if (u < a.Hkv) append_tile<kBf16, kLanes, kMode, true>(a, weights[1], sh, kept, tile0, tile, u);
+        else append_tile<kBf16, kLanes, kMode, false>(a, weights[1], sh, kept, tile0, tile, u - a.Hkv);
     }
 }
 
 template <bool kBf16, int kLanes>
-void launch_block_vec(const StoreArgs &a, unsigned grid, int groups, int tile, int64_t items, unsigned kv_blocks,
-                      cudaStream_t stream) {
+cudaError_t launch_block_vec(const StoreArgs &a, unsigned grid, int groups, int tile, int64_t items, unsigned kv_blocks,
+                             cudaStream_t stream) {
     auto kernel = a.interleaved    ? store_block_vec_kernel<kBf16, kLanes, 2>
                   : a.Rd == a.D    ? store_block_vec_kernel<kBf16, kLanes, 0>
                                    : store_block_vec_kernel<kBf16, kLanes, 1>;
-    kernel<<<grid, kVecThreads, 0, stream>>>(a, groups, tile, items, kv_blocks);
+    constexpr int kSmem = kKept * 8 * kLanes * sizeof(float);
+    const cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), kSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kVecThreads, kSmem, stream>>>(a, groups, tile, items, kv_blocks);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -401,21 +459,26 @@ cudaError_t launch_store_block_vec(const StoreArgs &a, cudaStream_t stream, bool
     const int lanes = a.D / 8, groups = store_row_groups(a, 1);
     const int64_t room = static_cast<int64_t>(device_sm_count()) * kVecCtas;
     // rows of a tile: so many that the appending CTAs are a few to an SM
-    const int64_t per_cta = static_cast<int64_t>(a.T) * 2 * a.Hkv / (8 * device_sm_count());
+    const int64_t per_cta = static_cast<int64_t>(a.T) * 2 * a.Hkv / (2 * device_sm_count());
     int tile = 8;
     while (tile < kMaxTile && tile < per_cta) tile *= 2;
     const int64_t items = (static_cast<int64_t>(a.T) + tile - 1) / tile * 2 * a.Hkv;
     const unsigned kv_blocks = static_cast<unsigned>(items < 16 * room ? items : 16 * room);
     const int tokens = kVecThreads / lanes / groups;
     const int64_t want = (static_cast<int64_t>(a.T) + tokens - 1) / tokens;
-    const unsigned grid = kv_blocks + static_cast<unsigned>(want < room ? want : room);
+    // as many query CTAs as there are places beside the appending ones, or a few
+    // rounds of them: what one takes is to be short next to the call
+    const int64_t beside = room > 2 * static_cast<int64_t>(kv_blocks) ? room - kv_blocks : 4 * room;
+    const unsigned grid = kv_blocks + static_cast<unsigned>(want < beside ? want : beside);
     const bool bf16 = a.in_dt == SPD_BF16;
-    if (lanes == 8) (bf16 ? launch_block_vec<true, 8> : launch_block_vec<false, 8>)(a, grid, groups, tile, items, kv_blocks, stream);
-    else if (lanes == 16) (bf16 ? launch_block_vec<true, 16> : launch_block_vec<false, 16>)(a, grid, groups, tile, items, kv_blocks, stream);
-    else (bf16 ? launch_block_vec<true, 32> : launch_block_vec<false, 32>)(a, grid, groups, tile, items, kv_blocks, stream);
+    const auto launch = lanes == 8    ? (bf16 ? launch_block_vec<true, 8> : launch_block_vec<false, 8>)
+                        : lanes == 16 ? (bf16 ? launch_block_vec<true, 16> : launch_block_vec<false, 16>)
+                                      : (bf16 ? launch_block_vec<true, 32> : launch_block_vec<false, 32>);
+    const cudaError_t e = launch(a, grid, groups, tile, items, kv_blocks, stream);
+    if (e != cudaSuccess) return e;
     count_launches(1);
     *used = true;
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace spd
