@@ -63,6 +63,7 @@
 namespace spd {
 
 cudaError_t launch_attention_tc(const AttnArgs &a, void *ws, size_t ws_bytes, cudaStream_t stream, bool *used);
+int group_rows(const AttnArgs &a, int G);
 
 namespace {
 
@@ -1136,6 +1137,8 @@ bool make_tmap_q(CUtensorMap *m, const uint8_t *base, int64_t T, int64_t hq, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 // Query rows of one request that share a unit (a group).  A group reads each
 // block of the union of its rows' selections once, but the softmax cost of a
 // block grows with the group's width: 16 columns cost about half of 32 or 64
@@ -1151,8 +1154,6 @@ int group_rows(const AttnArgs &a, int G) {
     const double uni = a.NB * (1.0 - std::pow(keep, g));
     return (2.0 * uni > static_cast<double>(g) * a.K) ? 1 : g;
 }
-
-}  // namespace
 
 // The fast path covers: head dim 128, E4M3 caches whose rows are 16-byte
 // aligned, G*gmax <= 64, page tables of at most 256 blocks, at most 4096 rows.

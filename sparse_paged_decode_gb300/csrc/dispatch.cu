@@ -54,6 +54,8 @@ cudaError_t launch_attention_tc(const AttnArgs &a, void *ws, size_t ws_bytes, cu
 cudaError_t launch_attention_bf16_tc(const AttnArgs &a, void *ws, size_t ws_bytes, cudaStream_t stream, bool *used);
 cudaError_t launch_attention_e4m3_rows(const AttnArgs &a, void *ws, size_t ws_bytes, cudaStream_t stream,
                                        bool *used);
+cudaError_t launch_attention_single(const AttnArgs &a, void *ws, size_t ws_bytes, cudaStream_t stream, bool *used);
+int group_rows(const AttnArgs &a, int G);  // rows of a request that share a unit of the keys-on-lanes kernel
 cudaError_t launch_sdpa_tc(const SdpaArgs &a, cudaStream_t stream, bool *used);
 
 namespace {
@@ -100,11 +102,23 @@ cudaError_t dispatch_attention(const AttnArgs &a, void *workspace, size_t worksp
     const int pol = g_policy[3];
     if (pol == 0 && a.kv_dt == SPD_BF16) {
         e = launch_attention_bf16_tc(a, workspace, workspace_bytes, stream, &used);
-    } else if (a.kv_dt == SPD_E4M3 && (pol == 0 || pol == 2 || pol == 3)) {
+    } else if (a.kv_dt == SPD_E4M3 && (pol == 0 || pol == 2 || pol == 3 || pol == 4)) {
         const int64_t G = a.Hkv > 0 ? a.Hq / a.Hkv : 0;
         const bool wide = static_cast<int64_t>(a.T) * G >= 48LL * a.R;
+        // block-scaled caches: rows that have their blocks to themselves (single
+        // tokens, or selections with little in common) take the kernel of
+        // single rows
+        const bool alone = a.T <= a.R || (a.tk != nullptr && group_rows(a, static_cast<int>(G)) == 1);
+        if (pol == 4 || (pol == 0 && !wide && alone)) {
+            e = launch_attention_single(a, workspace, workspace_bytes, stream, &used);
+            if (e == cudaSuccess && used) {
+                count_launches(2);  // the line of blocks + attention
+                return cudaSuccess;
+            }
+            if (e != cudaSuccess) return e;
+        }
         if (pol == 3 || (pol == 0 && wide)) e = launch_attention_e4m3_rows(a, workspace, workspace_bytes, stream, &used);
-        if (e == cudaSuccess && !used && pol != 3) e = launch_attention_tc(a, workspace, workspace_bytes, stream, &used);
+        if (e == cudaSuccess && !used && pol != 3 && pol != 4) e = launch_attention_tc(a, workspace, workspace_bytes, stream, &used);
     }
     if (e != cudaSuccess) return e;
     if (used) {

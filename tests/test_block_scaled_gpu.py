@@ -358,17 +358,17 @@ def test_decode(spd, i, K, dt):
     c = dict(DECODE[i])
     s = attention_inputs(c.pop("lengths"), c.pop("new"), c.pop("Hq"), c.pop("Hkv"), c.pop("D", 128), dt, 200 + i, K=K,
                          general=i % 2 == 1, **c)
-    check_decode(spd, s, (None, 1, 2, 3), "case %d" % i)
+    check_decode(spd, s, (None, 1, 2, 3, 4), "case %d" % i)
 
 
-@pytest.mark.parametrize("pol", [None, 1, 2, 3])
+@pytest.mark.parametrize("pol", [None, 1, 2, 3, 4])
 @pytest.mark.parametrize("K", [0, 5])
 def test_decode_scales_far_apart(spd, K, pol):
     s = attention_inputs([1500, 260, 640], [4, 1, 8], 16, 2, 128, BF16, 31, K=K, wild=24)
     check_decode(spd, s, (pol,), "far apart")
 
 
-@pytest.mark.parametrize("pol", [None, 1, 2, 3])
+@pytest.mark.parametrize("pol", [None, 1, 2, 3, 4])
 def test_decode_scales_outside_the_range(spd, pol):
     """0, negative and NaN count as 2^-64, what is above 2^64 as that."""
     s = attention_inputs([1500, 260, 640], [4, 1, 8], 16, 2, 128, BF16, 32)
@@ -383,7 +383,7 @@ def test_decode_scales_outside_the_range(spd, pol):
 
 def test_decode_bad_metadata(spd):
     """Rows outside the table, pages outside the pool, lengths past the table."""
-    for pol in (None, 1, 2, 3):
+    for pol in (None, 1, 2, 3, 4):
         s = attention_inputs([700, 300, 900], [2, 2, 2], 16, 2, 128, BF16, 33)
         s["req"][0], s["req"][1] = -1, 99
         s["table"][s["rows"][1].long(), 1] = -5
@@ -451,7 +451,7 @@ def test_rows_of_one_small_block_and_heavy_logits(spd, pol):
     s["ks"].fill_(1.0)
     s["vs"][t[0]], s["vs"][t[1]] = 2.0 ** -40, 2.0 ** 30
     check_prefill(spd, s, (pol,), "prefill")
-    check_decode(spd, s, (None, 1, 2, 3), "decode")
+    check_decode(spd, s, (None, 1, 2, 3, 4), "decode")
 
 
 @pytest.mark.parametrize("K", [0, 3])
