@@ -137,6 +137,16 @@ __device__ __forceinline__ int row_places(const AttnArgs &a, int t) {
     return max(n, 1);
 }
 
+// Pieces that the line is cut into, and where piece i begins.  A line has at most
+// kPlanMaxT * kMaxNB places: 32 bits hold it times the teams.
+constexpr int kLeastPlaces = 2;  // of a piece, where the line is short
+__device__ __forceinline__ int line_teams(int most, int total) {
+    return min(most, (total + kLeastPlaces - 1) / kLeastPlaces);
+}
+__device__ __forceinline__ int line_begin(int i, int total, int teams) {
+    return static_cast<int>(static_cast<uint32_t>(i) * static_cast<uint32_t>(total) / static_cast<uint32_t>(teams));
+}
+
 constexpr int kLineThreads = 512;
 
 // base[t], the first place of row t, base[T] the line's length; the row in which
@@ -183,9 +193,9 @@ __global__ void __launch_bounds__(kLineThreads) line_kernel(const __grid_constan
         base[a.T] = total;
     }
     __syncthreads();
-    const int teams = min(t.teams, total);
+    const int teams = line_teams(t.teams, total);
     for (int i = tid; i < teams; i += kLineThreads) {
-        const int x = static_cast<int>(static_cast<int64_t>(i) * total / teams);
+        const int x = line_begin(i, total, teams);
         int lo = 0, hi = a.T;  // s_base[lo] <= x < s_base[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -315,31 +325,71 @@ __device__ void join_row(const SingleArgs &t, const Unit &u, int pair, int h, in
     const AttnArgs &a = t.a;
     const int w = st >> 5, d4 = (st & 31) * 4;
     const float *parts = reinterpret_cast<const float *>(t.ws + t.lay.partials);
-    for (int r = w; r < t.G; r += 4) {
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < u.n_split; ++i) {
-            const int64_t cta = static_cast<int64_t>(u.team0 + i) * t.pairs + pair;
-            const float *row = parts + (((cta * 2 + (i == 0 ? u.slot0 : 0)) * 2 + h) * kN + r) * kStride;
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(row + kD));
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(row + d4));
-            if (ml.x == -INFINITY) continue;
-            const float mc = fmaxf(m, ml.x);
-            const float s0 = m == -INFINITY ? 0.f : tc::ex2(m - mc), s1 = tc::ex2(ml.x - mc);
-            l = fmaf(s1, ml.y, l * s0);
-            o.x = fmaf(s1, x.x, o.x * s0);
-            o.y = fmaf(s1, x.y, o.y * s0);
-            o.z = fmaf(s1, x.z, o.z * s0);
-            o.w = fmaf(s1, x.w, o.w * s0);
-            m = mc;
+    // kRows rows at a time, kParts pieces of each in flight
+    constexpr int kRows = 2, kParts = 4;
+    for (int r0 = w; r0 < t.G; r0 += 4 * kRows) {
+        float m[kRows], l[kRows];
+        float4 o[kRows];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            m[j] = -INFINITY;
+            l[j] = 0.f;
+            o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const float inv = l != 0.f ? 1.f / l : 0.f;
-        __nv_bfloat16 *out = a.out + u.row * a.o_s0 + static_cast<int64_t>((2 * pair + h) * t.G + r) * a.o_s1;
-        out[(d4 + 0) * a.o_s2] = __float2bfloat16_rn(o.x * inv);
-        out[(d4 + 1) * a.o_s2] = __float2bfloat16_rn(o.y * inv);
-        out[(d4 + 2) * a.o_s2] = __float2bfloat16_rn(o.z * inv);
-        out[(d4 + 3) * a.o_s2] = __float2bfloat16_rn(o.w * inv);
+        for (int i0 = 0; i0 < u.n_split; i0 += kParts) {
+            float2 ml[kRows][kParts];
+            float4 x[kRows][kParts];
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                const int i = i0 + k;
+                const int64_t cta = static_cast<int64_t>(u.team0 + i) * t.pairs + pair;
+                const float *part = parts + ((cta * 2 + (i == 0 ? u.slot0 : 0)) * 2 + h) * kN * kStride;
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) {
+                    const int r = r0 + 4 * j;
+                    ml[j][k] = make_float2(-INFINITY, 0.f);
+                    x[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < u.n_split && r < t.G) {
+                        ml[j][k] = __ldcg(reinterpret_cast<const float2 *>(part + r * kStride + kD));
+                        x[j][k] = __ldcg(reinterpret_cast<const float4 *>(part + r * kStride + d4));
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+                float top = m[j];
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) top = fmaxf(top, ml[j][k].x);
+                if (top == -INFINITY) continue;  // nothing read so far
+                const float s0 = tc::ex2(m[j] - top);
+                l[j] *= s0;
+                o[j].x *= s0;
+                o[j].y *= s0;
+                o[j].z *= s0;
+                o[j].w *= s0;
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) {
+                    const float s1 = tc::ex2(ml[j][k].x - top);  // 0 for a piece that read nothing
+                    l[j] = fmaf(s1, ml[j][k].y, l[j]);
+                    o[j].x = fmaf(s1, x[j][k].x, o[j].x);
+                    o[j].y = fmaf(s1, x[j][k].y, o[j].y);
+                    o[j].z = fmaf(s1, x[j][k].z, o[j].z);
+                    o[j].w = fmaf(s1, x[j][k].w, o[j].w);
+                }
+                m[j] = top;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            const int r = r0 + 4 * j;
+            if (r >= t.G) continue;
+            const float inv = l[j] != 0.f ? 1.f / l[j] : 0.f;
+            __nv_bfloat16 *out = a.out + u.row * a.o_s0 + static_cast<int64_t>((2 * pair + h) * t.G + r) * a.o_s1;
+            out[(d4 + 0) * a.o_s2] = __float2bfloat16_rn(o[j].x * inv);
+            out[(d4 + 1) * a.o_s2] = __float2bfloat16_rn(o[j].y * inv);
+            out[(d4 + 2) * a.o_s2] = __float2bfloat16_rn(o[j].z * inv);
+            out[(d4 + 3) * a.o_s2] = __float2bfloat16_rn(o[j].w * inv);
+        }
     }
 }
 
@@ -719,9 +769,9 @@ attention_single_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
     } else {
         // ------------------------------------------------------- block lists
         const int32_t *base = reinterpret_cast<const int32_t *>(t.ws + t.lay.gstart);
-        const int total = base[a.T], teams = min(t.teams, total);
-        auto begin_of = [&](int i) { return static_cast<int>(static_cast<int64_t>(i) * total / teams); };
-        auto team_of = [&](int x) { return static_cast<int>((static_cast<int64_t>(x + 1) * teams - 1) / total); };
+        const int total = base[a.T], teams = line_teams(t.teams, total);
+        auto begin_of = [&](int i) { return line_begin(i, total, teams); };
+        auto team_of = [&](int x) { return static_cast<int>((static_cast<uint32_t>(x + 1) * teams - 1) / total); };
         int x = 0, x1 = 0, row = 0;
         if (team < teams) {
             x = begin_of(team);
@@ -892,7 +942,8 @@ cudaError_t launch_attention_single(const AttnArgs &a, void *ws, size_t ws_bytes
     t.sm_log2 = a.sm_scale * 1.4426950408889634f;
     const int n = G <= 8 ? 8 : 16;
     // two partial rows' slots of a CTA, two heads each, and a word a team
-    if (static_cast<int64_t>(t.teams) * t.pairs * 4 * n > t.lay.rows_cap || t.teams > t.lay.unit_cap) return cudaSuccess;
+    if (static_cast<int64_t>(t.teams) * t.pairs * 4 * n > t.lay.rows_cap || t.teams > t.lay.unit_cap || t.teams > 1000)
+        return cudaSuccess;
     CUtensorMap mk, mv;
     if (!make_map(&mk, a.k, a.P * kKeys, a.Hkv, a.k_s0, a.k_s1) || !make_map(&mv, a.v, a.P * kKeys, a.Hkv, a.v_s0, a.v_s1))
         return cudaSuccess;
