@@ -178,14 +178,14 @@ __device__ __forceinline__ void set_abort(Shared &sh, int32_t *status) {
 }
 
 __device__ __forceinline__ bool wait_or_abort(Shared &sh, uint64_t *bar, uint32_t parity, int32_t *status) {
-    if (tc::mbar_wait(bar, parity)) return true;
+    if (tc::mbar_wait_tries(bar, parity)) return true;
     set_abort(sh, status);
     return false;
 }
 
 // Warp-uniform wait: the warp goes on only if every lane saw the phase.
 __device__ __forceinline__ bool warp_wait(Shared &sh, uint64_t *bar, uint32_t parity, int32_t *status) {
-    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity));
+    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_tries(bar, parity));
     if (!ok) set_abort(sh, status);
     return ok;
 }
@@ -402,11 +402,11 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
                 }
                 // every issued copy lands before the CTA may exit (the last
                 // phase of each barrier is the only one still pending)
-                if (nq > 0) tc::mbar_wait(&sh.q_full, (nq - 1) & 1);
+                if (nq > 0) tc::mbar_wait_tries(&sh.q_full, (nq - 1) & 1);
                 for (uint32_t b = (nk > kStages ? nk - kStages : 0); b < nk; ++b)
-                    tc::mbar_wait(&sh.k_full[b % kStages], (b / kStages) & 1);
+                    tc::mbar_wait_tries(&sh.k_full[b % kStages], (b / kStages) & 1);
                 for (uint32_t b = (nv > kStages ? nv - kStages : 0); b < nv; ++b)
-                    tc::mbar_wait(&sh.v_full[b % kStages], (b / kStages) & 1);
+                    tc::mbar_wait_tries(&sh.v_full[b % kStages], (b / kStages) & 1);
             }
         } else if (warp == kWarpMma) {
             // --------------------------------------------------- MMA issuer
@@ -481,7 +481,7 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
                     ++uc;
                 }
                 tc::mma_commit(&sh.drain);
-                tc::mbar_wait(&sh.drain, 0);
+                tc::mbar_wait_tries(&sh.drain, 0);
             }
         } else {
             // ------------------------------------------------ V widening (6-7)

@@ -210,14 +210,14 @@ __global__ void __launch_bounds__(kLineThreads) line_kernel(const __grid_constan
 __device__ __forceinline__ bool aborted(Shared &sh) { return *reinterpret_cast<volatile int *>(&sh.abort) != 0; }
 
 __device__ __forceinline__ bool wait_or_abort(Shared &sh, uint64_t *bar, uint32_t parity) {
-    if (tc::mbar_wait(bar, parity)) return true;
+    if (tc::mbar_wait_tries(bar, parity)) return true;
     *reinterpret_cast<volatile int *>(&sh.abort) = 1;
     return false;
 }
 
 // Warp-uniform: the warp goes on only if every lane saw the phase.
 __device__ __forceinline__ bool warp_wait(Shared &sh, uint64_t *bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity));
+    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_tries(bar, parity));
     if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
     return ok;
 }
@@ -409,7 +409,7 @@ __device__ __forceinline__ void softmax_group(const SingleArgs &t, Shared &sh, u
     bool begun = false;  // the row's piece has had a page
     for (uint32_t n = 0;; ++n) {
         Unit &u = sh.unit[n & 1];
-        const bool got = tc::mbar_wait(&sh.u_full[n & 1], (n >> 1) & 1);
+        const bool got = tc::mbar_wait_tries(&sh.u_full[n & 1], (n >> 1) & 1);
         if (!got) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
         if (group_any(h, !got || aborted(sh))) return;  // together, or not at all
         const int count = u.count;
@@ -681,7 +681,7 @@ attention_single_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
                 if (ok) tc::mbar_arrive(&sh.u_empty[n & 1]);
             }
             // every issued copy lands before the CTA may exit
-            for (uint32_t k = b > kStages ? b - kStages : 0; k < b; ++k) tc::mbar_wait(&sh.kv_full[k % kStages], (k / kStages) & 1);
+            for (uint32_t k = b > kStages ? b - kStages : 0; k < b; ++k) tc::mbar_wait_tries(&sh.kv_full[k % kStages], (k / kStages) & 1);
         }
     } else if (warp == kWarpQk) {
         if (lane == 0) {
@@ -724,7 +724,7 @@ attention_single_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
             }
             // every issued product completes before tensor memory is released
             tc::mma_commit(&sh.drain[0]);
-            tc::mbar_wait(&sh.drain[0], 0);
+            tc::mbar_wait_tries(&sh.drain[0], 0);
         }
     } else if (warp == kWarpPv) {
         if (lane == 0) {
@@ -764,7 +764,7 @@ attention_single_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
                 if (ok) tc::mbar_arrive(&sh.u_empty[n & 1]);
             }
             tc::mma_commit(&sh.drain[1]);
-            tc::mbar_wait(&sh.drain[1], 0);
+            tc::mbar_wait_tries(&sh.drain[1], 0);
         }
     } else {
         // ------------------------------------------------------- block lists

@@ -318,32 +318,15 @@ __device__ __forceinline__ bool elect_one() {
 
 __device__ __forceinline__ bool aborted(Shared &sh) { return *reinterpret_cast<volatile int *>(&sh.abort) != 0; }
 
-// Waits for the phase with the given parity; false once kWaitTries tries have
-// failed, about 2 s (a try gives up after 2 us; a unit of the longest request
-// takes 2 ms).  Counting the tries instead of reading a clock keeps the waits
-// short in instructions, whose fetching bounds the kernel beside the tensor
-// pipe: with a clock read in each of some thirty places dense bf16 took 489
-// instead of 466 us, ragged E4M3 108 instead of 98.
-constexpr uint32_t kWaitTries = 1u << 20;
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-#pragma unroll 1
-    for (uint32_t i = 0; i < kWaitTries; ++i) {
-        __nanosleep(30);
-        if (tc::mbar_try_wait(bar, parity)) return true;
-    }
-    return false;
-}
-
 __device__ __forceinline__ bool wait_or_abort(Shared &sh, uint64_t *bar, uint32_t parity) {
-    if (bar_wait(bar, parity)) return true;
+    if (tc::mbar_wait_tries(bar, parity)) return true;
     *reinterpret_cast<volatile int *>(&sh.abort) = 1;
     return false;
 }
 
 // Warp-uniform wait, for the warp-collective accesses that follow it.
 __device__ __forceinline__ bool warp_wait(Shared &sh, uint64_t *bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, bar_wait(bar, parity));
+    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_tries(bar, parity));
     if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
     return ok;
 }
@@ -1081,12 +1064,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 // every issued copy lands before the CTA may exit; only after
                 // an abort can one still be in flight
                 if (!ok) {
-                    if (nq > 0) bar_wait(&sh.q_full, (nq - 1) & 1);
+                    if (nq > 0) tc::mbar_wait_tries(&sh.q_full, (nq - 1) & 1);
                     auto landed = [&](const auto &ring, uint64_t *full, int slots) {
                         for (int i = 0; i < slots; ++i) {
                             // the last round of slot i that was begun
                             const uint32_t rounds = ring.round + (static_cast<uint32_t>(i) < ring.slot ? 1 : 0);
-                            if (rounds > 0) bar_wait(&full[i], (rounds - 1) & 1);
+                            if (rounds > 0) tc::mbar_wait_tries(&full[i], (rounds - 1) & 1);
                         }
                     };
                     if (M != kModeWide) landed(rk, sh.k_full, S::kKs);
@@ -1282,7 +1265,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             // every issued product completes before tensor memory is released
             if (elect_one()) tc::mma_commit(&sh.drain[i]);
             __syncwarp();
-            bar_wait(&sh.drain[i], 0);
+            tc::mbar_wait_tries(&sh.drain[i], 0);
         } else if (warp == kWarpSched) {
             // ---------------------------------------------- units, page lists
             const ChunkPair *pairs = reinterpret_cast<const ChunkPair *>(t.ws + t.lay.pairs);
