@@ -555,13 +555,14 @@ SPD_API void paged_norm_rope_store_block_scaled(const spd_tensor *q, const spd_t
  *
  * k_cache, v_cache [P*128, Hkv, D] e4m3; k_scales, v_scales [P, Hkv] f32, any
  * strides; workspaces, the other arguments and the domain as for the calls without
- * the suffix.  The rounding is theirs too, but that the weights which the tensor
- * cores round to f16 are those times vs: they keep their 11 bits down to 2^-21
- * (prefill) or 2^-14 (decode) of the row's largest product of the two, and the
- * bound becomes
- *   |out - exact| <= 2^-8 |exact| + (2^-8 + 2^-10) A + 2^-22 M
- * with A = sum_tau softmax(z)_tau |vs * v| and M = 448 times the row's largest
- * softmax(z)_tau * vs, per key that is read.
+ * the suffix.  The rounding is theirs too, but for the weights, which are those
+ * times vs: f16 ones keep 11 bits down to 2^-21 (prefill) or 2^-14 (decode) of the
+ * row's largest product of the two, and the decode kernel of single rows takes
+ * them as three E4M3 terms, off by at most 2^-12 of themselves or 2^-22 of that
+ * largest product.  With A = sum_tau softmax(z)_tau |vs * v|, and n keys read, the
+ * bound of paged_prefill_attention becomes
+ *   |out - exact| <= 2^-8 |exact| + (2^-8 + 2^-10) A + n 2^-22 M,
+ *   M = 448 times the row's largest softmax(z)_tau * vs
  */
 SPD_API void paged_decode_attention_block_scaled(const spd_tensor *q, const spd_tensor *k_cache,
                                                  const spd_tensor *v_cache, const spd_tensor *k_scales,
@@ -642,7 +643,10 @@ SPD_API int spd_set_attention_kernel(int policy);
  * one (the default takes the query-rows kernel for bf16 queries of head dim
  * 128, G <= 16 and on average at least 48 query rows per request and kv
  * head, the keys-on-lanes one otherwise; a shape the picked kernel does not
- * cover runs on the general-layout kernel).  All give identical selections, and
+ * cover runs on the general-layout kernel).  Over block-scaled caches policy 4
+ * picks the kernel of single rows (the default takes it ahead of the
+ * keys-on-lanes one where there are no more query rows than page-table rows, or
+ * selections with little in common, and an even number of kv heads shares them).  All give identical selections, and
  * attention results that agree within the stated tolerance.  Returns the
  * previous setting, or -1 for an unknown stage.
  */

@@ -163,6 +163,14 @@ __global__ void __launch_bounds__(kWarps * 32) store_block_generic_kernel(const 
 // thread a run fixes its scale; the rows are rounded and stored from shared
 // memory.  Held codes that grow are multiplied by the whole CTA behind that (16 KB
 // a run at most: one round trip).
+//
+// Measured, 64 + 8 + 8 rows of 128 dims a token, called one by one (graph of calls
+// in brackets): 8192 tokens 80.4 (78.1) us, 0.6 of the measured copy rate; 476
+// rows of 64 requests 11.2 (9.1) us; 16 requests of a token 6.2 (3.7) us.  The
+// queries alone take 54 us of the 8192 tokens, the appending alone 32: warps that
+// wait bound it (24 an SM; issue on 49 % of the cycles, DRAM at 45 %).  One warp a
+// short run and rows read twice took 84 us, rows kept in registers and 128
+// registers a thread 96, four rows in flight instead of two 83.
 constexpr int kMaxTile = 128;
 constexpr int kKept = kBlock;  // rows kept in shared memory: a whole page's run
 
@@ -458,7 +466,9 @@ cudaError_t launch_store_block_vec(const StoreArgs &a, cudaStream_t stream, bool
     if (!store_vec_covers(a)) return cudaSuccess;
     const int lanes = a.D / 8, groups = store_row_groups(a, 1);
     const int64_t room = static_cast<int64_t>(device_sm_count()) * kVecCtas;
-    // rows of a tile: so many that the appending CTAs are a few to an SM
+    // rows of a tile: so many that the appending CTAs are two to an SM, in powers of
+    // two (476 rows: 9.1 us with two, 10.4 with four, 12.6 with eight; 1999 rows of
+    // chunks 23.5, 24.2, 25.8)
     const int64_t per_cta = static_cast<int64_t>(a.T) * 2 * a.Hkv / (2 * device_sm_count());
     int tile = 8;
     while (tile < kMaxTile && tile < per_cta) tile *= 2;
@@ -467,7 +477,8 @@ cudaError_t launch_store_block_vec(const StoreArgs &a, cudaStream_t stream, bool
     const int tokens = kVecThreads / lanes / groups;
     const int64_t want = (static_cast<int64_t>(a.T) + tokens - 1) / tokens;
     // as many query CTAs as there are places beside the appending ones, or a few
-    // rounds of them: what one takes is to be short next to the call
+    // rounds of them: what one takes is to be short next to the call (8192 tokens:
+    // 84.8 us with one round, 79.7 with four)
     const int64_t beside = room > 2 * static_cast<int64_t>(kv_blocks) ? room - kv_blocks : 4 * room;
     const unsigned grid = kv_blocks + static_cast<unsigned>(want < beside ? want : beside);
     const bool bf16 = a.in_dt == SPD_BF16;

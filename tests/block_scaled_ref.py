@@ -11,7 +11,8 @@ serve_ref.py):
   * attention: serve_ref's bound over the dequantised caches.  The weights
     that are rounded to f16 are p vs / w, w the row's largest such product (at a
     raise of its offset; the products may exceed it, never be below it): below 2^-14 a rounding
-    is off by at most 2^-25 w, so a key adds at most 2^-25 w 448 to the bound.  A scale
+    is off by at most 2^-25 w, so a key adds at most 2^-25 w 448 to the bound (the kernel of
+    single rows is granted 2^-22 by the header; here it has to do with this).  A scale
     enters by its logarithm, whose error of 2^-22 (and the fp32 sum's with an
     offset of up to a few hundred, 2^-16) moves a weight by less than 2^-15 of
     itself: inside the 2^-10 A that serve_ref grants to logits, next to whose 2^-11 it stays.
