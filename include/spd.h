@@ -551,7 +551,9 @@ SPD_API void paged_norm_rope_store_block_scaled(const spd_tensor *q, const spd_t
  * where ks and vs are the scales of tau's page and of kv head h, each taken as
  * the nearest value of [2^-64, 2^64] (the smallest for a NaN): any positive
  * scales will do, not only powers of two.  Scales of pages that a row does not
- * read never reach its output.
+ * read never reach its output.  A NaN value that a row reads shows in its dims; a
+ * NaN key, or a query that is not finite, makes the head's output NaN (from the
+ * decode kernels of wider groups and the general one: NaN or zeros).
  *
  * k_cache, v_cache [P*128, Hkv, D] e4m3; k_scales, v_scales [P, Hkv] f32, any
  * strides; workspaces, the other arguments and the domain as for the calls without

@@ -488,8 +488,9 @@ __device__ __forceinline__ void softmax_group(const SingleArgs &t, Shared &sh, u
 #pragma unroll
                 for (int r = 0; r < kN; ++r) {
                     const float top = fmaxf(fmaxf(sh.red[h][0][r], sh.red[h][1][r]), fmaxf(sh.red[h][2][r], sh.red[h][3][r]));
-                    // rows whose logits are all NaN have no maximum: any offset will do
-                    const float by = (top > kCap || !begun) && top != -INFINITY ? top - kTarget : 0.f;
+                    // rows whose logits are all NaN have no maximum: any offset that is a
+                    // number will do, and their sums stay NaN through the join
+                    const float by = (top > kCap || !begun) && top > -INFINITY ? top - kTarget : 0.f;
                     alpha[r] = tc::ex2(-by);
                     moved |= by != 0.f;
                     m[r] += by;

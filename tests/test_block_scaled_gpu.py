@@ -687,3 +687,95 @@ def test_both_ways_of_marshalling(spd, monkeypatch):
             got += [run_decode(spd, a), run_prefill(spd, a)]
         outs.append(digest(*got))
     assert outs[0] == outs[1]
+
+
+# ------------------------------------------------- decode of single rows
+
+
+def shared_selection(s, K, seed, kind="random"):
+    """One selection for all kv heads: repeated ids, -1 and ids past the table among them."""
+    g = torch.Generator().manual_seed(seed)
+    T, NB = s["q"].shape[0], s["NB"]
+    tk = torch.randint(-1, NB + 2, (1, T, K), generator=g).to(I32)
+    if kind == "whole":  # every block, in an order of its own, some of them twice
+        tk = torch.stack([torch.cat((torch.randperm(NB, generator=g), torch.randint(0, NB, (K,), generator=g)))[:K] for _ in range(T)])[None].to(I32)
+    tk[0, ::5] = -1  # rows that select nothing
+    s["topk"] = tk.to(DEV).expand(s["Hkv"], -1, -1)
+    return s
+
+
+@pytest.mark.parametrize("dt", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("heads", [(64, 8), (16, 2), (6, 2), (32, 2), (4, 4), (2, 2)])
+@pytest.mark.parametrize("K,kind", [(1, "random"), (5, "random"), (12, "whole"), (40, "whole")])
+def test_single_rows_with_a_shared_selection(spd, K, kind, heads, dt):
+    s = attention_inputs([1300, 129, 700, 5, 1024, 256], [1, 1, 4, 1, 2, 1], *heads, 128, dt, 51, pad=2, general=True)
+    check_decode(spd, shared_selection(s, K, 52, kind), (None, 1, 4), "K=%d %s" % (K, kind))
+
+
+@pytest.mark.parametrize("K", [0, 9])
+@pytest.mark.parametrize("n", [1, 40, 200])
+def test_single_rows_of_many_requests(spd, n, K):
+    """Pieces that hold many rows, that end inside a row, and rows without keys among them."""
+    r = random.Random(n)
+    lengths = [r.choice((0, 1, 90, 128, 300, 1500)) if n > 1 else 3000 for _ in range(n)]
+    s = attention_inputs(lengths, [1 if L else 0 for L in lengths], 16, 2, 128, BF16, 53, pad=3, NB=24)
+    if K:
+        shared_selection(s, K, 54)
+    check_decode(spd, s, (None, 4), "%d requests" % n)
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (64, 64)])
+def test_single_rows_over_long_page_tables(spd, heads):
+    """Up to 1024 blocks, and pieces of more blocks than the kernel lists at a time (against 64 bits on the GPU)."""
+    Hq, Hkv = heads
+    D, NB, T = 128, 1024 if Hkv == 2 else 300, 3 if Hkv == 2 else 8
+    g = torch.Generator(device=DEV).manual_seed(55)
+    pool = NB + 3
+    kc, vc = (torch.randn((pool * BS, Hkv, D), generator=g, device=DEV).mul_(m).to(E4M3) for m in (2.0, 60.0))
+    ks, vs = (torch.exp2(torch.randint(-2, 3, (pool, Hkv), generator=g, device=DEV).float()) for _ in range(2))
+    table = torch.randperm(pool, generator=g, device=DEV)[:NB].to(I32)[None].contiguous()
+    lens = i32([NB * BS - 77 * i for i in range(T)])
+    q = torch.randn((T, Hq, D), generator=g, device=DEV).to(BF16)
+    out = nan_like((T, Hq, D), BF16, DEV)
+    ws = torch.randint(0, 256, (spd.decode_workspace_bytes(T, Hq, Hkv, D, NB),), dtype=torch.uint8, device=DEV)
+    old = spd.set_kernel_policy(3, 4)
+    try:
+        spd.paged_decode_attention_block_scaled(q, kc, vc, ks, vs, table, lens, i32([0] * T), out, D ** -0.5, BS, ws)
+    finally:
+        spd.set_kernel_policy(3, old)
+    torch.cuda.synchronize()
+    assert spd.workspace_status(ws) & 1 == 0
+    G = Hq // Hkv
+    for h in sorted({0, 1, Hkv // 2, Hkv - 1}):
+        pages = table[0].long()
+        k = (kc.view(pool, BS, Hkv, D)[pages, :, h].double() * ks[pages, h].double()[:, None, None]).view(-1, D)
+        v = (vc.view(pool, BS, Hkv, D)[pages, :, h].double() * vs[pages, h].double()[:, None, None]).view(-1, D)
+        for t in range(T):
+            n = int(lens[t])
+            z = q[t, h * G:(h + 1) * G].double() @ k[:n].T * D ** -0.5
+            p = torch.softmax(z, -1)
+            ref, A = p @ v[:n], p @ v[:n].abs()
+            most = (p * vs[pages, h].double().repeat_interleave(BS)[:n]).amax(-1, keepdim=True)
+            tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -10) * A + n * 2.0 ** -22 * 448 * most
+            assert bool(((out[t, h * G:(h + 1) * G].double() - ref).abs() <= tol).all()), (h, t)
+
+
+@pytest.mark.parametrize("pol", [0, 4])
+def test_single_rows_not_finite(spd, pol):
+    """A NaN that a row reads shows in its dims (V) or its heads (K, q), and nowhere else."""
+    s = attention_inputs([700, 300, 400], [1, 1, 1], 16, 2, 128, BF16, 56)
+    t = s["table"][s["rows"].long()].long()
+    s["vc"].view(torch.uint8)[t[0, 2] * BS + 5, 1, 17] = 0x7F
+    s["kc"].view(torch.uint8)[t[1, 0] * BS + 9, 0, 3] = 0xFF
+    s["q"][2, 5, 64] = float("inf")
+    old = spd.set_kernel_policy(3, pol)
+    try:
+        out = run_decode(spd, s, None)
+    finally:
+        spd.set_kernel_policy(3, old)
+    bad = torch.isnan(out.float())
+    want = torch.zeros_like(bad)
+    want[0, 8:, 17] = True
+    want[1, :8] = True
+    want[2, 5] = True
+    assert torch.equal(bad, want)
