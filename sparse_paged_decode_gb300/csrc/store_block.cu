@@ -150,8 +150,9 @@ __global__ void __launch_bounds__(kWarps * 32) store_block_generic_kernel(const 
     }
 }
 
-// The layouts of the vector store (store.cuh), one launch: some CTAs append K
-// and V, the others write the queries as store_vec_kernel does.
+// The layouts of the vector store (store.cuh), one launch: the first CTAs append K
+// and V, the others write the queries as store_vec_kernel does (in turn with the
+// appending ones they took the same time).
 //
 // An appending CTA takes one K or V head of `tile` batch rows: the runs that
 // begin in them, with the rows behind the tile that end the last one.  Runs are
@@ -421,17 +422,12 @@ store_block_vec_kernel(const StoreArgs a, int groups, int tile, int64_t items, u
     __shared__ Append sh;
     extern __shared__ uint4 kept[];  // kKept rows of 8 * kLanes floats
     load_weights<kLanes>(a, weights);
-    // the two kinds of CTA in turn, as long as there are both: the queries' loads
-    // fill the time that the appending ones wait
-    const unsigned q_blocks = gridDim.x - kv_blocks, both = 2 * min(kv_blocks, q_blocks);
-    const bool of_q = blockIdx.x < both ? blockIdx.x & 1 : q_blocks > kv_blocks;
-    const unsigned block = blockIdx.x < both ? blockIdx.x / 2 : blockIdx.x - both / 2;
-    if (of_q) {
-        store_rows<kBf16, true, kLanes, kMode, false>(a, weights, groups, block, q_blocks);
+    if (blockIdx.x >= kv_blocks) {
+        store_rows<kBf16, true, kLanes, kMode, false>(a, weights, groups, blockIdx.x - kv_blocks, gridDim.x - kv_blocks);
         return;
     }
     const int n_heads = 2 * a.Hkv;
-    for (int64_t item = block; item < items; item += kv_blocks) {
+    for (int64_t item = blockIdx.x; item < items; item += kv_blocks) {
         const int u = static_cast<int>(item % n_heads);
         const int64_t tile0 = item / n_heads * tile;
         if (u < a.Hkv) append_tile<kBf16, kLanes, kMode, true>(a, weights[1], sh, kept, tile0, tile, u);
@@ -478,7 +474,7 @@ cudaError_t launch_store_block_vec(const StoreArgs &a, cudaStream_t stream, bool
     const int64_t want = (static_cast<int64_t>(a.T) + tokens - 1) / tokens;
     // as many query CTAs as there are places beside the appending ones, or a few
     // rounds of them: what one takes is to be short next to the call (8192 tokens:
-    // 84.8 us with one round, 79.7 with four)
+    // 84.8 us with one round, 80.3 with two, 78 with four, 79 with eight)
     const int64_t beside = room > 2 * static_cast<int64_t>(kv_blocks) ? room - kv_blocks : 4 * room;
     const unsigned grid = kv_blocks + static_cast<unsigned>(want < beside ? want : beside);
     const bool bf16 = a.in_dt == SPD_BF16;
