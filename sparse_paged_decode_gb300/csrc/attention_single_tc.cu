@@ -103,7 +103,11 @@ struct Shared {
     uint64_t drain[2];
     float2 scale[2][kScaleRing];
     float cfac[2][16];
+    // of each head's warps, by query head: a block's maxima, and the sums of a piece.
+    // Apart: a warp may write its sums while another still reads the maxima of the
+    // piece's last block, and no barrier lies between.
     float red[2][4][16];
+    float sum[2][4][16];
     int vote[2][2][4];
     int last[2];
     uint32_t tmem_base;
@@ -561,7 +565,7 @@ __device__ __forceinline__ void softmax_group(const SingleArgs &t, Shared &sh, u
                 float s = l[r];
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                if (lane == 0) sh.red[h][warp][r] = s;
+                if (lane == 0) sh.sum[h][warp][r] = s;
             }
             if (begun) warp_wait(sh, &sh.pv_done[h], (b - 1) & 1);
             tc::tc_fence_after();
@@ -569,7 +573,7 @@ __device__ __forceinline__ void softmax_group(const SingleArgs &t, Shared &sh, u
             float o[kN];
 #pragma unroll
             for (int r = 0; r < kN; ++r) {
-                l[r] = (sh.red[h][0][r] + sh.red[h][1][r]) + (sh.red[h][2][r] + sh.red[h][3][r]);
+                l[r] = (sh.sum[h][0][r] + sh.sum[h][1][r]) + (sh.sum[h][2][r] + sh.sum[h][3][r]);
                 o[r] = 0.f;
             }
             if (begun) {
