@@ -213,6 +213,7 @@ __device__ __forceinline__ bool soft_any(bool v) {
 // dims; the (offset, sum) and output values of two partials of both rows are
 // loaded together, then folded with an online maximum.  Partials are read
 // with ld.global.cg: other CTAs wrote them during this launch.
+template <bool kBs>
 __device__ void merge_pair(const RowsArgs &a, const PlanUnit &un, const float *partials, int st_id) {
     constexpr int kParts = 2;
     const int rows = un.nt * a.G, ns = un.n_split;
@@ -246,16 +247,17 @@ __device__ void merge_pair(const RowsArgs &a, const PlanUnit &un, const float *p
 #pragma unroll
                 for (int q = 0; q < kParts; ++q) mc = fmaxf(mc, ml[u][q].x);
                 if (mc == -INFINITY) continue;
-                const float sc = (m[u] == -INFINITY) ? 0.f : tc::ex2(m[u] - mc);
-                den[u] *= sc;
+                const float sc = kBs ? rescale(den[u], m[u] - mc) : ((m[u] == -INFINITY) ? 0.f : tc::ex2(m[u] - mc));
+                if (!kBs) den[u] *= sc;
                 acc[u].x *= sc;
                 acc[u].y *= sc;
                 acc[u].z *= sc;
                 acc[u].w *= sc;
 #pragma unroll
                 for (int q = 0; q < kParts; ++q) {
-                    const float wt = (ml[u][q].x == -INFINITY) ? 0.f : tc::ex2(ml[u][q].x - mc);
-                    den[u] = fmaf(wt, ml[u][q].y, den[u]);
+                    const float wt = kBs ? rescale(ml[u][q].y, ml[u][q].x - mc)
+                                         : ((ml[u][q].x == -INFINITY) ? 0.f : tc::ex2(ml[u][q].x - mc));
+                    den[u] = kBs ? den[u] + ml[u][q].y : fmaf(wt, ml[u][q].y, den[u]);
                     acc[u].x = fmaf(wt, o[u][q].x, acc[u].x);
                     acc[u].y = fmaf(wt, o[u][q].y, acc[u].y);
                     acc[u].z = fmaf(wt, o[u][q].z, acc[u].z);
@@ -577,7 +579,7 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
             soft_sync();
             if (sh.last) {
                 __threadfence();  // the other units' partials before the merge reads them
-                merge_pair(a, pend, partials, st_id);
+                merge_pair<kBs>(a, pend, partials, st_id);
             }
             soft_sync();  // sh.last is rewritten by the next resolution
             pend.pair = -1;
@@ -672,12 +674,17 @@ attention_e4m3_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __g
                     // raise the offset if the block's maximum runs more than
                     // 2^kRaise above it (or the row had none yet)
                     if (bm != -INFINITY && (m_run == -INFINITY || bm > m_run + kRaise)) {
-                        alpha = (m_run == -INFINITY) ? 0.f : tc::ex2(m_run - bm);
+                        alpha = kBs ? rescale(l, m_run - bm) : ((m_run == -INFINITY) ? 0.f : tc::ex2(m_run - bm));
+                        if (!kBs) l *= alpha;
                         m_run = bm;
-                        l *= alpha;
                     }
                     const float m_eff = ((m_run == -INFINITY) ? 0.f : m_run) - (kBs ? bs.lg_v : 0.f);
                     float sum = kBs ? 0.f : l;
+                    if (kBs && low_scale(bs)) {
+                        const float m_own = (m_run == -INFINITY) ? 0.f : m_run;
+#pragma unroll
+                        for (int k = 0; k < kHalf; ++k) l += (k < lim) ? tc::ex2(fmaf(s[k], cb, -m_own)) : 0.f;
+                    }
                     // p = 2^(s c - m) in [0, 2^kRaise], f16; masked keys take
                     // p = 0 whatever the sign of c
                     if (lim >= kHalf) {

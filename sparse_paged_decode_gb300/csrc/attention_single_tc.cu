@@ -372,16 +372,15 @@ __device__ void join_row(const SingleArgs &t, const Unit &u, int pair, int h, in
 #pragma unroll
                 for (int k = 0; k < kParts; ++k) top = fmaxf(top, ml[j][k].x);
                 if (top == -INFINITY) continue;  // nothing read so far
-                const float s0 = tc::ex2(m[j] - top);
-                l[j] *= s0;
+                const float s0 = rescale(l[j], m[j] - top);
                 o[j].x *= s0;
                 o[j].y *= s0;
                 o[j].z *= s0;
                 o[j].w *= s0;
 #pragma unroll
                 for (int k = 0; k < kParts; ++k) {
-                    const float s1 = tc::ex2(ml[j][k].x - top);  // 0 for a piece that read nothing
-                    l[j] = fmaf(s1, ml[j][k].y, l[j]);
+                    const float s1 = rescale(ml[j][k].y, ml[j][k].x - top);  // 0 for a piece that read nothing
+                    l[j] += ml[j][k].y;
                     o[j].x = fmaf(s1, x[j][k].x, o[j].x);
                     o[j].y = fmaf(s1, x[j][k].y, o[j].y);
                     o[j].z = fmaf(s1, x[j][k].z, o[j].z);
@@ -495,10 +494,10 @@ __device__ __forceinline__ void softmax_group(const SingleArgs &t, Shared &sh, u
                     // rows whose logits are all NaN have no maximum: any offset that is a
                     // number will do, and their sums stay NaN through the join
                     const float by = (top > kCap || !begun) && top > -INFINITY ? top - kTarget : 0.f;
-                    alpha[r] = tc::ex2(-by);
+                    alpha[r] = rescale(l[r], -by);
+                    if (!begun) l[r] = 0.f;
                     moved |= by != 0.f;
                     m[r] += by;
-                    l[r] = begun ? l[r] * alpha[r] : 0.f;
                     x[r] -= by;
                 }
                 if (begun && moved) {
@@ -529,7 +528,7 @@ __device__ __forceinline__ void softmax_group(const SingleArgs &t, Shared &sh, u
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     p[k] = tc::ex2(x[r + k]);
-                    l[r + k] = fmaf(p[k], bs.inv_v, l[r + k]);
+                    l[r + k] += tc::ex2(x[r + k] - bs.lg_v);  // not p / vs: block_scale.cuh
                 }
                 split_p(p[0], p[1], lo);
                 split_p(p[2], p[3], hi);

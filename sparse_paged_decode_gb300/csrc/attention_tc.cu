@@ -415,7 +415,8 @@ __device__ __forceinline__ bool unit_blocks(const Soft &c, const TcArgs &a, cons
                     float al = 1.f, delta = 0.f;
                     if (bu != -INFINITY && (old == -INFINITY || bu > kRaise)) {
                         const float bm = meff + bu;
-                        al = (old == -INFINITY) ? 0.f : tc::ex2(old - bm);
+                        // block-scaled: its root, for the sums' sake (block_scale.cuh)
+                        al = (old == -INFINITY) ? 0.f : tc::ex2(kBs ? 0.5f * (old - bm) : old - bm);
                         any |= old != -INFINITY;
                         m_run[col] = bm;
                         delta = bu;
@@ -434,6 +435,7 @@ __device__ __forceinline__ bool unit_blocks(const Soft &c, const TcArgs &a, cons
             for (int col = 0; col < kNMax; ++col) {
                 if (col < n) {
                     lsum[col] *= sh.alpha[wg][col];
+                    if (kBs) lsum[col] *= sh.alpha[wg][col];
                     u[col] -= sh.delta[wg][col];  // -inf stays -inf
                 }
             }
@@ -448,7 +450,10 @@ __device__ __forceinline__ bool unit_blocks(const Soft &c, const TcArgs &a, cons
                         tc::tmem_ld16(tO + 16 * ch, v);
                         tc::tmem_wait_ld();
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) v[q] *= sh.alpha[wg][16 * ch + q];
+                        for (int q = 0; q < 16; ++q) {
+                            v[q] *= sh.alpha[wg][16 * ch + q];
+                            if (kBs) v[q] *= sh.alpha[wg][16 * ch + q];
+                        }
                         tc::tmem_st16(tO + 16 * ch, v);
                         tc::tmem_wait_st();
                     }
@@ -460,6 +465,11 @@ __device__ __forceinline__ bool unit_blocks(const Soft &c, const TcArgs &a, cons
 
         // this group's P tile was read by the product of its previous block
         if (b >= 2) wait_or_abort(sh, &sh.pv_done[wg], (k - 1) & 1, c.status);
+        if (kBs && have && low_scale(bs)) {
+#pragma unroll
+            for (int col = 0; col < kNMax; ++col)
+                if (col < n) lsum[col] += tc::ex2(u[col] - bs.lg_v);
+        }
         // probabilities p = 2^u <= 2^14 in f16 (11-bit significand, normal
         // from 2^-14 to 65504), the B operand of P V; masked columns have
         // u = -inf, p = 0
@@ -501,6 +511,7 @@ __device__ __forceinline__ bool unit_blocks(const Soft &c, const TcArgs &a, cons
 // its pair is split.  One thread per column first works out the column's two
 // weights and its output row; then group w takes columns [w N/2, (w+1) N/2),
 // each thread its d lane.
+template <bool kBs>
 __device__ __forceinline__ void unit_finish(const Soft &c, const TcArgs &a, const PlanUnit &un, uint32_t gb,
                                             bool ok) {
     Shared &sh = *c.sh;
@@ -532,7 +543,12 @@ __device__ __forceinline__ void unit_finish(const Soft &c, const TcArgs &a, cons
         if (m1 != -INFINITY) w1 = tc::ex2(m1 - m);
         const float l0 = (sh.lsum[0][0][col] + sh.lsum[0][1][col]) + (sh.lsum[0][2][col] + sh.lsum[0][3][col]);
         const float l1 = (sh.lsum[1][0][col] + sh.lsum[1][1][col]) + (sh.lsum[1][2][col] + sh.lsum[1][3][col]);
-        const float l = w0 * l0 + w1 * l1;
+        float l = w0 * l0 + w1 * l1;
+        if (kBs) {
+            float y0 = m0 == -INFINITY ? 0.f : l0, y1 = m1 == -INFINITY ? 0.f : l1;
+            if (m != -INFINITY) rescale(y0, m0 - m), rescale(y1, m1 - m);
+            l = y0 + y1;
+        }
         int64_t off = -1;  // first element of the column's output (or partial) row; -1 for padding
         if (col < rows) {
             if (un.part_row < 0) {
@@ -585,6 +601,7 @@ __device__ __forceinline__ void unit_finish(const Soft &c, const TcArgs &a, cons
 // values, four partials of two rows per round with an online maximum, so a
 // round costs one round trip to L2.  Partials are read with
 // ld.global.cg: other CTAs wrote them during this launch.
+template <bool kBs>
 __device__ __forceinline__ void merge_partials(const Soft &c_, const TcArgs &a_, const PlanUnit &un_) {
     const Soft c = c_;
     const TcArgs a = a_;
@@ -628,16 +645,17 @@ __device__ __forceinline__ void merge_partials(const Soft &c_, const TcArgs &a_,
 #pragma unroll
                 for (int q = 0; q < kParts; ++q) mc = fmaxf(mc, ml[j][q].x);
                 if (mc == -INFINITY) continue;
-                const float sc = (m[j] == -INFINITY) ? 0.f : tc::ex2(m[j] - mc);
-                den[j] *= sc;
+                const float sc = kBs ? rescale(den[j], m[j] - mc) : ((m[j] == -INFINITY) ? 0.f : tc::ex2(m[j] - mc));
+                if (!kBs) den[j] *= sc;
                 acc[j].x *= sc;
                 acc[j].y *= sc;
                 acc[j].z *= sc;
                 acc[j].w *= sc;
 #pragma unroll
                 for (int q = 0; q < kParts; ++q) {
-                    const float w = (ml[j][q].x == -INFINITY) ? 0.f : tc::ex2(ml[j][q].x - mc);
-                    den[j] = fmaf(w, ml[j][q].y, den[j]);
+                    const float w = kBs ? rescale(ml[j][q].y, ml[j][q].x - mc)
+                                        : ((ml[j][q].x == -INFINITY) ? 0.f : tc::ex2(ml[j][q].x - mc));
+                    den[j] = kBs ? den[j] + ml[j][q].y : fmaf(w, ml[j][q].y, den[j]);
                     acc[j].x = fmaf(w, o[j][q].x, acc[j].x);
                     acc[j].y = fmaf(w, o[j][q].y, acc[j].y);
                     acc[j].z = fmaf(w, o[j][q].z, acc[j].z);
@@ -677,6 +695,7 @@ __device__ __forceinline__ void take_ticket(const Soft &c, const PlanUnit &un, P
     }
 }
 
+template <bool kBs>
 __device__ __forceinline__ void resolve_ticket(const Soft &c, const TcArgs &a, PendingMerge &pm) {
     Shared &sh = *c.sh;
     if (pm.un.pair < 0) return;
@@ -685,7 +704,7 @@ __device__ __forceinline__ void resolve_ticket(const Soft &c, const TcArgs &a, P
         if (sh.combine) __threadfence();  // the other units' partials before the merge reads them
     }
     soft_sync();
-    if (sh.combine) merge_partials(c, a, pm.un);
+    if (sh.combine) merge_partials<kBs>(c, a, pm.un);
     soft_sync();
     pm.un.pair = -1;
 }
@@ -1079,7 +1098,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
             }
             soft_sync();
             const bool ok = unit_blocks<kBs>(c, a, un, gb);
-            unit_finish(c, a, un, gb, ok);
+            unit_finish<kBs>(c, a, un, gb, ok);
             tc::mbar_arrive(&sh.meta_empty[c.mb]);
             gb += un.count;
             // the next unit's record (published before this unit's loads)
@@ -1089,9 +1108,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                 nx = sh.ring[(uc + 1) & 3];
             state = vote(((aborted(sh) || !ok) ? 1 : 0) | (nx.pair < 0 ? 2 : 0));
             if (!(state & 1)) {
-                resolve_ticket(c, a, pending);
+                resolve_ticket<kBs>(c, a, pending);
                 if (un.part_row >= 0) take_ticket(c, un, pending);
-                if (state & 2) resolve_ticket(c, a, pending);
+                if (state & 2) resolve_ticket<kBs>(c, a, pending);
             }
             tc::mbar_arrive(&sh.unit_empty[uc & 3]);
             un = nx;

@@ -11,6 +11,15 @@
 // without scales.  (A scale in the widened f16 values instead would leave the
 // range of f16 for scales 2^8 apart.)
 //
+// The sum has a wider range than the weights.  A page's scale may be 2^-128 of
+// another's, and ex2 gives 0 below 2^-126, so w may be lost where its key's softmax
+// weight is not.  Pages of scales below 2^kLowScale therefore add 2^(z - m) itself, an
+// exponential more a key (the kernel of single rows, which HBM bounds, adds it for
+// every page); any other page lies within 2^96 of all, and a w that is 0 there belongs
+// to a key of less than 2^-30 of the softmax weight of the key that the offset comes
+// from.  z - m is at most 64 and the raise's headroom, and the sum at least 2^-64, so
+// it is brought to a new offset in two steps (`rescale`).
+//
 // The loading thread copies a page's two scales beside its keys, with cp.async
 // and an arrival on the same barrier: a ring of kScaleRing pages, which no
 // loader runs ahead of (each kernel says why).
@@ -21,9 +30,21 @@
 
 namespace spd {
 
+constexpr float kLowScale = -32.f;  // log2
+
 struct BlockScale {
-    float k, lg_v, inv_v;  // the K scale, log2 of the V scale, its reciprocal
+    float k, lg_v, inv_v;  // the K scale, log2 of the V scale, its reciprocal: 0 for a low one
 };
+
+// The sum adds its keys' 2^(z - m) for this page, not w / vs.
+__device__ __forceinline__ bool low_scale(const BlockScale &s) { return s.inv_v == 0.f; }
+
+// A sum times 2^by, by <= 0 of any size (-inf: 0).  Returns 2^by.
+__device__ __forceinline__ float rescale(float &l, float by) {
+    const float root = tc::ex2(0.5f * by);
+    l = l * root * root;
+    return root * root;
+}
 
 __device__ __forceinline__ BlockScale block_scale(float2 kv) {
     BlockScale s;
@@ -35,7 +56,7 @@ __device__ __forceinline__ BlockScale block_scale(float2 kv) {
              __log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
     // of the very factor that the exponent carries, and one instruction where a
     // division takes ten, for every thread and page (prefill dense 518 -> 507 us)
-    s.inv_v = tc::ex2(-s.lg_v);
+    s.inv_v = s.lg_v < kLowScale ? 0.f : tc::ex2(-s.lg_v);
     return s;
 }
 

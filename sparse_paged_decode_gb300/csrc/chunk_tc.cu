@@ -75,6 +75,7 @@
 // 0 and 1 (warp 13 owns tensor memory), warp 14 claims units and builds their
 // page lists one unit ahead.  Every wait is bounded: one that gives up sets bit
 // 0 of the workspace status word and the CTA winds down.
+#include <limits.h>
 #include <math.h>
 
 #include <cuda_bf16.h>
@@ -515,6 +516,22 @@ __device__ __noinline__ void take_marked(const TcArgs &t, const UnitRec &u, int 
     }
 }
 
+// What half a page of a low V scale (block_scale.cuh) adds to a row's sum: 2^(z + off)
+// of its first `left` keys.  Rare, so short and out of line: over the logits in
+// registers, unrolled, it cost every page 2 % in instructions to fetch.
+__device__ __noinline__ float low_page_sum(uint32_t col, int left, float c, float off) {
+    float l = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < kHalf; i0 += 8) {
+        float z[8];
+        tc::tmem_ld8(col + i0, z);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l += i0 + i < left ? tc::ex2(fmaf(z[i], c, off)) : 0.f;
+    }
+    return l;
+}
+
 // kBs: block-scaled caches (block_scale.cuh); E4M3 modes only.
 template <int D, Mode M, bool kBs>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -628,6 +645,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             // is in log2 units then, m2 without the V scale
             float cb = c;
             BlockScale bs = {1.f, 0.f, 1.f};
+            int look = kHalf;             // rows with fewer keys left are looked at more closely: all of a low page's
             bool seen = false, ok = true;
             int word_at = -1;
             uint32_t word = 0;
@@ -659,6 +677,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     tc::tc_fence_after();
                     if (kBs && h == 0) {
                         bs = block_scale(sh.scale[(page0 + j) % kScaleRing]);
+                        look = low_scale(bs) ? INT_MAX : kHalf;
                         cb = fmaxf(c * bs.k, 1e-37f);  // above 0: masked logits are -inf
                         c2 = pair(cb, cb);
                     }
@@ -681,7 +700,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     } else {
                         float mx = fmaxf(top[0], top[1]);
                         if (kBs) mx = fmaf(mx, cb, bs.lg_v);
-                        if (__any_sync(0xffffffffu, left < kHalf || mx > threshold)) {
+                        if (__any_sync(0xffffffffu, left < look || mx > threshold)) {
                             if (left < kHalf) {
                                 mx = -INFINITY;
 #pragma unroll
@@ -697,9 +716,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                             float alpha = 1.f;
                             if (raise) {
                                 const float bm = kBs ? mx - kLift : fmaf(mx, c, -kLift);
-                                alpha = tc::ex2(m_run - bm);  // 0 for a row that had none
+                                alpha = kBs ? rescale(l, m_run - bm) : tc::ex2(m_run - bm);  // 0 for a row that had none
+                                if (!kBs) l *= alpha;
                                 m_run = bm;
-                                l *= alpha;
                                 // lower by what the rounding of large offsets
                                 // may add, so that p stays below 2^(kLift + kRaise)
                                 const float most = fmaf(fabsf(m_run), -0x1p-22f, m_run + (kLift + kRaise));
@@ -721,6 +740,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                                     tc::tmem_st16(col_o + ch * 16, o);
                                 }
                             }
+                            if (kBs && __builtin_expect(low_scale(bs), 0))
+                                l += low_page_sum(col_s + h * kHalf, left, cb, m_run == -INFINITY ? 0.f : -m_run);
                         }
                         const uint64_t off2 = kBs ? add2(m2, pair(bs.lg_v, bs.lg_v)) : m2;
 #pragma unroll
@@ -781,9 +802,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 const float2 other = sh.dual_stats[r];
                 const float m = fmaxf(m_run, other.x);
                 if (m != -INFINITY) {
-                    w_own = tc::ex2(m_run - m);
-                    w_other = tc::ex2(other.x - m);
-                    l = l * w_own + other.y * w_other;  // a NaN stays one, whatever its weight
+                    float l_other = other.y;  // a NaN stays one, whatever its weight
+                    w_own = kBs ? rescale(l, m_run - m) : tc::ex2(m_run - m);
+                    w_other = kBs ? rescale(l_other, other.x - m) : tc::ex2(other.x - m);
+                    l = kBs ? l + l_other : l * w_own + l_other * w_other;
                     m_run = m;
                 } else {
                     l += other.y;
@@ -1474,7 +1496,13 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
         for (int p = lane % kJoinLanes; p < pr.pieces; p += kJoinLanes)
             if (mine) {
                 const float2 s = stats[p * 256 + own];
-                L += M == -INFINITY ? s.y : s.y * tc::ex2(s.x - M);  // a NaN stays one, whatever its weight
+                // a NaN stays one, whatever its weight
+                float y = s.y;
+                if (M != -INFINITY) {
+                    if (a.sc.k != nullptr) rescale(y, s.x - M);
+                    else y *= tc::ex2(s.x - M);
+                }
+                L += y;
             }
 #pragma unroll
         for (int d = kJoinLanes / 2; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);

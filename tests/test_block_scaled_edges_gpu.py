@@ -3,8 +3,8 @@ definitions and tolerances of block_scaled_ref.py."""
 import pytest
 import torch
 
-from test_block_scaled_gpu import (BF16, BS, DEV, E4M3, F16, attention_inputs, check_decode, run_decode, shared_selection,
-                                   spd)  # noqa: F401 (fixture)
+from test_block_scaled_gpu import (BF16, BS, DEV, E4M3, F16, attention_inputs, check_decode, check_prefill, run_decode,
+                                   shared_selection, spd)  # noqa: F401 (fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +36,66 @@ def test_pieces_of_one_page_repeat_themselves(spd, K, heads, dt):  # noqa: F811
         f(*ins, out, s["sm"], BS, ws)
         differ += (out.view(torch.int16) != first.view(torch.int16)).sum()
     assert int(differ) == 0
+
+
+# ------------------------------------------------ V scales far apart in a row
+#
+# Both ends of the range, 2^-64 and 2^64, in one row.  The keys of the low pages
+# add next to nothing to the row's products and most of its softmax sum: without
+# them the output would be up to (low + high pages) / (high pages) times as large,
+# where the bound allows it to be off by 2^-7.
+
+ORDERS = {"low first": lambda j, n: j < n - 2, "high first": lambda j, n: j >= 2, "one low": lambda j, n: j == n // 2,
+          "one high": lambda j, n: j != n // 2, "in turn": lambda j, n: j % 2 == 0}
+
+
+def far_apart(lengths, new, Hq, Hkv, D, dt, seed, order, level, low=-64, high=64, **kw):
+    """Requests whose pages have V scales of 2^low or 2^high; the logits of the low
+    pages lie level / sqrt(D) above the others'."""
+    s = attention_inputs(lengths, new, Hq, Hkv, D, dt, seed, **kw)
+    s["q"][:, :, 0] = 1.0
+    kc, t = s["kc"].view(torch.uint8).view(-1, BS, Hkv, D), s["table"][s["rows"].long()].long()
+    code = int(torch.tensor(float(level)).to(E4M3).view(torch.uint8))
+    for b, L in enumerate(lengths):
+        n = -(-L // BS)
+        for j in range(n):
+            is_low = ORDERS[order](j, n)
+            s["vs"][t[b, j]] = 2.0 ** (low if is_low else high)
+            s["ks"][t[b, j]] = 1.0
+            kc[t[b, j], :L - j * BS, :, 0] = code if is_low else 0
+    return s
+
+
+@pytest.mark.parametrize("level", [-32, 0, 96])
+@pytest.mark.parametrize("order", list(ORDERS))
+@pytest.mark.parametrize("heads", [(16, 2), (32, 2), (9, 3)])
+def test_decode_v_scales_at_both_ends(spd, heads, order, level):  # noqa: F811
+    for K in (0, 9):
+        s = far_apart([2300, 130, 1000, 2000], [1, 2, 16, 1], *heads, 128, BF16, 83, order, level, K=K)
+        check_decode(spd, s, (None, 1, 2, 3, 4), "%s, K=%d" % (order, K))
+
+
+@pytest.mark.parametrize("dt", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("order", list(ORDERS))
+def test_decode_v_scales_at_both_ends_of_single_rows(spd, order, dt):  # noqa: F811
+    s = far_apart([6000, 257, 3001], [1, 1, 1], 8, 2, 128, dt, 84, order, 0)  # rows in many pieces
+    check_decode(spd, s, (None, 2, 3, 4), order)
+
+
+@pytest.mark.parametrize("level", [-32, 0, 96])
+@pytest.mark.parametrize("order", list(ORDERS))
+@pytest.mark.parametrize("kind", [(128, BF16), (128, F16), (64, BF16)], ids=["terms", "f16", "wide64"])
+def test_prefill_v_scales_at_both_ends(spd, kind, order, level):  # noqa: F811
+    D, dt = kind
+    for K in (0, 9):
+        s = far_apart([2300, 130, 1000, 3000], [3, 2, 150, 20], 16, 2, D, dt, 85, order, level, K=K, bq=16)
+        check_prefill(spd, s, (None, 1), "%s, K=%d" % (order, K))
+
+
+@pytest.mark.parametrize("apart", [(-33, 64), (-32, 64), (-31, 64), (-64, 40), (-64, 63)])
+def test_v_scales_around_the_low_ones(spd, apart):  # noqa: F811
+    """Either side of 2^-32, below which a page adds its weights apart from its products."""
+    for order in ("low first", "one high"):
+        s = far_apart([2300, 130], [1, 16], 16, 2, 128, BF16, 86, order, 32, *apart)
+        check_decode(spd, s, (None, 2, 3, 4), "decode, " + order)
+        check_prefill(spd, s, (None,), "prefill, " + order)
