@@ -103,12 +103,12 @@ cudaError_t dispatch_attention(const AttnArgs &a, void *workspace, size_t worksp
     if (pol == 0 && a.kv_dt == SPD_BF16) {
         e = launch_attention_bf16_tc(a, workspace, workspace_bytes, stream, &used);
     } else if (a.kv_dt == SPD_E4M3 && (pol == 0 || pol == 2 || pol == 3 || pol == 4)) {
-        const int64_t G = a.Hkv > 0 ? a.Hq / a.Hkv : 0;
+        const int64_t G = a.Hq / a.Hkv;
         const bool wide = static_cast<int64_t>(a.T) * G >= 48LL * a.R;
         // block-scaled caches: rows that have their blocks to themselves (single
         // tokens, or selections with little in common) take the kernel of
         // single rows
-        const bool alone = a.T <= a.R || (a.tk != nullptr && group_rows(a, static_cast<int>(G)) == 1);
+        const bool alone = a.sc.k != nullptr && (a.T <= a.R || (a.tk != nullptr && group_rows(a, static_cast<int>(G)) == 1));
         if (pol == 4 || (pol == 0 && !wide && alone)) {
             e = launch_attention_single(a, workspace, workspace_bytes, stream, &used);
             if (e == cudaSuccess && used) {

@@ -307,7 +307,7 @@ bool attention(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v, co
         const uintptr_t wlo = reinterpret_cast<uintptr_t>(ws), whi = wlo + ws_bytes;
         if (numel(out) > 0 && olo < whi && wlo < ohi) return fail(SPD_ERR_ALIASING, "out overlaps the workspace");
     }
-    if (T == 0) return true;
+    if (T == 0 || Hq == 0) return true;  // no cell to write (and no group of heads: Hq / Hkv divides below)
 
     AttnArgs a{};
     a.q = q->data; a.q_s0 = q->stride[0]; a.q_s1 = q->stride[1]; a.q_s2 = q->stride[2];
