@@ -100,29 +100,34 @@ cudaError_t dispatch_attention(const AttnArgs &a, void *workspace, size_t worksp
     // grow with the group's width up to 128 rows, the second one's does, and
     // it is the faster of the two for narrow groups.
     const int pol = g_policy[3];
+    int launches = 3;  // list and unit planner kernels + attention
+    auto single = [&] {
+        e = launch_attention_single(a, workspace, workspace_bytes, stream, &used);
+        if (used) launches = 2;  // the line of blocks + attention
+    };
     if (pol == 0 && a.kv_dt == SPD_BF16) {
         e = launch_attention_bf16_tc(a, workspace, workspace_bytes, stream, &used);
     } else if (a.kv_dt == SPD_E4M3 && (pol == 0 || pol == 2 || pol == 3 || pol == 4)) {
         const int64_t G = a.Hq / a.Hkv;
+        const bool block = a.sc.k != nullptr;
         const bool wide = static_cast<int64_t>(a.T) * G >= 48LL * a.R;
         // block-scaled caches: rows that have their blocks to themselves (single
         // tokens, or selections with little in common) take the kernel of
         // single rows
-        const bool alone = a.sc.k != nullptr && (a.T <= a.R || (a.tk != nullptr && group_rows(a, static_cast<int>(G)) == 1));
-        if (pol == 4 || (pol == 0 && !wide && alone)) {
-            e = launch_attention_single(a, workspace, workspace_bytes, stream, &used);
-            if (e == cudaSuccess && used) {
-                count_launches(2);  // the line of blocks + attention
-                return cudaSuccess;
-            }
-            if (e != cudaSuccess) return e;
-        }
-        if (pol == 3 || (pol == 0 && wide)) e = launch_attention_e4m3_rows(a, workspace, workspace_bytes, stream, &used);
-        if (e == cudaSuccess && !used && pol != 3 && pol != 4) e = launch_attention_tc(a, workspace, workspace_bytes, stream, &used);
+        const bool alone = block && (a.T <= a.R || (a.tk != nullptr && group_rows(a, static_cast<int>(G)) == 1));
+        const bool first = pol == 4 || (pol == 0 && !wide && alone);
+        if (first) single();
+        if (e == cudaSuccess && !used && (pol == 3 || (pol == 0 && wide)))
+            e = launch_attention_e4m3_rows(a, workspace, workspace_bytes, stream, &used);
+        if (e == cudaSuccess && !used && pol != 3 && pol != 4)
+            e = launch_attention_tc(a, workspace, workspace_bytes, stream, &used);
+        // the two above end at page tables of kPlanMaxNB blocks, this one does not (300
+        // blocks, 8 requests of 4 rows, every page: 181 us, the general kernel 14.1 ms)
+        if (e == cudaSuccess && !used && pol == 0 && block && !first) single();
     }
     if (e != cudaSuccess) return e;
     if (used) {
-        count_launches(3);  // list and unit planner kernels + attention
+        count_launches(launches);
         return cudaSuccess;
     }
     count_launches(1);

@@ -99,3 +99,21 @@ def test_v_scales_around_the_low_ones(spd, apart):  # noqa: F811
         s = far_apart([2300, 130], [1, 16], 16, 2, 128, BF16, 86, order, 32, *apart)
         check_decode(spd, s, (None, 2, 3, 4), "decode, " + order)
         check_prefill(spd, s, (None,), "prefill, " + order)
+
+
+# ------------------------------------------------------- long page tables
+
+
+@pytest.mark.parametrize("dt", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("K", [0, 5])
+@pytest.mark.parametrize("new", [(1, 1), (3, 2), (16, 16)], ids=["single", "drafts", "wide"])
+def test_decode_over_long_page_tables_by_default(spd, new, K, dt):  # noqa: F811
+    """More than 256 blocks, whatever the rows of a request: a tensor-core kernel (two
+    launches), not the general one."""
+    s = attention_inputs([700, 1290], list(new), 16, 2, 128, dt, 87, NB=300)
+    if K:
+        shared_selection(s, K, 88, "whole")
+    before = spd.launch_count()
+    run_decode(spd, s)
+    assert spd.launch_count() - before == 2
+    check_decode(spd, s, (None,), "long table")
