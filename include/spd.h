@@ -646,9 +646,13 @@ SPD_API int spd_set_attention_kernel(int policy);
  * 128, G <= 16 and on average at least 48 query rows per request and kv
  * head, the keys-on-lanes one otherwise; a shape the picked kernel does not
  * cover runs on the general-layout kernel).  Over block-scaled caches policy 4
- * picks the kernel of single rows (the default takes it ahead of the
- * keys-on-lanes one where there are no more query rows than page-table rows, or
- * selections with little in common, and an even number of kv heads shares them).  All give identical selections, and
+ * picks the kernel of single rows.  The default takes it ahead of the
+ * keys-on-lanes one where an even number of kv heads shares the blocks and there
+ * are no more query rows than page-table rows, or selections with little in
+ * common; and for page tables of more than 256 blocks.  It reads a page once for
+ * each row: for batches of several rows a request, pass a block_table that has no
+ * more rows than there are requests, or pick policy 3 (up to three times faster
+ * there).  All give identical selections, and
  * attention results that agree within the stated tolerance.  Returns the
  * previous setting, or -1 for an unknown stage.
  */

@@ -113,7 +113,13 @@ cudaError_t dispatch_attention(const AttnArgs &a, void *workspace, size_t worksp
         const bool wide = static_cast<int64_t>(a.T) * G >= 48LL * a.R;
         // block-scaled caches: rows that have their blocks to themselves (single
         // tokens, or selections with little in common) take the kernel of
-        // single rows
+        // single rows.  How many requests the rows belong to stands in device
+        // memory, so no more rows than the page table has are taken for single
+        // tokens: 64 of them over up to 8192 keys take 93 us (keys on lanes: 153).
+        // Draft rows over a table with spare rows pay for that, every page being
+        // read once a row: 64 requests of 4 rows 340 us (query rows 165, keys on
+        // lanes 208), of 1 to 16 rows 617 (211, 352), over 64 selected blocks
+        // 941 (504, 579).
         const bool alone = block && (a.T <= a.R || (a.tk != nullptr && group_rows(a, static_cast<int>(G)) == 1));
         const bool first = pol == 4 || (pol == 0 && !wide && alone);
         if (first) single();
