@@ -416,7 +416,8 @@ SPD_API void paged_assign_slots(const spd_tensor *new_lens, const spd_tensor *pr
  * q_out      OUT [T, Hq, D] f32 | bf16 | f16
  * k_cache, v_cache IN/OUT [P*block_size, Hkv, D] f32 | bf16 | f16 | e4m3, one
  *            dtype for both; only the named slots are written; v_cache NULL
- *            exactly when v is
+ *            exactly when v is.  They may be the parts of one allocation, beside
+ *            each other by slots or by heads, with equal strides
  * eps        finite and >= 0; k_scale, v_scale finite and > 0 with a finite
  *            reciprocal (1.0 for a cache stored unscaled)
  * block_size must be 128
@@ -532,7 +533,8 @@ SPD_API void paged_sparse_prefill_attention(const spd_tensor *q, const spd_tenso
  * same inputs changes nothing.
  *
  * k_cache, v_cache IN/OUT [P*block_size, Hkv, D] e4m3
- * k_scales, v_scales IN/OUT [P, Hkv] f32: only the named pages' entries are written
+ * k_scales, v_scales IN/OUT [P, Hkv] f32: only the named pages' entries are written;
+ *            they may be the parts of one allocation as the caches may
  * the other arguments as in paged_norm_rope_store
  */
 SPD_API void paged_norm_rope_store_block_scaled(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v,

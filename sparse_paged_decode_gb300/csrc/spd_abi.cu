@@ -489,21 +489,48 @@ bool assign_slots(const spd_tensor *nw, const spd_tensor *pre, const spd_tensor 
 
 // ------------------------------------- norm, rotary positions, cache store
 
-// Two caches whose byte spans overlap are still disjoint when they interleave
-// slot by slot: equal strides, and an offset that keeps one cache's rows
-// inside the gaps between the other's.
-bool caches_interleave(const spd_tensor *k, const spd_tensor *v) {
-    for (int i = 0; i < 3; ++i)
-        if (k->shape[i] > 1 && k->stride[i] != v->stride[i]) return false;
-    const int es = elem_size(k->dtype);
-    int64_t delta = static_cast<int64_t>(reinterpret_cast<intptr_t>(v->data) - reinterpret_cast<intptr_t>(k->data));
-    if (delta % es != 0 || k->stride[0] <= 0) return false;
-    const int64_t s0 = k->stride[0];
-    int64_t row = 1;  // elements spanned by one slot
-    for (int i = 1; i < 3; ++i)
-        if (k->shape[i] > 1) row += k->stride[i] * (k->shape[i] - 1);
-    const int64_t off = ((delta / es) % s0 + s0) % s0;
-    return off >= row && off <= s0 - row;
+struct Dim {
+    int64_t extent, stride;
+};
+
+// Whether `apart` is a distance between two cells of n dims of these extents and
+// strides, the strides descending and nested: of each only two multiples can be part
+// of it.
+bool is_distance(const Dim *dims, int n, int64_t apart) {
+    if (n == 0) return apart == 0;
+    const Dim d = dims[0];
+    const int64_t low = apart / d.stride - (apart % d.stride < 0 ? 1 : 0);
+    for (int64_t k = low; k <= low + 1; ++k)
+        if (k > -d.extent && k < d.extent && is_distance(dims + 1, n - 1, apart - k * d.stride)) return true;
+    return false;
+}
+
+// Whether two outputs of one shape and legal layout whose byte spans overlap are
+// still disjoint: with equal strides, as K and V beside each other in one allocation.
+bool side_by_side(const spd_tensor *a, const spd_tensor *b) {
+    Dim dims[4];
+    int n = 0;
+    for (int i = 0; i < a->ndim; ++i) {
+        if (a->shape[i] <= 1) continue;
+        if (a->stride[i] != b->stride[i]) return false;
+        dims[n++] = {a->shape[i], a->stride[i]};
+    }
+    std::sort(dims, dims + n, [](const Dim &x, const Dim &y) { return x.stride > y.stride; });
+    const int es = elem_size(a->dtype);
+    const int64_t bytes = static_cast<int64_t>(reinterpret_cast<intptr_t>(b->data) - reinterpret_cast<intptr_t>(a->data));
+    return bytes % es == 0 && !is_distance(dims, n, bytes / es);
+}
+
+// K's and V's part of an output, each with a legal layout and apart from `ins` and
+// from one another.
+bool check_output_pair(const Output &k, const Output &v, std::initializer_list<const spd_tensor *> ins) {
+    if (!check_outputs({k}, ins) || !check_outputs({v}, ins)) return false;
+    if (numel(k.t) == 0 || numel(v.t) == 0) return true;
+    uintptr_t alo, ahi, blo, bhi;
+    byte_span(k.t, &alo, &ahi);
+    byte_span(v.t, &blo, &bhi);
+    if (alo < bhi && blo < ahi && !side_by_side(k.t, v.t)) return fail(SPD_ERR_ALIASING, "%s overlaps %s", k.name, v.name);
+    return true;
 }
 
 bool norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_tensor *v, const spd_tensor *wq,
@@ -562,16 +589,11 @@ bool norm_rope_store(const spd_tensor *q, const spd_tensor *k, const spd_tensor 
                      !check_scales(vs, "v_scales", kc->shape[0] / kBlock, Hkv)))
         return false;
     if (!check_outputs({{qo, "q_out"}, {kc, "k_cache"}}, {q, k, v, wq, wk, cs, tl, slots})) return false;
-    if (vc != nullptr && numel(vc) > 0) {
-        if (!check_output_layout(vc, "v_cache") || !check_no_overlap(vc, "v_cache", {q, k, v, wq, wk, cs, tl, slots, qo}))
-            return false;
-        uintptr_t alo, ahi, blo, bhi;
-        byte_span(kc, &alo, &ahi);
-        byte_span(vc, &blo, &bhi);
-        if (alo < bhi && blo < ahi && !caches_interleave(kc, vc))
-            return fail(SPD_ERR_ALIASING, "k_cache overlaps v_cache");
-    }
-    if (sc.block && !check_outputs({{ks, "k_scales"}, {vs, "v_scales"}}, {q, k, v, wq, wk, cs, tl, slots, qo, kc, vc}))
+    if (vc != nullptr &&
+        !check_output_pair({kc, "k_cache"}, {vc, "v_cache"}, {q, k, v, wq, wk, cs, tl, slots, qo}))
+        return false;
+    if (sc.block &&
+        !check_output_pair({ks, "k_scales"}, {vs, "v_scales"}, {q, k, v, wq, wk, cs, tl, slots, qo, kc, vc}))
         return false;
     if (T == 0) return true;
 

@@ -3,8 +3,8 @@ definitions and tolerances of block_scaled_ref.py."""
 import pytest
 import torch
 
-from test_block_scaled_gpu import (BF16, BS, DEV, E4M3, F16, attention_inputs, check_decode, check_prefill, run_decode,
-                                   shared_selection, spd)  # noqa: F401 (fixture)
+from test_block_scaled_gpu import (BF16, BS, DEV, E4M3, F16, attention_inputs, check_decode, check_prefill, check_store,
+                                   run_decode, shared_selection, spd, store_inputs)  # noqa: F401 (fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,25 @@ def test_decode_over_long_page_tables_by_default(spd, new, K, dt):  # noqa: F811
     run_decode(spd, s)
     assert spd.launch_count() - before == 2
     check_decode(spd, s, (None,), "long table")
+
+
+# ------------------------------------------- K and V parts of one allocation
+
+
+@pytest.mark.parametrize("cache", ["slots", "heads"])
+@pytest.mark.parametrize("scale", ["rows", "pairs"])
+@pytest.mark.parametrize("dt", [BF16, torch.float32], ids=["vector", "general"])
+def test_store_and_attention_over_parts_of_one_allocation(spd, dt, scale, cache):  # noqa: F811
+    """Scales [P, 2, Hkv] or [P, Hkv, 2], caches [slots, 2, Hkv, D] or [slots, Hkv, 2, D]: K and V as views."""
+    s = store_inputs([(60, 100), (0, 30), (126, 9)], 8, 2, 128, 128, dt, 89)
+    at = {"slots": 1, "heads": 2}[cache]
+    both = torch.stack((s["kc"].view(torch.uint8), s["vc"].view(torch.uint8)), at).view(E4M3)
+    s["kc"], s["vc"] = both.select(at, 0), both.select(at, 1)
+    both = torch.stack((s["ks"], s["vs"]), {"rows": 1, "pairs": 2}[scale])
+    s["ks"], s["vs"] = both.select({"rows": 1, "pairs": 2}[scale], 0), both.select({"rows": 1, "pairs": 2}[scale], 1)
+    check_store(spd, s, "%s, %s" % (scale, cache))
+    s["ks"].fill_(2.0 ** -5)  # logits of a few units
+    a = attention_inputs([300, 70], [3, 2], 8, 2, 128, BF16, 90)
+    a.update({x: s[x] for x in ("kc", "vc", "ks", "vs")}, table=a["table"].clamp(0, s["ks"].shape[0] - 1))
+    check_decode(spd, a, (None, 1), "decode")
+    check_prefill(spd, a, (None, 1), "prefill")
