@@ -51,7 +51,9 @@ __device__ __forceinline__ BlockScale block_scale(float2 kv) {
     const float v = clip_scale(kv.y);
     const uint32_t bits = __float_as_uint(v);
     s.k = clip_scale(kv.x);
-    // exponent and significand apart: exact for powers of two, 2^-22 off at most
+    // exponent and significand apart: exact for powers of two.  Else off by the
+    // logarithm's 2^-22 and the rounding of the sum, up to 2^-19 for scales from 2^32
+    // on (or below 2^-32), which a weight takes over as 0.7 times that of itself
     s.lg_v = static_cast<float>(static_cast<int>(bits >> 23) - 127) +
              __log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
     // of the very factor that the exponent carries, and one instruction where a

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from test_block_scaled_gpu import (BF16, BS, DEV, E4M3, F16, attention_inputs, check_decode, check_prefill, check_store,
-                                   run_decode, shared_selection, spd, store_inputs)  # noqa: F401 (fixture)
+                                   run_decode, run_prefill, run_store, shared_selection, spd, store_inputs)  # noqa: F401 (fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +139,32 @@ def test_store_and_attention_over_parts_of_one_allocation(spd, dt, scale, cache)
     a.update({x: s[x] for x in ("kc", "vc", "ks", "vs")}, table=a["table"].clamp(0, s["ks"].shape[0] - 1))
     check_decode(spd, a, (None, 1), "decode")
     check_prefill(spd, a, (None, 1), "prefill")
+
+
+# ----------------------------------------------------------------- repeats
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("K", [0, 7])
+def test_attention_repeats_itself(spd, K, which):  # noqa: F811
+    """Which CTA takes a unit and which joins a row's pieces changes from call to call; no bit of the output does."""
+    new = [1, 4, 16, 1, 8, 2] if which == "decode" else [100, 4, 333, 1, 64, 2]
+    s = attention_inputs([4000, 1300, 2500, 700, 3100, 129], new, 64, 8, 128, BF16, 91, K=K, bq=16 if which == "prefill" else 1, wild=6)
+    if K and which == "decode":
+        shared_selection(s, K, 92)
+    run = run_decode if which == "decode" else run_prefill
+    for pol in (None, 2, 3, 4) if which == "decode" else (None,):
+        first = run(spd, s, pol).view(torch.int16)
+        for _ in range(25):
+            assert torch.equal(run(spd, s, pol).view(torch.int16), first), pol
+
+
+def test_store_repeats_itself(spd):  # noqa: F811
+    def once():
+        s = store_inputs([(p, 2 + p % 150) for p in range(0, 1270, 29)], 8, 4, 128, 128, BF16, 93, pad=5)
+        out = run_store(spd, s)
+        return [x.view(torch.uint8) for x in (out, s["kc"], s["vc"], s["ks"], s["vs"])]
+
+    first = once()
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(once(), first))
