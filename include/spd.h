@@ -184,7 +184,10 @@ SPD_API void msa_select_topk(const spd_tensor *scores, const spd_tensor *topk_id
  *            concurrently
  * Domain: D in [1, 256], Hq / Hkv <= 16, NB in [1, 1024], K >= 1.
  * Query rows of one request that sit next to each other (the draft tokens
- * of a verification row) share each K/V page read.
+ * of a verification row) share each K/V page read.  Values that are not finite
+ * (a NaN; in a BF16 cache an infinity too) may show in their dim of all the rows
+ * that share the read, also of those that do not read the token: their weight of 0
+ * is multiplied by it on the tensor cores.
  */
 SPD_API void paged_sparse_decode_attention(const spd_tensor *q, const spd_tensor *k_cache,
                                    const spd_tensor *v_cache, const spd_tensor *block_table,
@@ -555,7 +558,9 @@ SPD_API void paged_norm_rope_store_block_scaled(const spd_tensor *q, const spd_t
  * scales will do, not only powers of two.  Scales of pages that a row does not
  * read never reach its output.  A NaN value that a row reads shows in its dims; a
  * NaN key, or a query that is not finite, makes the head's output NaN (from the
- * decode kernels of wider groups and the general one: NaN or zeros).
+ * decode kernels of wider groups and the general one: NaN or zeros).  From the decode
+ * kernels of wider groups a NaN value shows in its dim of every query row of the
+ * request that shares the page's read, as in the calls without the suffix.
  *
  * k_cache, v_cache [P*128, Hkv, D] e4m3; k_scales, v_scales [P, Hkv] f32, any
  * strides; workspaces, the other arguments and the domain as for the calls without
