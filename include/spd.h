@@ -555,7 +555,9 @@ SPD_API void paged_norm_rope_store_block_scaled(const spd_tensor *q, const spd_t
  *   out[t][g] = sum_tau softmax(z)_tau * vs * v_cache[slot(tau)][h]
  * where ks and vs are the scales of tau's page and of kv head h, each taken as
  * the nearest value of [2^-64, 2^64] (the smallest for a NaN): any positive
- * scales will do, not only powers of two.  Scales of pages that a row does not
+ * scales will do, not only powers of two, while the logits stay below 2^22 in
+ * magnitude (beyond, fp32 cannot tell weights apart, and the tensor-core kernels may
+ * give NaN).  Scales of pages that a row does not
  * read never reach its output.  A NaN value that a row reads shows in its dims; a
  * NaN key, or a query that is not finite, makes the head's output NaN (from the
  * decode kernels of wider groups and the general one: NaN or zeros).  From the decode

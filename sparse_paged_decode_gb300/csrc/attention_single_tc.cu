@@ -34,10 +34,10 @@
 //    page's V scale: block_scale.cuh) are raised when a logit runs more than 2^8
 //    above, to 2^2 below the block's maximum.
 //
-// Measured (64 / 8 heads, graph of calls): 16 rows over 16384 keys 86.7 us, 6.2 TB/s
-// or 0.92 of the measured copy rate, where the keys-on-lanes kernel (one head a
+// Measured (64 / 8 heads, graph of calls): 16 rows over 16384 keys 86.9 us, 6.2 TB/s
+// or 0.91 of the measured copy rate, where the keys-on-lanes kernel (one head a
 // unit, V widened, two planner kernels) took 137; 16 rows over 16 selected blocks
-// each 22.7 us (34.5); one row over 2048 keys 12.5 us (22.2).  Rows that share
+// each 22.7 us (34.5); one row over 2048 keys 12.8 us (22.2).  Rows that share
 // their blocks read them once each here: 452 rows of 64 requests over 64 of up to
 // 128 blocks take 460 us, the query-rows kernel 264.
 //
